@@ -94,8 +94,32 @@ def build_block_lib(force=False, verbose=False):
     return BLOCK_LIB
 
 
+# Causal attention over packed sequences: its own library.
+PACKED_LIB = os.path.join(HERE, "libpacked_attn.so")
+PACKED_SOURCES = [os.path.join(HERE, "csrc", f) for f in ("pa_api.cu", "pa_layout.cpp")]
+PACKED_HEADERS = [os.path.join(ROOT, "include", f) for f in ("packed_attn.h", "sparse_attn.h")] + [
+    os.path.join(HERE, "csrc", f) for f in ("pa_internal.h", "pa_simple.cuh", "sa_device.cuh", "sa_internal.h")]
+
+
+def build_packed_lib(force=False, verbose=False, extra=()):
+    """Compile libpacked_attn.so if out of date; return its path."""
+    if not force and os.path.exists(PACKED_LIB):
+        t = os.path.getmtime(PACKED_LIB)
+        if all(os.path.getmtime(p) <= t for p in PACKED_SOURCES + PACKED_HEADERS):
+            return PACKED_LIB
+    cmd = [nvcc_path(), "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
+           "-Xcompiler", "-fPIC,-O3", "-shared", "-cudart", "static", "-Xlinker", "-soname=libpacked_attn.so",
+           "-I", os.path.join(ROOT, "include"), "-o", PACKED_LIB, *extra, *PACKED_SOURCES]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    return PACKED_LIB
+
+
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True,
           extra=["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else [])
     build_test_lib(force="--force" in sys.argv, verbose=True)
     build_block_lib(force="--force" in sys.argv, verbose=True)
+    build_packed_lib(force="--force" in sys.argv, verbose=True,
+                     extra=["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else [])

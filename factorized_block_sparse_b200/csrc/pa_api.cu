@@ -1,0 +1,227 @@
+// C ABI of libpacked_attn.so (include/packed_attn.h): argument checks, the
+// device copies of a packing's tables, and the launches.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "pa_internal.h"
+#include "pa_simple.cuh"
+
+namespace pa {
+namespace {
+
+__device__ int g_pa_status = 0;
+
+// Calls that a capture on another thread must not be broken by.
+struct RelaxedCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// The tables on the current device: found, or copied there (not inside a
+// capture of `s`, whose graph would hold an allocation that it cannot replay).
+int to_device(const pa_layout* L, cudaStream_t s, DeviceCopy* out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SA_ERR_CUDA;
+  std::lock_guard<std::mutex> g(L->mu);
+  for (auto& d : L->dev)
+    if (d.device == dev) {
+      *out = d;
+      return SA_OK;
+    }
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) return SA_ERR_CUDA;
+  if (cap != cudaStreamCaptureStatusNone) return SA_ERR_INVALID_ARG;
+  RelaxedCapture relaxed;
+  const std::vector<Slot>* tabs[3] = {&L->fwd, &L->fwd2, &L->bwd};
+  size_t n = 0;
+  for (auto* t : tabs) n += t->size();
+  Slot* dptr = nullptr;
+  if (cudaMalloc(reinterpret_cast<void**>(&dptr), (n ? n : 1) * sizeof(Slot)) != cudaSuccess) return SA_ERR_CUDA;
+  DeviceCopy d;
+  d.device = dev;
+  d.blob = dptr;
+  const Slot** fields[3] = {&d.fwd, &d.fwd2, &d.bwd};
+  size_t at = 0;
+  bool ok = true;
+  for (int i = 0; i < 3; ++i) {
+    *fields[i] = dptr + at;
+    const size_t bytes = tabs[i]->size() * sizeof(Slot);
+    if (bytes)
+      ok = ok && cudaMemcpyAsync(dptr + at, tabs[i]->data(), bytes, cudaMemcpyHostToDevice, cudaStreamPerThread) ==
+                     cudaSuccess;
+    at += tabs[i]->size();
+  }
+  // on the device before any stream may read it
+  ok = cudaStreamSynchronize(cudaStreamPerThread) == cudaSuccess && ok;
+  if (!ok) {
+    cudaFree(dptr);
+    return SA_ERR_CUDA;
+  }
+  try {
+    L->dev.push_back(d);
+  } catch (...) {
+    cudaFree(dptr);
+    return SA_ERR_CUDA;
+  }
+  *out = d;
+  return SA_OK;
+}
+
+struct Call {
+  long long rows;
+  int Hq, Hkv, D, dtype;
+  float scale;
+  cudaStream_t s;
+};
+
+bool stride_ok(int64_t st, int64_t extent) { return extent <= 1 || (st > 0 && st % 8 == 0 && st < (int64_t(1) << 38)); }
+
+bool tensor_ok(const pa_tensor* t, const Call& c, int heads) {
+  if (!t || !t->data || (reinterpret_cast<uintptr_t>(t->data) & 15)) return false;
+  return stride_ok(t->row_stride, c.rows) && stride_ok(t->head_stride, heads);
+}
+
+// An output's (row, head) vectors must not overlap: heads inside a row, or rows inside a head.
+bool output_ok(const pa_tensor* t, const Call& c, int heads) {
+  if (!tensor_ok(t, c, heads)) return false;
+  const int64_t rs = c.rows > 1 ? t->row_stride : 0, hs = heads > 1 ? t->head_stride : 0;
+  if (c.rows > 1 && rs < c.D) return false;
+  if (heads > 1 && hs < c.D) return false;
+  if (c.rows <= 1 || heads <= 1) return true;
+  return (heads - 1) * hs + c.D <= rs || (c.rows - 1) <= (hs - c.D) / rs;
+}
+
+int check_call(const Call& c, const pa_layout* L) {
+  if (!L || c.Hq < 1 || c.Hkv < 1 || c.Hq > 65535 || c.Hq % c.Hkv || c.rows < L->rows ||
+      c.rows > (int64_t(1) << 31) - 1024 || (c.dtype != PA_BF16 && c.dtype != PA_FP16))
+    return SA_ERR_INVALID_ARG;
+  if (!(c.scale > 0.f) || !std::isfinite(c.scale)) return SA_ERR_INVALID_ARG;
+  if (c.D != 32 && c.D != 64 && c.D != 128) return SA_ERR_UNSUPPORTED;
+  return SA_OK;
+}
+
+View view(const pa_tensor* t) { return View{t->data, t->row_stride, t->head_stride}; }
+
+int launched() { return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA; }
+
+size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+
+template <typename F>
+int dispatch(const Call& c, F&& f) {
+  auto by_d = [&](auto t) -> int {
+    switch (c.D) {
+      case 32: return f(t, std::integral_constant<int, 32>{});
+      case 64: return f(t, std::integral_constant<int, 64>{});
+      default: return f(t, std::integral_constant<int, 128>{});
+    }
+  };
+  return c.dtype == PA_BF16 ? by_d(__nv_bfloat16{}) : by_d(__half{});
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+void packed_attn_layout_free(pa_layout* L) {
+  if (!L) return;
+  int cur = -1;
+  const bool have = !L->dev.empty() && cudaGetDevice(&cur) == cudaSuccess;
+  {
+    RelaxedCapture relaxed;
+    for (auto& d : L->dev)
+      if (cudaSetDevice(d.device) == cudaSuccess) cudaFree(d.blob);
+  }
+  if (have) cudaSetDevice(cur);
+  delete L;
+}
+
+int packed_attn_layout_upload(const pa_layout* L, void* stream) {
+  if (!L) return SA_ERR_INVALID_ARG;
+  DeviceCopy dc;
+  return to_device(L, static_cast<cudaStream_t>(stream), &dc);
+}
+
+int packed_attn_fwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, const pa_tensor* o, float* lse,
+                    int64_t lse_stride, int64_t rows, int Hq, int Hkv, int D, int dtype, float scale,
+                    const pa_layout* L, void* stream) {
+  const Call c{rows, Hq, Hkv, D, dtype, scale, static_cast<cudaStream_t>(stream)};
+  int st = check_call(c, L);
+  if (st) return st;
+  if (L->rows == 0) return SA_OK;
+  if (!tensor_ok(q, c, Hq) || !tensor_ok(k, c, Hkv) || !tensor_ok(v, c, Hkv) || !output_ok(o, c, Hq) || !lse ||
+      lse_stride < rows || o->data == q->data || o->data == k->data || o->data == v->data)
+    return SA_ERR_INVALID_ARG;
+  DeviceCopy dc;
+  if ((st = to_device(L, c.s, &dc))) return st;
+  return dispatch(c, [&](auto t, auto d) -> int {
+    simple_fwd_kernel<decltype(t), d.value><<<dim3(L->fwd.size(), Hq), 512, 0, c.s>>>(
+        dc.fwd, view(q), view(k), view(v), view(o), lse, lse_stride, Hq / Hkv, scale);
+    return launched();
+  });
+}
+
+size_t packed_attn_bwd_workspace_size(int Hq, int Hkv, int D, const pa_layout* L) {
+  const Call c{L ? static_cast<long long>(L->rows) : 0, Hq, Hkv, D, PA_BF16, 1.f, nullptr};
+  if (check_call(c, L)) return 0;
+  return align256(static_cast<size_t>(Hq) * L->rows * sizeof(float)) + 256;
+}
+
+int packed_attn_bwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, const pa_tensor* o, const float* lse,
+                    int64_t lse_stride, const pa_tensor* dO, const pa_tensor* dq, const pa_tensor* dk,
+                    const pa_tensor* dv, int64_t rows, int Hq, int Hkv, int D, int dtype, float scale,
+                    const pa_layout* L, void* ws, size_t ws_bytes, void* stream) {
+  const Call c{rows, Hq, Hkv, D, dtype, scale, static_cast<cudaStream_t>(stream)};
+  int st = check_call(c, L);
+  if (st) return st;
+  if (L->rows == 0) return SA_OK;
+  if (!tensor_ok(q, c, Hq) || !tensor_ok(k, c, Hkv) || !tensor_ok(v, c, Hkv) || !tensor_ok(o, c, Hq) ||
+      !tensor_ok(dO, c, Hq) || !output_ok(dq, c, Hq) || !output_ok(dk, c, Hkv) || !output_ok(dv, c, Hkv) || !lse ||
+      lse_stride < rows)
+    return SA_ERR_INVALID_ARG;
+  const pa_tensor* outs[3] = {dq, dk, dv};
+  const pa_tensor* ins[5] = {q, k, v, o, dO};
+  for (int i = 0; i < 3; ++i) {
+    for (auto* t : ins)
+      if (outs[i]->data == t->data) return SA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (outs[i]->data == outs[j]->data) return SA_ERR_INVALID_ARG;
+  }
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < packed_attn_bwd_workspace_size(Hq, Hkv, D, L))
+    return SA_ERR_WORKSPACE;
+  DeviceCopy dc;
+  if ((st = to_device(L, c.s, &dc))) return st;
+  float* delta = static_cast<float*>(ws);
+  return dispatch(c, [&](auto t, auto d) -> int {
+    using T = decltype(t);
+    constexpr int DD = d.value;
+    const int G = Hq / Hkv;
+    simple_delta_kernel<T, DD><<<dim3((L->rows + 7) / 8, Hq), 256, 0, c.s>>>(view(o), view(dO), delta, L->rows);
+    simple_dq_kernel<T, DD><<<dim3(L->fwd.size(), Hq), 512, 0, c.s>>>(dc.fwd, view(q), view(k), view(v), view(dO),
+                                                                      view(dq), lse, lse_stride, delta, L->rows, G, scale);
+    simple_dkv_kernel<T, DD><<<dim3(L->bwd.size(), Hkv), 512, 0, c.s>>>(
+        dc.bwd, view(q), view(k), view(v), view(dO), view(dk), view(dv), lse, lse_stride, delta, L->rows, G, scale);
+    return launched();
+  });
+}
+
+int packed_attn_status(void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaStreamSynchronize(s) != cudaSuccess) return SA_ERR_CUDA;
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_pa_status, sizeof(int)) != cudaSuccess) return SA_ERR_CUDA;
+  if (v != 0) {
+    const int zero = 0;
+    cudaMemcpyToSymbol(g_pa_status, &zero, sizeof(int));
+    return v;
+  }
+  return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+}  // extern "C"

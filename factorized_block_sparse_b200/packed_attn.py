@@ -1,0 +1,263 @@
+"""Thin Python binding of the C ABI in ``include/packed_attn.h``: causal
+attention over packed sequences of different lengths, with grouped heads.
+
+Argument marshalling only: the computation runs in the CUDA kernels of
+``libpacked_attn.so``.  ``q`` is ``[T, Hq, D]``, ``k`` and ``v``
+``[T, Hkv, D]`` (bf16 or fp16, the last dimension contiguous, rows and heads
+at any stride that is a multiple of 8 elements, so slices of a fused
+projection are taken as they are); the sequences of the layout lie one
+behind another in the rows.  ``lse`` is float32 ``[Hq, T]``.  The stream is
+torch's current stream of the tensors' device unless one is given.  There is
+no CPU fallback: if the library is missing, loading this module raises.
+
+Use::
+
+    lay = pa.Layout([4096, 17, 901])           # built once per batch
+    o, lse = pa.forward(q, k, v, lay)
+    dq, dk, dv = pa.backward(q, k, v, o, lse, dO, lay)
+"""
+
+import ctypes
+import math
+import os
+
+import numpy as np
+
+from . import sparse_attn as sa
+
+_HERE = os.path.dirname(os.path.abspath(__file__))
+LIB_PATH = os.path.join(_HERE, "libpacked_attn.so")
+
+# Every entry point declared in include/packed_attn.h.
+EXPORTS = ("packed_attn_layout", "packed_attn_layout_free", "packed_attn_layout_rows", "packed_attn_layout_upload",
+           "packed_attn_fwd", "packed_attn_bwd_workspace_size", "packed_attn_bwd", "packed_attn_status")
+
+
+class _Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+def load_library(path=None):
+    path = path or LIB_PATH
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with "
+                           "`python -m factorized_block_sparse_b200.build` (no CPU fallback exists)")
+    lib = ctypes.CDLL(path)
+    I, VP, SZ, L64, F = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64, ctypes.c_float
+    T = ctypes.POINTER(_Tensor)
+    lib.packed_attn_layout.argtypes = [VP, I, ctypes.POINTER(VP)]
+    lib.packed_attn_layout.restype = I
+    lib.packed_attn_layout_free.argtypes = [VP]
+    lib.packed_attn_layout_free.restype = None
+    lib.packed_attn_layout_rows.argtypes = [VP]
+    lib.packed_attn_layout_rows.restype = L64
+    lib.packed_attn_layout_upload.argtypes = [VP, VP]
+    lib.packed_attn_layout_upload.restype = I
+    lib.packed_attn_fwd.argtypes = [T, T, T, T, VP, L64, L64, I, I, I, I, F, VP, VP]
+    lib.packed_attn_fwd.restype = I
+    lib.packed_attn_bwd_workspace_size.argtypes = [I, I, I, VP]
+    lib.packed_attn_bwd_workspace_size.restype = SZ
+    lib.packed_attn_bwd.argtypes = [T, T, T, T, VP, L64, T, T, T, T, L64, I, I, I, I, F, VP, VP, SZ, VP]
+    lib.packed_attn_bwd.restype = I
+    lib.packed_attn_status.argtypes = [VP]
+    lib.packed_attn_status.restype = I
+    return lib
+
+
+lib = load_library()
+
+
+class Layout:
+    """Owns a ``pa_layout*`` of the given sequence lengths (host integers)."""
+
+    def __init__(self, lengths):
+        self._h = ctypes.c_void_p()
+        wide = np.asarray(lengths, dtype=np.int64).reshape(-1)
+        if wide.size and (wide.min() < 0 or wide.max() > np.iinfo(np.int32).max):
+            raise ValueError("sequence lengths must be at least 0 and fit 32 bits")
+        self.lengths = tuple(int(n) for n in wide)
+        arr = np.ascontiguousarray(wide, dtype=np.int32)
+        h = ctypes.c_void_p()
+        sa._check(lib.packed_attn_layout(arr.ctypes.data, int(arr.size), ctypes.byref(h)), "packed_attn_layout")
+        self._h = h
+        self.rows = int(lib.packed_attn_layout_rows(h))
+
+    @property
+    def handle(self):
+        if not self._h.value:
+            raise ValueError("the layout is closed")
+        return self._h
+
+    def upload(self, device=None, stream=None):
+        """Tables to ``device`` (default: the current one); needed before a call is captured into a graph."""
+        import torch
+
+        with torch.cuda.device(device):
+            sa._check(lib.packed_attn_layout_upload(self.handle, sa._stream_ptr(stream)), "packed_attn_layout_upload")
+
+    def close(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            lib.packed_attn_layout_free(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _dtype(t):
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        return 0
+    if t.dtype == torch.float16:
+        return 1
+    raise ValueError(f"expected bf16 or fp16 tensors, got {t.dtype}")
+
+
+def _desc(t):
+    """The C view of a ``[T, H, D]`` tensor; the strides of extents of 1 carry no meaning and are not read."""
+    return _Tensor(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _check_tensors(q, k, v, layout, more=()):
+    """Shapes, types and devices of a call; returns (T, Hq, Hkv, D)."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("expected q [T, Hq, D] and k, v [T, Hkv, D]")
+    T, Hq, D = (int(x) for x in q.shape)
+    Hkv = int(k.shape[1])
+    if tuple(k.shape) != (T, Hkv, D) or k.shape != v.shape:
+        raise ValueError(f"k and v must be [{T}, Hkv, {D}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    if T < layout.rows:
+        raise ValueError(f"the layout has {layout.rows} rows, the tensors {T}")
+    for name, t, shape in (("q", q, q.shape), ("k", k, k.shape), ("v", v, k.shape), *more):
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        if t.dtype != q.dtype or t.device != q.device or t.device.type != "cuda":
+            raise ValueError(f"{name} must be a {q.dtype} tensor on the CUDA device of q")
+        if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"the last dimension of {name} must be contiguous")
+    return T, Hq, Hkv, D
+
+
+def _check_lse(lse, Hq, T, q):
+    import torch
+
+    if tuple(lse.shape) != (Hq, T) or lse.dtype != torch.float32 or lse.device != q.device:
+        raise ValueError(f"lse must be float32 [{Hq}, {T}] on the device of q")
+    if T > 1 and lse.stride(1) != 1:
+        raise ValueError("the rows of lse must be contiguous")
+    return lse.stride(0) if Hq > 1 else T
+
+
+def _stream_of(t, stream):
+    if stream is not None:
+        return sa._stream_ptr(stream)
+    import torch
+
+    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+
+
+class _On:
+    """The device of a tensor as the current one for the length of a call (nothing to do when it is)."""
+
+    def __init__(self, t):
+        import torch
+
+        self.guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.guard:
+            self.guard.__enter__()
+
+    def __exit__(self, *a):
+        if self.guard:
+            self.guard.__exit__(*a)
+
+
+def packed_attn_fwd(q, k, v, o, lse, layout, stream=None, scale=None):
+    """Writes ``o`` and ``lse`` in place (C ABI call); ``scale`` None is 1/sqrt(D)."""
+    T, Hq, Hkv, D = _check_tensors(q, k, v, layout, (("o", o, q.shape),))
+    ls = _check_lse(lse, Hq, T, q)
+    dt = _dtype(q)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    with _On(q):
+        sa._check(lib.packed_attn_fwd(_desc(q), _desc(k), _desc(v), _desc(o), sa._ptr(lse), ls, T, Hq, Hkv, D, dt, scale,
+                                      layout.handle, _stream_of(q, stream)), "packed_attn_fwd")
+
+
+def packed_attn_bwd(q, k, v, o, lse, dO, dq, dk, dv, layout, ws, stream=None, scale=None):
+    """Writes ``dq``, ``dk``, ``dv`` in place (C ABI call); ``scale`` None is 1/sqrt(D)."""
+    T, Hq, Hkv, D = _check_tensors(q, k, v, layout, (("o", o, q.shape), ("dO", dO, q.shape), ("dq", dq, q.shape),
+                                                     ("dk", dk, k.shape), ("dv", dv, k.shape)))
+    ls = _check_lse(lse, Hq, T, q)
+    dt = _dtype(q)
+    if ws.device != q.device or not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the device of q")
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    with _On(q):
+        sa._check(lib.packed_attn_bwd(_desc(q), _desc(k), _desc(v), _desc(o), sa._ptr(lse), ls, _desc(dO), _desc(dq),
+                                      _desc(dk), _desc(dv), T, Hq, Hkv, D, dt, scale, layout.handle, sa._ptr(ws),
+                                      ws.numel() * ws.element_size(), _stream_of(q, stream)), "packed_attn_bwd")
+
+
+def packed_attn_status(stream=None):
+    return int(lib.packed_attn_status(sa._stream_ptr(stream)))
+
+
+# ------------------------------------------------------------ conveniences
+def _on_stream(stream, t):
+    """torch work of a call (allocation, zeroing) on the stream that the call runs on."""
+    import contextlib
+
+    import torch
+
+    if stream is None:
+        return contextlib.nullcontext()
+    s = torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int) else stream
+    return torch.cuda.stream(s)
+
+
+def _empty(t, heads, rows):
+    """An output like ``t`` with ``heads`` heads, zero in the rows behind the last sequence."""
+    import torch
+
+    out = torch.empty((t.shape[0], heads, t.shape[2]), dtype=t.dtype, device=t.device)
+    if rows < t.shape[0]:
+        out[rows:].zero_()
+    return out
+
+
+def workspace(Hq, Hkv, D, layout, device):
+    import torch
+
+    n = int(lib.packed_attn_bwd_workspace_size(Hq, Hkv, D, layout.handle))
+    if n == 0:
+        raise sa.SparseAttnError(sa.SA_ERR_INVALID_ARG, "packed_attn_bwd_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def forward(q, k, v, layout, stream=None, scale=None):
+    """Allocates ``o`` and ``lse`` (zero in rows behind the last sequence) and runs the forward pass."""
+    import torch
+
+    T, Hq, _, _ = _check_tensors(q, k, v, layout)
+    with _on_stream(stream, q):
+        o = _empty(q, Hq, layout.rows)
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+        if layout.rows < T:
+            lse[:, layout.rows:].zero_()
+    packed_attn_fwd(q, k, v, o, lse, layout, stream, scale)
+    return o, lse
+
+
+def backward(q, k, v, o, lse, dO, layout, ws=None, stream=None, scale=None):
+    """Allocates ``dq``, ``dk``, ``dv`` (zero in rows behind the last sequence), and a workspace if none is given."""
+    _, Hq, Hkv, D = _check_tensors(q, k, v, layout)
+    with _on_stream(stream, q):
+        ws = workspace(Hq, Hkv, D, layout, q.device) if ws is None else ws
+        dq, dk, dv = _empty(q, Hq, layout.rows), _empty(k, Hkv, layout.rows), _empty(k, Hkv, layout.rows)
+    packed_attn_bwd(q, k, v, o, lse, dO, dq, dk, dv, layout, ws, stream, scale)
+    return dq, dk, dv
