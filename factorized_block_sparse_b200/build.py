@@ -68,7 +68,7 @@ def build_test_lib(force=False, verbose=False):
 # The Sparse Transformer block around the op: its own library, linked against
 # libsparse_attn.so (found next to it) and cuBLAS (the projections).
 BLOCK_LIB = os.path.join(HERE, "libsparse_block.so")
-BLOCK_SOURCES = [os.path.join(HERE, "csrc", "sb_block.cu")]
+BLOCK_SOURCES = [os.path.join(HERE, "csrc", f) for f in ("sb_block.cu", "sb_train.cu")]
 BLOCK_HEADERS = [os.path.join(ROOT, "include", "sparse_block.h"), os.path.join(ROOT, "include", "sparse_attn.h")]
 
 

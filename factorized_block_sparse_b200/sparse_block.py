@@ -18,7 +18,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsparse_block.so")
 
 PARAMS = ("ln1_g", "ln1_b", "w_qkv", "w_o", "ln2_g", "ln2_b", "w_1", "w_2")
-EXPORTS = ("sparse_block_workspace_size", "sparse_block_fwd", "sparse_block_bwd", "sparse_block_gelu")
+EXPORTS = ("sparse_block_workspace_size", "sparse_block_fwd", "sparse_block_bwd", "sparse_block_gelu",
+           "sparse_block_layer_norm_fwd", "sparse_block_layer_norm_bwd_workspace_size", "sparse_block_layer_norm_bwd",
+           "sparse_block_clip_workspace_size", "sparse_block_clip_grads")
 
 
 class _Params(ctypes.Structure):
@@ -41,6 +43,17 @@ def load_library(path=None):
     lib.sparse_block_bwd.restype = I
     lib.sparse_block_gelu.argtypes = [VP, VP, VP, SZ, VP]
     lib.sparse_block_gelu.restype = I
+    L64, F = ctypes.c_int64, ctypes.c_float
+    lib.sparse_block_layer_norm_fwd.argtypes = [VP, L64, VP, VP, VP, L64, VP, VP, L64, I, F, I, VP]
+    lib.sparse_block_layer_norm_fwd.restype = I
+    lib.sparse_block_layer_norm_bwd_workspace_size.argtypes = [L64, I]
+    lib.sparse_block_layer_norm_bwd_workspace_size.restype = SZ
+    lib.sparse_block_layer_norm_bwd.argtypes = [VP, L64, VP, VP, L64, VP, VP, VP, L64, VP, VP, L64, I, I, VP, SZ, VP]
+    lib.sparse_block_layer_norm_bwd.restype = I
+    lib.sparse_block_clip_workspace_size.argtypes = []
+    lib.sparse_block_clip_workspace_size.restype = SZ
+    lib.sparse_block_clip_grads.argtypes = [I, VP, VP, VP, VP, ctypes.c_double, VP, VP, SZ, VP]
+    lib.sparse_block_clip_grads.restype = I
     return lib
 
 
@@ -93,8 +106,10 @@ def forward(x, params, H, layout, ws=None, stream=None):
     return y
 
 
-def backward(x, dy, params, H, layout, ws=None, stream=None):
-    """``(dx, grads)``: grads holds float32 tensors of the parameters' shapes."""
+def backward(x, dy, params, H, layout, ws=None, stream=None, max_norm=None):
+    """``(dx, grads)``: grads holds float32 tensors of the parameters' shapes.
+    With ``max_norm`` the gradients are clipped by their global norm in place
+    (``clip_grads``) and the result is ``(dx, grads, norm)``."""
     import torch
 
     B, N, D = _dims(x, H)
@@ -102,6 +117,8 @@ def backward(x, dy, params, H, layout, ws=None, stream=None):
     dx = torch.empty_like(x)
     grads = {n: torch.empty(params[n].shape, dtype=torch.float32, device=x.device) for n in PARAMS}
     sparse_block_bwd(x, dy, params, dx, grads, H, layout, ws, stream)
+    if max_norm is not None:
+        return dx, grads, clip_grads(grads, max_norm, stream=stream)
     return dx, grads
 
 
@@ -118,3 +135,171 @@ def gelu(u, grad=False, stream=None):
     d = torch.empty_like(u) if grad else None
     sparse_block_gelu(u, g, d, stream)
     return (g, d) if grad else g
+
+
+# ------------------------------------------------------------ layer norm
+def _dtype(t):
+    import torch
+
+    try:
+        return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}[t.dtype]
+    except KeyError:
+        raise ValueError(f"expected a bf16, fp16 or float32 tensor, got {t.dtype}") from None
+
+
+def _rows(name, t, like=None):
+    """``t`` as ``(pointer tensor, rows, C, row stride)``: the leading dimensions must be one run of rows."""
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} must have at least one channel")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must be a {like.dtype} tensor of shape {tuple(like.shape)} on {like.device}")
+    C = int(t.shape[-1])
+    if C > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    rows, ld = 1, C
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if rows > 1 and n > 0 and st != rows * ld:
+            raise ValueError(f"the leading dimensions of {name} must be rows at one stride")
+        if rows == 1:
+            ld = int(st)
+        rows *= int(n)
+    if rows > 1 and ld < C:
+        raise ValueError(f"the rows of {name} overlap")
+    return rows, C, (ld if rows > 1 else C)
+
+
+def _vector(name, t, C, device):
+    import torch
+
+    if t.dtype != torch.float32 or t.device != device or tuple(t.shape) != (C,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 [{C}] tensor on {device}")
+    return sa._ptr(t)
+
+
+def _on(t):
+    """The device of ``t`` as the current one for the length of a call."""
+    import contextlib
+
+    import torch
+
+    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _stream(t, stream):
+    import torch
+
+    if stream is None:
+        return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    return sa._stream_ptr(stream)
+
+
+def _alloc_on(stream, t):
+    """torch allocations of a call belong to the stream that the call runs on."""
+    import contextlib
+
+    import torch
+
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int) else stream)
+
+
+def layer_norm(x, g, b=None, eps=1e-5, stream=None):
+    """``(y, mean, rstd)`` of rows ``x [..., C]`` (bf16, fp16 or float32; rows at any one stride): y of x's type and
+    shape, contiguous; mean and rstd float32 of the leading shape, for ``layer_norm_backward``.  ``g`` and ``b`` are
+    float32 ``[C]``; without ``b`` there is no bias."""
+    import torch
+
+    M, C, ld = _rows("x", x)
+    dt = _dtype(x)
+    gp = _vector("g", g, C, x.device)
+    bp = _vector("b", b, C, x.device) if b is not None else None
+    with _on(x), _alloc_on(stream, x):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device)
+        mean, rstd = stats[0], stats[1]
+        if M:
+            sa._check(lib.sparse_block_layer_norm_fwd(sa._ptr(x), ld, gp, bp, sa._ptr(y), C, sa._ptr(mean),
+                                                      sa._ptr(rstd), M, C, eps, dt, _stream(x, stream)),
+                      "sparse_block_layer_norm_fwd")
+    return y, mean, rstd
+
+
+def layer_norm_backward(x, g, dy, mean, rstd, bias=True, stream=None):
+    """``(dx, dg, db)`` from ``layer_norm``'s input, gain and statistics and the upstream gradient ``dy``: dx of x's
+    type and shape, contiguous; dg and db float32 ``[C]`` (db None without ``bias``)."""
+    import torch
+
+    M, C, ld = _rows("x", x)
+    dt = _dtype(x)
+    _, _, ldd = _rows("dy", dy, x)
+    gp = _vector("g", g, C, x.device)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or t.shape != x.shape[:-1] or t.device != x.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(x.shape[:-1])} on {x.device}")
+    with _on(x), _alloc_on(stream, x):
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dg = torch.empty(C, dtype=torch.float32, device=x.device)
+        db = torch.empty(C, dtype=torch.float32, device=x.device) if bias else None
+        n = int(lib.sparse_block_layer_norm_bwd_workspace_size(M, C))
+        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=x.device)
+        if M == 0:
+            dg.zero_()
+            if bias:
+                db.zero_()
+        else:
+            sa._check(lib.sparse_block_layer_norm_bwd(sa._ptr(x), ld, gp, sa._ptr(dy), ldd, sa._ptr(mean), sa._ptr(rstd),
+                                                      sa._ptr(dx), C, sa._ptr(dg), sa._ptr(db) if bias else None, M, C,
+                                                      dt, sa._ptr(ws), ws.numel(), _stream(x, stream)),
+                      "sparse_block_layer_norm_bwd")
+    return dx, dg, db
+
+
+# ------------------------------------------------- norm and clipping of gradients
+def _clip(grads, max_norm, out, stream):
+    import torch
+
+    grads = list(grads.values()) if isinstance(grads, dict) else list(grads)
+    outs = None if out is None else (list(out.values()) if isinstance(out, dict) else list(out))
+    if not grads:
+        raise ValueError("expected at least one gradient")
+    if outs is not None and len(outs) != len(grads):
+        raise ValueError(f"{len(grads)} gradients, {len(outs)} outputs")
+    dev = grads[0].device
+    if dev.type != "cuda":
+        raise ValueError("gradients must be CUDA tensors")
+    for t in grads:
+        if t.device != dev or not t.is_contiguous():
+            raise ValueError(f"gradients must be contiguous tensors on {dev}")
+    n = len(grads)
+    dts = [_dtype(t) for t in grads]
+    if outs is not None:
+        for t, o in zip(grads, outs):
+            if o.shape != t.shape or o.dtype != t.dtype or o.device != dev or not o.is_contiguous():
+                raise ValueError("an output must be a contiguous tensor of its gradient's shape, type and device")
+    VPn, SZn, In = ctypes.c_void_p * n, ctypes.c_size_t * n, ctypes.c_int * n
+    gp = VPn(*[t.data_ptr() for t in grads])
+    op = None if outs is None else VPn(*[t.data_ptr() for t in outs])
+    with _on(grads[0]), _alloc_on(stream, grads[0]):
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        ws = torch.empty(int(lib.sparse_block_clip_workspace_size()), dtype=torch.uint8, device=dev)
+        sa._check(lib.sparse_block_clip_grads(n, gp, op, SZn(*[t.numel() for t in grads]), In(*dts), float(max_norm),
+                                              sa._ptr(norm), sa._ptr(ws), ws.numel(), _stream(grads[0], stream)),
+                  "sparse_block_clip_grads")
+    return norm
+
+
+def grad_norm(grads, stream=None):
+    """The norm of all gradients (a list or dict of contiguous bf16, fp16 or float32 tensors) taken as one vector, as
+    a float32 scalar tensor on their device."""
+    return _clip(grads, 0.0, None, stream)
+
+
+def clip_grads(grads, max_norm, out=None, stream=None):
+    """Multiplies every gradient by ``min(1, max_norm / (norm + 1e-6))``, in place or into the tensors of ``out``, and
+    returns ``norm``, the global norm before it (a float32 scalar tensor on the device; nothing waits for it)."""
+    return _clip(grads, max_norm, grads if out is None else out, stream)

@@ -122,6 +122,68 @@ int sparse_block_bwd(const void* x, const void* dy, const sb_params* p, void* dx
                      int B, int N, int H, int D, const sa_layout* layout, void* workspace,
                      size_t ws_bytes, void* stream);
 
+/* Element types of the calls below. */
+enum sb_dtype { SB_BF16 = 0, SB_FP16 = 1, SB_FP32 = 2 };
+
+/*
+ * sparse_block_layer_norm_fwd - layer norm on its own, over M rows of C
+ * channels: mean = sum x / C, rstd = 1 / sqrt(sum (x - mean)^2 / C + eps),
+ * y = (x - mean) rstd g + b, and the float32 statistics mean and rstd [M]
+ * for the backward pass (either may be null).  x, y: rows of `dtype` at
+ * strides of ldx and ldy elements (>= C); g, b: float32 [C], b may be null
+ * (no bias).  Sums, statistics and the affine map are float32; y is rounded
+ * once.  Any C up to 16384 and any alignment of the type itself; rows whose
+ * addresses and widths are multiples of 16 bytes are moved in 16-byte words.
+ * y may be x (with ldy == ldx), and must not overlap it otherwise.
+ * Errors: SA_ERR_INVALID_ARG (x, g or y null, M < 0, C < 1, a stride below C,
+ * an unknown type, a misaligned pointer, eps negative or not finite),
+ * SA_ERR_UNSUPPORTED (C above 16384), SA_ERR_CUDA.
+ */
+int sparse_block_layer_norm_fwd(const void* x, int64_t ldx, const float* g, const float* b, void* y, int64_t ldy,
+                                float* mean, float* rstd, int64_t M, int C, float eps, int dtype, void* stream);
+
+/* Bytes of device workspace the backward call needs; 0 for a shape it refuses. */
+size_t sparse_block_layer_norm_bwd_workspace_size(int64_t M, int C);
+
+/*
+ * sparse_block_layer_norm_bwd - from dy and the forward's x, mean and rstd,
+ * with xh = (x - mean) rstd and t = dy g:
+ *   dx = rstd (t - sum t / C - xh sum (t xh) / C),
+ *   dg = sum over rows dy xh,  db = sum over rows dy  (float32, overwritten;
+ *   db may be null).
+ * dg and db are summed in a fixed order: the same call gives the same bits.
+ * dx may be dy or x (with the same stride), and must not overlap them
+ * otherwise.  M = 0 writes zeros to dg and db.  workspace: at least
+ * sparse_block_layer_norm_bwd_workspace_size() bytes, 256-byte aligned.
+ * Errors: as sparse_block_layer_norm_fwd, and SA_ERR_WORKSPACE.
+ */
+int sparse_block_layer_norm_bwd(const void* x, int64_t ldx, const float* g, const void* dy, int64_t lddy,
+                                const float* mean, const float* rstd, void* dx, int64_t lddx, float* dg, float* db,
+                                int64_t M, int C, int dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace sparse_block_clip_grads needs. */
+size_t sparse_block_clip_workspace_size(void);
+
+/*
+ * sparse_block_clip_grads - the norm of n gradients taken as one vector, and
+ * their clipping by it:
+ *   norm = sqrt(sum over tensors and elements of g^2),
+ *   out_i = c g_i  with  c = min(1, max_norm / (norm + 1e-6)).
+ * grads, outs, numel, dtypes: host arrays of n device pointers, counts and
+ * sb_dtype values, read before the call returns; outs null computes the norm
+ * alone.  out_i may be grads_i (in place; nothing is written where c = 1);
+ * other than that no output may overlap a gradient or another output.
+ * norm: one float32 on the device.  The sum of squares does not overflow or
+ * vanish in float32 and has a fixed order.  A norm that is not finite acts as
+ * the formula says: c = 0 for inf, NaN for NaN.
+ * Errors: SA_ERR_INVALID_ARG (a null array, a null pointer with a count above
+ * 0, n < 0, an unknown type, a pointer not aligned to its element, outputs
+ * that overlap, max_norm negative or NaN), SA_ERR_WORKSPACE, SA_ERR_CUDA.
+ */
+int sparse_block_clip_grads(int n, const void* const* grads, void* const* outs, const size_t* numel,
+                            const int* dtypes, double max_norm, float* norm, void* workspace, size_t ws_bytes,
+                            void* stream);
+
 #ifdef __cplusplus
 }
 #endif

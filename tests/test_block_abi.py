@@ -68,3 +68,50 @@ def test_gelu_argument_checks(sb):
     assert f(a, b, a, 8, None) == sa.SA_ERR_INVALID_ARG                 # dgelu is u
     assert f(a, b, b, 8, None) == sa.SA_ERR_INVALID_ARG                 # dgelu is g
     assert f(a, b, c, 0, None) == sa.SA_OK                              # nothing to do
+
+
+def test_layer_norm_and_clip_argument_checks(sb):
+    # refused before anything reaches the device (no GPU needed)
+    from factorized_block_sparse_b200 import sparse_attn as sa
+
+    INV, UNS, WS = sa.SA_ERR_INVALID_ARG, sa.SA_ERR_UNSUPPORTED, sa.SA_ERR_WORKSPACE
+    A, Bp, Cp, Dp, Ep = 0x10000, 0x20000, 0x30000, 0x40000, 0x50000
+
+    def fwd(x=A, ldx=64, g=Bp, b=Cp, y=Dp, ldy=64, mean=Ep, rstd=0x60000, M=4, C=64, eps=1e-5, dt=0):
+        return sb.lib.sparse_block_layer_norm_fwd(x, ldx, g, b, y, ldy, mean, rstd, M, C, eps, dt, None)
+
+    for kw in (dict(x=None), dict(g=None), dict(y=None), dict(M=-1), dict(C=0), dict(ldx=63), dict(ldy=63), dict(dt=3),
+               dict(dt=-1), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(x=A + 1), dict(b=Cp + 2),
+               dict(mean=Ep + 2), dict(y=A, ldx=64, ldy=72), dict(dt=2, x=A + 2)):
+        assert fwd(**kw) == INV, kw
+    assert fwd(C=16385, ldx=16385, ldy=16385) == UNS
+    assert fwd(M=0) == sa.SA_OK
+    size = sb.lib.sparse_block_layer_norm_bwd_workspace_size
+    assert size(-1, 64) == 0 and size(4, 0) == 0 and size(4, 16385) == 0 and size(0, 64) > 0
+
+    def bwd(x=A, ldx=64, g=Bp, dy=Cp, lddy=64, mean=Dp, rstd=Ep, dx=0x60000, lddx=64, dg=0x70000, db=0x80000, M=4, C=64,
+            dt=0, ws=0x90000, wb=1 << 30):
+        return sb.lib.sparse_block_layer_norm_bwd(x, ldx, g, dy, lddy, mean, rstd, dx, lddx, dg, db, M, C, dt, ws, wb, None)
+
+    for kw in (dict(x=None), dict(g=None), dict(dy=None), dict(mean=None), dict(rstd=None), dict(dx=None), dict(dg=None),
+               dict(M=-1), dict(C=0), dict(ldx=63), dict(lddy=63), dict(lddx=63), dict(dt=5), dict(dx=A, lddx=72),
+               dict(dx=Cp, lddx=72), dict(db=0x70000), dict(dy=Cp + 1), dict(dg=0x70002)):
+        assert bwd(**kw) == INV, kw
+    assert bwd(C=20000, ldx=20000, lddy=20000, lddx=20000) == UNS
+    assert bwd(ws=None) == WS and bwd(ws=0x90010) == WS and bwd(wb=100) == WS
+
+    VP, SZ, I = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+
+    def clip(g=(A, Bp), o=(A, Bp), n=(16, 16), dt=(0, 2), mx=1.0, norm=Ep, ws=0x90000, wb=1 << 20, count=None):
+        k = len(g)
+        return sb.lib.sparse_block_clip_grads(k if count is None else count, (VP * k)(*g), (VP * k)(*o) if o else None,
+                                              (SZ * k)(*n), (I * k)(*dt), mx, norm, ws, wb, None)
+
+    for kw in (dict(count=-1), dict(norm=None), dict(norm=Ep + 2), dict(mx=-1.0), dict(mx=float("nan")), dict(dt=(0, 3)),
+               dict(g=(0, Bp)), dict(g=(A + 1, Bp)), dict(g=(A, Bp + 2)), dict(o=(A, 0)), dict(o=(A, Bp + 2)),
+               dict(n=(16, 1 << 41)),
+               dict(g=(A, A), dt=(0, 0)),                       # one buffer twice
+               dict(g=(A, Bp), o=(Bp, A)),                      # written over another gradient
+               dict(o=(A + 16, Bp)), dict(o=(Cp, Cp)), dict(o=(Cp, Cp + 16), dt=(0, 0))):
+        assert clip(**kw) == INV, kw
+    assert clip(ws=None) == WS and clip(ws=0x90008) == WS and clip(wb=64) == WS
