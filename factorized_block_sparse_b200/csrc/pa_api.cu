@@ -1,18 +1,21 @@
 // C ABI of libpacked_attn.so (include/packed_attn.h): argument checks, the
 // device copies of a packing's tables, and the launches.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <new>
 
 #include "pa_internal.h"
+#include "pa_fwd.cuh"
 #include "pa_simple.cuh"
 
 namespace pa {
 namespace {
-
-__device__ int g_pa_status = 0;
 
 // Calls that a capture on another thread must not be broken by.
 struct RelaxedCapture {
@@ -23,7 +26,7 @@ struct RelaxedCapture {
 
 // The tables on the current device: found, or copied there (not inside a
 // capture of `s`, whose graph would hold an allocation that it cannot replay).
-int to_device(const pa_layout* L, cudaStream_t s, DeviceCopy* out) {
+int to_device(const pa_layout* L, cudaStream_t s, DeviceTables* out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SA_ERR_CUDA;
   std::lock_guard<std::mutex> g(L->mu);
@@ -41,7 +44,7 @@ int to_device(const pa_layout* L, cudaStream_t s, DeviceCopy* out) {
   for (auto* t : tabs) n += t->size();
   Slot* dptr = nullptr;
   if (cudaMalloc(reinterpret_cast<void**>(&dptr), (n ? n : 1) * sizeof(Slot)) != cudaSuccess) return SA_ERR_CUDA;
-  DeviceCopy d;
+  DeviceTables d;
   d.device = dev;
   d.blob = dptr;
   const Slot** fields[3] = {&d.fwd, &d.fwd2, &d.bwd};
@@ -108,6 +111,104 @@ View view(const pa_tensor* t) { return View{t->data, t->row_stride, t->head_stri
 
 int launched() { return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA; }
 
+// ------------------------------------------------------------ tensor maps
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+bool have_encode() {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return g_encode != nullptr;
+}
+
+// {D, heads, rows}, box: up to 64 columns of `box_rows` rows of one head.
+// `rows` ends with the last sequence, so nothing behind it is ever read.
+int map_rows(CUtensorMap* m, const pa_tensor* t, const Call& c, int heads, long long rows, int box_rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)c.D, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? t->head_stride : c.D) * 2,
+                                 (cuuint64_t)(c.rows > 1 ? t->row_stride : c.D) * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)std::min(c.D, 64), 1, (cuuint32_t)box_rows};
+  const cuuint32_t es[3] = {1, 1, 1};
+  const auto type = c.dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const auto swz = c.D >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  return g_encode(m, type, 3, t->data, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? SA_OK
+             : SA_ERR_CUDA;
+}
+
+constexpr int kMaxDevices = 64;
+
+// SMs of the current device (asked once a device).
+int sm_count(int* out) {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SA_ERR_CUDA;
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return SA_ERR_CUDA;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  *out = n;
+  return SA_OK;
+}
+
+// Allows a kernel its dynamic shared memory (once a kernel and device).
+template <auto Kernel, int Bytes>
+int allow_smem() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SA_ERR_CUDA;
+  if ((done.load(std::memory_order_acquire) >> dev) & 1u) return SA_OK;
+  if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Bytes) != cudaSuccess) return SA_ERR_CUDA;
+  done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+  return SA_OK;
+}
+
+template <typename T, int D>
+int run_fwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, const pa_tensor* o, float* lse,
+            int64_t ls, const pa_layout* L, const DeviceTables& dc) {
+  CUtensorMap mq, mk, mv;
+  int st, sms;
+  if ((st = map_rows(&mq, q, c, c.Hq, L->rows, kTile)) || (st = map_rows(&mk, k, c, c.Hkv, L->rows, kTile)) ||
+      (st = map_rows(&mv, v, c, c.Hkv, L->rows, kTile)) || (st = sm_count(&sms)) ||
+      (st = allow_smem<pa_fwd_kernel<T, D>, FwdCfg<D>::SMEM>()))
+    return st;
+  FwdArgs a;
+  a.G = c.Hq / c.Hkv;
+  a.o = view(o);
+  a.lse = lse;
+  a.ls = ls;
+  a.scale_log2 = static_cast<float>(static_cast<double>(c.scale) * 1.4426950408889634);
+  const long long tiles = static_cast<long long>(L->fwd.size());
+  long long items;
+  if (tiles * c.Hq <= sms) {  // a CTA for every tile: nothing to pair
+    a.pairing = kSingle;
+    a.slots = dc.fwd;
+    a.heads = c.Hq;
+    items = tiles * c.Hq;
+  } else if (a.G % 2 == 0) {
+    a.pairing = kHeads;
+    a.slots = dc.fwd;
+    a.heads = c.Hq / 2;
+    items = tiles * a.heads;
+  } else {
+    a.pairing = kTiles;
+    a.slots = dc.fwd2;
+    a.heads = c.Hq;
+    items = static_cast<long long>(L->fwd2.size()) * a.heads;
+  }
+  if (items > (1ll << 30)) return SA_ERR_UNSUPPORTED;  // item numbers stay in 31 bits
+  a.n_items = static_cast<int>(items);
+  pa_fwd_kernel<T, D><<<std::min(a.n_items, sms), FwdCfg<D>::THREADS, FwdCfg<D>::SMEM, c.s>>>(mq, mk, mv, a);
+  return launched();
+}
+
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
 template <typename F>
@@ -144,7 +245,7 @@ void packed_attn_layout_free(pa_layout* L) {
 
 int packed_attn_layout_upload(const pa_layout* L, void* stream) {
   if (!L) return SA_ERR_INVALID_ARG;
-  DeviceCopy dc;
+  DeviceTables dc;
   return to_device(L, static_cast<cudaStream_t>(stream), &dc);
 }
 
@@ -158,12 +259,11 @@ int packed_attn_fwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, 
   if (!tensor_ok(q, c, Hq) || !tensor_ok(k, c, Hkv) || !tensor_ok(v, c, Hkv) || !output_ok(o, c, Hq) || !lse ||
       lse_stride < rows || o->data == q->data || o->data == k->data || o->data == v->data)
     return SA_ERR_INVALID_ARG;
-  DeviceCopy dc;
+  if (!have_encode()) return SA_ERR_CUDA;
+  DeviceTables dc;
   if ((st = to_device(L, c.s, &dc))) return st;
   return dispatch(c, [&](auto t, auto d) -> int {
-    simple_fwd_kernel<decltype(t), d.value><<<dim3(L->fwd.size(), Hq), 512, 0, c.s>>>(
-        dc.fwd, view(q), view(k), view(v), view(o), lse, lse_stride, Hq / Hkv, scale);
-    return launched();
+    return run_fwd<decltype(t), d.value>(c, q, k, v, o, lse, lse_stride, L, dc);
   });
 }
 
@@ -195,7 +295,7 @@ int packed_attn_bwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, 
   }
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < packed_attn_bwd_workspace_size(Hq, Hkv, D, L))
     return SA_ERR_WORKSPACE;
-  DeviceCopy dc;
+  DeviceTables dc;
   if ((st = to_device(L, c.s, &dc))) return st;
   float* delta = static_cast<float*>(ws);
   return dispatch(c, [&](auto t, auto d) -> int {
@@ -215,10 +315,10 @@ int packed_attn_status(void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(s) != cudaSuccess) return SA_ERR_CUDA;
   int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_pa_status, sizeof(int)) != cudaSuccess) return SA_ERR_CUDA;
+  if (cudaMemcpyFromSymbol(&v, sa::g_status, sizeof(int)) != cudaSuccess) return SA_ERR_CUDA;
   if (v != 0) {
     const int zero = 0;
-    cudaMemcpyToSymbol(g_pa_status, &zero, sizeof(int));
+    cudaMemcpyToSymbol(sa::g_status, &zero, sizeof(int));
     return v;
   }
   return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;

@@ -1,0 +1,131 @@
+// Device helpers shared by the packed attention kernels: element types,
+// operand descriptors of 128-row tiles, the diagonal mask.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "pa_internal.h"
+#include "sa_device.cuh"
+
+namespace pa {
+
+using namespace sa;  // mbarrier, TMA, tcgen05 and fp32-pair helpers
+
+// Rows of a tensor: first element, distance of rows and heads in elements.
+struct View {
+  const void* p;
+  long long rs, hs;
+};
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<__nv_bfloat16> {
+  static constexpr uint32_t kFormat = 1;  // instruction descriptor: bf16
+  static constexpr float kBias = 0.f;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16(lo, hi); }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+  }
+};
+template <>
+struct Elem<__half> {
+  static constexpr uint32_t kFormat = 0;  // f16
+  // The forward's P is at most 2^8 (its running maximum trails by up to 8 in
+  // the exponent); 2^7 on top keeps it below fp16's 2^16 and moves the
+  // subnormals, which lose relative precision, from 2^-14 down to 2^-21 of
+  // the row's largest weight.  The factor cancels in o = sum P v / sum P.
+  static constexpr float kBias = 7.f;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+};
+
+// Instruction descriptor, kind::f16, float32 accumulator (make_idesc_bf16 with the element type).
+template <typename T>
+__host__ __device__ constexpr uint32_t make_idesc(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (Elem<T>::kFormat << 7) | (Elem<T>::kFormat << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// A tile of 128 rows of D elements in shared memory: panels of up to 64
+// columns, a row of a panel 128 (D = 32: 64) bytes, swizzled over its width.
+template <int D>
+struct TileGeo {
+  static constexpr int ROWB = D >= 64 ? 128 : 64;
+  static constexpr int PANELS = D >= 64 ? D / 64 : 1;
+  static constexpr int BOXW = D >= 64 ? 64 : D;
+  static constexpr uint64_t SWZ = D >= 64 ? kSwizzle128 : kSwizzle64;
+  static constexpr int PANEL_BYTES = kTile * ROWB;
+  static constexpr int BYTES = kTile * D * 2;
+  // the rows as M or N, k-step kk = 16 of the D columns
+  static __device__ __forceinline__ uint64_t kmajor(uint32_t base, int kk) {
+    constexpr int spp = ROWB / 32;
+    return make_desc(base + (kk / spp) * PANEL_BYTES + (kk % spp) * 32, 16, 8 * ROWB, SWZ);
+  }
+  // the D columns as N, k-step kk = 16 rows
+  static __device__ __forceinline__ uint64_t mnmajor(uint32_t base, int kk) {
+    return make_desc(base + kk * 16 * ROWB, PANEL_BYTES, 8 * ROWB, SWZ);
+  }
+};
+
+// The 128 rows from `row` of head h (rows past the tensor's end read as zero).
+template <int D>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int h, int row) {
+  using G = TileGeo<D>;
+#pragma unroll
+  for (int p = 0; p < G::PANELS; ++p) tma_load_3d(dst + p * G::PANEL_BYTES, m, bar, p * 64, h, row);
+}
+
+// Zeroes rows [r0, 128) of a tile, by a whole warp: rows that a TMA box took
+// from the next sequence must not meet a weight of zero (0 * NaN).
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int lane) {
+  using G = TileGeo<D>;
+#pragma unroll
+  for (int p = 0; p < G::PANELS; ++p)
+    for (int i = r0 * G::ROWB + lane * 16; i < kTile * G::ROWB; i += 32 * 16)
+      *reinterpret_cast<uint4*>(tile + p * G::PANEL_BYTES + i) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// 32 lanes x 32 bit, 32 consecutive columns: thread t gets lane (base + t).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Keeps v[i] for i <= last (i in [0, 32)), sets the others to `fill`.
+__device__ __forceinline__ void mask_after32(float* v, int last, float fill) {
+  const uint32_t m = last < 0 ? 0u : (last >= 31 ? 0xffffffffu : ((2u << last) - 1u));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = ((m >> i) & 1u) ? v[i] : fill;
+}
+
+// Item k of a CTA's share: rounds alternate direction, so that long and short
+// items pair up (the slots are sorted longest first).
+__device__ __forceinline__ int zigzag(int k, int cta, int n_ctas) {
+  return k * n_ctas + ((k & 1) ? (n_ctas - 1 - cta) : cta);
+}
+
+}  // namespace pa

@@ -1,0 +1,363 @@
+// Forward kernel of packed causal attention on tcgen05.
+//
+// Persistent: each CTA walks a zig-zag share of the items, longest first.  An
+// item is two units of 128 query rows that share their K/V tiles: two query
+// heads of one K/V head (same rows), or two neighbouring row tiles of one
+// head.  Per key tile of 128 and unit u
+//   S_u = Q_u K^T     both operands in shared memory, fp32 in TMEM
+//   P = 2^(S c - m)   one thread a row; running maximum and sum of the online
+//                     softmax in registers; P over the S columns, rounded
+//   O_u += P V        P read from TMEM, fp32 accumulator in TMEM
+// and o = O / sum at the end.  While one unit's softmax runs, the tensor core
+// works on the other unit.  The running maximum moves only when it grows by
+// more than 2^8, so O is rescaled rarely; numerator and denominator use the
+// same maximum, so the quotient is exact up to rounding.
+//
+// Roles (320 threads): warps 0..3 the softmax and epilogue of unit 0, warps
+// 4..7 of unit 1 (thread = query row = TMEM lane 32 (w mod 4) + lane), warp 8
+// lane 0 the TMA producer, warp 9 TMEM and the MMAs.  TMEM columns: S_u (and
+// P_u) at 128 u, O_u at 256 + D u.  Order makes three waits unnecessary: MMAs
+// of one thread execute in order, so S_u(j+1) after PV_u(j) cannot overwrite
+// a P_u(j) still being read, and the commit behind S_u(j+1) also says that O_u
+// holds PV_u(j), which is what a rescale needs.
+#pragma once
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+enum Pairing : int { kSingle = 0, kHeads = 1, kTiles = 2 };
+
+struct FwdArgs {
+  const Slot* slots;
+  int n_items, heads;  // items = slots x heads (head pairs where two heads make an item)
+  int pairing;
+  int G;               // query heads of a K/V head
+  View o;
+  float* lse;
+  long long ls;
+  float scale_log2;
+};
+
+template <int D>
+struct FwdCfg {
+  using G = TileGeo<D>;
+  static constexpr int STAGES = D >= 128 ? 4 : 6;  // K and V tiles in turn
+  static constexpr int STG_ROWB = G::ROWB;         // staging: 32 rows of up to 64 columns per warp
+  static constexpr int STG_BYTES = 32 * STG_ROWB;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_KV = 2 * G::BYTES;
+  static constexpr int OFF_STG = OFF_KV + STAGES * G::BYTES;
+  static constexpr int OFF_BAR = OFF_STG + 8 * STG_BYTES;
+  static constexpr int N_BARS = 2 + 2 + 2 * STAGES + 2 * 4 + 1;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
+  static constexpr int SMEM = OFF_MISC + 16;
+  static constexpr int COL_O = 256;
+  static constexpr int THREADS = 320;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// What an item is: its units' query tiles and heads.
+struct FwdItem {
+  Slot s;
+  int hk;
+  int n[2];   // key tiles of each unit (0: no such unit)
+  int qt[2];  // query tile in the sequence
+  int h[2];   // query head
+};
+
+__device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int item) {
+  FwdItem it;
+  const int slot = item / a.heads, hi = item - slot * a.heads;
+  it.s = a.slots[slot];
+  if (a.pairing == kTiles) {
+    it.h[0] = it.h[1] = hi;
+    it.qt[0] = 2 * it.s.tile;
+    it.qt[1] = it.qt[0] + 1;
+    it.n[0] = it.qt[0] + 1;
+    it.n[1] = it.qt[1] * kTile < it.s.len ? it.qt[1] + 1 : 0;
+  } else {
+    it.h[0] = a.pairing == kHeads ? 2 * hi : hi;
+    it.h[1] = it.h[0] + 1;
+    it.qt[0] = it.qt[1] = it.s.tile;
+    it.n[0] = it.s.tile + 1;
+    it.n[1] = a.pairing == kHeads ? it.n[0] : 0;
+  }
+  it.hk = it.h[0] / a.G;
+  return it;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(320, 1)
+    pa_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, const FwdArgs a) {
+  using C = FwdCfg<D>;
+  using G = TileGeo<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sKV = smem + C::OFF_KV;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* bar_q_full = bars;                        // [2]
+  uint64_t* bar_q_free = bars + 2;                    // [2]
+  uint64_t* bar_kv_full = bars + 4;                   // [STAGES]
+  uint64_t* bar_kv_free = bar_kv_full + C::STAGES;    // [STAGES]
+  uint64_t* bar_s_full = bar_kv_free + C::STAGES;     // [2] S of a tile (and PV of the tile before)
+  uint64_t* bar_p_full = bar_s_full + 2;              // [2] P of a tile
+  uint64_t* bar_o_full = bar_p_full + 2;              // [2] the item's last PV
+  uint64_t* bar_o_free = bar_o_full + 2;              // [2] the epilogue has read O
+  uint64_t* bar_drain = bar_o_free + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x, n_ctas = gridDim.x;
+  if (threadIdx.x == 0) {
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(bar_q_full + u, 1);
+      mbar_init(bar_q_free + u, 1);
+      mbar_init(bar_s_full + u, 1);
+      mbar_init(bar_p_full + u, 128);
+      mbar_init(bar_o_full + u, 1);
+      mbar_init(bar_o_free + u, 128);
+    }
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(bar_kv_full + s, 1);
+      mbar_init(bar_kv_free + s, 1);
+    }
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) tmem_alloc<512>(tmem_slot);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 8) {
+    // -------------------------------------------------------------- producer
+    if (lane == 0) {
+      bool ok = true;
+      int ring = 0, nq[2] = {0, 0};
+      for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
+        const FwdItem it = fwd_item(a, item);
+        for (int u = 0; ok && u < 2; ++u) {
+          if (it.n[u] == 0) continue;
+          if (nq[u] > 0) ok = mbar_wait(bar_q_free + u, (nq[u] - 1) & 1, abort_flag);
+          if (!ok) break;
+          mbar_arrive_expect_tx(bar_q_full + u, G::BYTES);
+          load_tile<D>(sQ + u * G::BYTES, &mq, bar_q_full + u, it.h[u], it.s.start + it.qt[u] * kTile);
+          ++nq[u];
+        }
+        const int n = max(it.n[0], it.n[1]);
+        for (int j = 0; ok && j < 2 * n; ++j, ++ring) {  // K_0 V_0 K_1 V_1 ...
+          const int st = ring % C::STAGES;
+          if (ring >= C::STAGES && !mbar_wait(bar_kv_free + st, (ring / C::STAGES - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar_kv_full + st, G::BYTES);
+          load_tile<D>(sKV + st * G::BYTES, (j & 1) ? &mv : &mk, bar_kv_full + st, it.hk, it.s.start + (j >> 1) * kTile);
+        }
+      }
+      if (*(volatile int*)abort_flag) {  // no copy may land after the CTA has gone
+        for (int u = 0; u < 2; ++u)
+          if (nq[u] > 0) mbar_wait_drain(bar_q_full + u, (nq[u] - 1) & 1);
+        for (int h = ring > C::STAGES ? ring - C::STAGES : 0; h < ring; ++h)
+          mbar_wait_drain(bar_kv_full + h % C::STAGES, (h / C::STAGES) & 1);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ MMAs
+    constexpr uint32_t id_s = make_idesc<T>(128, 128, false, false);
+    constexpr uint32_t id_o = make_idesc<T>(128, D, false, true);
+    bool ok = true;
+    int ring = 0, nu[2] = {0, 0}, np[2] = {0, 0};  // K/V tiles, items and P tiles of each unit so far
+    const uint32_t q_base = smem_u32(sQ);
+    auto issue_s = [&](int u, int st) {
+      if (lane == 0) {
+        const uint32_t kb = smem_u32(sKV + st * G::BYTES);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16_ss(tmem + u * 128, G::kmajor(q_base + u * G::BYTES, kk), G::kmajor(kb, kk), id_s, kk > 0);
+        mma_commit(bar_s_full + u);
+      }
+      __syncwarp();
+    };
+    for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
+      const FwdItem it = fwd_item(a, item);
+      const int n = max(it.n[0], it.n[1]);
+      ok = mbar_wait(bar_kv_full + ring % C::STAGES, (ring / C::STAGES) & 1, abort_flag);
+      for (int u = 0; ok && u < 2; ++u)
+        if (it.n[u] > 0) {
+          ok = mbar_wait(bar_q_full + u, nu[u] & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(u, ring % C::STAGES);
+          if (it.n[u] == 1 && lane == 0) mma_commit(bar_q_free + u);
+        }
+      if (ok && lane == 0) mma_commit(bar_kv_free + ring % C::STAGES);
+      for (int j = 0; ok && j < n; ++j, ring += 2) {
+        const int sv = (ring + 1) % C::STAGES, sk = (ring + 2) % C::STAGES;
+        ok = mbar_wait(bar_kv_full + sv, ((ring + 1) / C::STAGES) & 1, abort_flag);
+        if (!ok) break;
+        const int tail = it.s.len - j * kTile;  // keys of this tile
+        if (tail < kTile) zero_rows<D>(sKV + sv * G::BYTES, tail, lane);
+        if (j + 1 < n) ok = mbar_wait(bar_kv_full + sk, ((ring + 2) / C::STAGES) & 1, abort_flag);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (!ok || j >= it.n[u]) continue;
+          ok = mbar_wait(bar_p_full + u, np[u] & 1, abort_flag);
+          if (ok && j == 0 && nu[u] > 0) ok = mbar_wait(bar_o_free + u, (nu[u] - 1) & 1, abort_flag);
+          if (!ok) break;
+          ++np[u];
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t vb = smem_u32(sKV + sv * G::BYTES);
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_bf16_ts(tmem + C::COL_O + u * D, tmem + u * 128 + kk * 8, G::mnmajor(vb, kk), id_o, (j > 0 || kk > 0));
+            if (j + 1 == it.n[u]) mma_commit(bar_o_full + u);
+          }
+          __syncwarp();
+          if (j + 1 < it.n[u]) {
+            issue_s(u, sk);
+            if (j + 2 == it.n[u] && lane == 0) mma_commit(bar_q_free + u);
+          }
+        }
+        if (ok && lane == 0) {
+          mma_commit(bar_kv_free + sv);
+          if (j + 1 < n) mma_commit(bar_kv_free + sk);
+        }
+      }
+      for (int u = 0; u < 2; ++u) nu[u] += it.n[u] > 0;
+    }
+    if (lane == 0) {  // every MMA has completed before TMEM is released
+      mma_commit(bar_drain);
+      mbar_wait_drain(bar_drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------- softmax, epilogue
+    const int u = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + u * 128, t_o = tmem + lane_base + C::COL_O + u * D;
+    uint8_t* stg = smem + C::OFF_STG + warp * C::STG_BYTES;
+    bool ok = true;
+    int ns = 0, nu = 0;
+    for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
+      const FwdItem it = fwd_item(a, item);
+      const int n = it.n[u];
+      if (n == 0) continue;
+      float m_used = -INFINITY, l_sum = 0.f;
+      for (int j = 0; j < n; ++j, ++ns) {
+        ok = ok && mbar_wait(bar_s_full + u, ns & 1, abort_flag);
+        tc_fence_after();
+        float s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, s + c * 32);
+        tmem_wait_ld();
+        if (j + 1 == n) {  // the diagonal tile: keys up to the row itself
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mask_after32(s + c * 32, row - c * 32, -INFINITY);
+        }
+        float mx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx[i] = s[i];
+#pragma unroll
+        for (int i = 8; i < 128; i += 16)
+#pragma unroll
+          for (int x = 0; x < 8; ++x) mx[x] = i + 8 + x < 128 ? max3(mx[x], s[i + x], s[i + 8 + x]) : fmaxf(mx[x], s[i + x]);
+        const float m_tile = a.scale_log2 * max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+        float factor = 1.f;
+        if (m_tile > m_used + 8.f) {
+          factor = ex2(m_used - m_tile);  // 0 for the first tile
+          m_used = m_tile;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, factor != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            float ov[16];
+            tmem_ld16(t_o + i * 16, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) ov[x] *= factor;
+            tmem_st16(t_o + i * 16, ov);
+          }
+        }
+        const float neg = Elem<T>::kBias - m_used;
+        const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), ng2 = f2_pack(neg, neg);
+        uint64_t rs[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = f2_unpack(f2_fma(f2_pack(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc2, ng2));
+            const float p0 = ex2(e.x), p1 = ex2(e.y);
+            rs[i & 3] = f2_add(rs[i & 3], f2_pack(p0, p1));
+            pk[i] = Elem<T>::pack(p0, p1);
+          }
+          tmem_st8(t_s + c * 16, pk);
+          tmem_st8(t_s + c * 16 + 8, pk + 8);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar_p_full + u);
+        const float2 r0 = f2_unpack(f2_add(f2_add(rs[0], rs[1]), f2_add(rs[2], rs[3])));
+        l_sum = l_sum * factor + (r0.x + r0.y);
+      }
+      // ------------------------------------------------------------ epilogue
+      ok = ok && mbar_wait(bar_o_full + u, nu & 1, abort_flag);
+      ++nu;
+      tc_fence_after();
+      const float inv = 1.f / l_sum;
+      const int r0 = it.qt[u] * kTile + quarter * 32;  // the warp's first row in the sequence
+      const long long row0 = static_cast<long long>(it.s.start) + r0;
+      const int rows = min(32, it.s.len - r0);
+      T* out = static_cast<T*>(const_cast<void*>(a.o.p)) + row0 * a.o.rs + static_cast<long long>(it.h[u]) * a.o.hs;
+      constexpr int CHUNKS = C::STG_ROWB / 16;  // 16-byte chunks of a staged row
+#pragma unroll
+      for (int p = 0; p < G::PANELS; ++p) {
+#pragma unroll
+        for (int i = 0; i < G::BOXW / 16; ++i) {
+          float ov[16];
+          tmem_ld16(t_o + p * 64 + i * 16, ov);
+          tmem_wait_ld();
+          if (p == G::PANELS - 1 && i == G::BOXW / 16 - 1) {
+            tc_fence_before();
+            mbar_arrive(bar_o_free + u);
+          }
+          uint32_t w[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) w[x] = Elem<T>::pack(ov[2 * x] * inv, ov[2 * x + 1] * inv);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            *reinterpret_cast<uint4*>(stg + lane * C::STG_ROWB + (((2 * i + x) ^ (lane & (CHUNKS - 1))) << 4)) =
+                make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+        }
+        __syncwarp();
+        // whole rows leave together: CHUNKS lanes a row
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+          const int r = i * (32 / CHUNKS) + lane / CHUNKS, c = lane % CHUNKS;
+          if (r < rows)
+            *reinterpret_cast<uint4*>(out + r * a.o.rs + p * 64 + c * 8) =
+                *reinterpret_cast<const uint4*>(stg + r * C::STG_ROWB + ((c ^ (r & (CHUNKS - 1))) << 4));
+        }
+        __syncwarp();
+      }
+      if (lane < rows)
+        a.lse[static_cast<long long>(it.h[u]) * a.ls + row0 + lane] =
+            (m_used + lg2(l_sum) - Elem<T>::kBias) * 0.6931471805599453f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc<512>(tmem);
+  }
+}
+
+}  // namespace pa

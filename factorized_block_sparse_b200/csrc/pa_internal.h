@@ -20,7 +20,7 @@ struct Slot {
   int32_t base;   // index of the sequence's first 128-row tile among all of them
 };
 
-struct DeviceCopy {
+struct DeviceTables {
   int device = -1;
   void* blob = nullptr;
   const Slot* fwd = nullptr;   // 128-row query tiles, longest key range first
@@ -36,5 +36,5 @@ struct pa_layout {
   std::vector<int32_t> lengths;
   std::vector<pa::Slot> fwd, fwd2, bwd;
   mutable std::mutex mu;
-  mutable std::vector<pa::DeviceCopy> dev;
+  mutable std::vector<pa::DeviceTables> dev;
 };

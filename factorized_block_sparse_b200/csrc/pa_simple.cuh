@@ -2,17 +2,9 @@
 // the formulas of include/packed_attn.h.
 #pragma once
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "pa_internal.h"
+#include "pa_device.cuh"
 
 namespace pa {
-
-struct View {
-  const void* p;
-  long long rs, hs;
-};
 
 template <typename T>
 __device__ __forceinline__ float to_f(T x) {
@@ -44,33 +36,6 @@ __device__ __forceinline__ float row_dot(const float* a, const float* b) {
 #pragma unroll
   for (int u = 0; u < D / 32; ++u) s += a[u] * b[u];
   return warp_sum(s);
-}
-
-// gridDim.x: slots, gridDim.y: query heads; a warp per row of the slot's tile.
-template <typename T, int D>
-__global__ void simple_fwd_kernel(const Slot* slots, View q, View k, View v, View o, float* lse, long long ls, int G,
-                                  float scale) {
-  const Slot s = slots[blockIdx.x];
-  const int h = blockIdx.y, lane = threadIdx.x & 31;
-  for (int r = threadIdx.x >> 5; r < kTile; r += blockDim.x >> 5) {
-    const int i = s.tile * kTile + r;
-    if (i >= s.len) break;
-    float qr[D / 32], acc[D / 32] = {}, m = -INFINITY, l = 0.f;
-    row_in<T, D>(qr, q, (long long)s.start + i, h, lane);
-    for (int j = 0; j <= i; ++j) {
-      float kr[D / 32], vr[D / 32];
-      row_in<T, D>(kr, k, (long long)s.start + j, h / G, lane);
-      row_in<T, D>(vr, v, (long long)s.start + j, h / G, lane);
-      const float x = row_dot<D>(qr, kr) * scale, mn = fmaxf(m, x);
-      const float f = __expf(m - mn), p = __expf(x - mn);
-      l = l * f + p;
-#pragma unroll
-      for (int u = 0; u < D / 32; ++u) acc[u] = acc[u] * f + p * vr[u];
-      m = mn;
-    }
-    row_out<T, D>(acc, o, (long long)s.start + i, h, lane, 1.f / l);
-    if (lane == 0) lse[h * ls + s.start + i] = m + logf(l);
-  }
 }
 
 // delta_i = <dO_i, o_i>, [Hq][rows].

@@ -43,6 +43,13 @@ CASES = [
     ([257, 3, 128], 6, 3, 32, torch.float16),
     ([1] * 40 + [2] * 30, 4, 2, 64, torch.bfloat16),
     ([512, 640], 16, 2, 128, torch.bfloat16),
+    # more tiles x heads than SMs: query heads or row tiles of an item in pairs
+    ([130, 300, 77] * 6, 8, 4, 128, torch.bfloat16),
+    ([130, 257, 300, 128, 1] * 3, 9, 3, 64, torch.float16),
+    ([385, 100] * 5, 10, 10, 128, torch.float16),
+    ([600, 1, 513], 24, 2, 64, torch.bfloat16),
+    ([129, 384] * 6, 6, 6, 32, torch.bfloat16),
+    ([700] * 3, 12, 6, 32, torch.float16),
 ]
 
 
