@@ -98,7 +98,7 @@ def build_block_lib(force=False, verbose=False):
 PACKED_LIB = os.path.join(HERE, "libpacked_attn.so")
 PACKED_SOURCES = [os.path.join(HERE, "csrc", f) for f in ("pa_api.cu", "pa_layout.cpp")]
 PACKED_HEADERS = [os.path.join(ROOT, "include", f) for f in ("packed_attn.h", "sparse_attn.h")] + [
-    os.path.join(HERE, "csrc", f) for f in ("pa_internal.h", "pa_device.cuh", "pa_fwd.cuh", "pa_simple.cuh", "sa_device.cuh", "sa_internal.h")]
+    os.path.join(HERE, "csrc", f) for f in ("pa_internal.h", "pa_device.cuh", "pa_fwd.cuh", "pa_bwd.cuh", "sa_device.cuh", "sa_internal.h")]
 
 
 def build_packed_lib(force=False, verbose=False, extra=()):

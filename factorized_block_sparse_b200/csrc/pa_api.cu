@@ -9,10 +9,11 @@
 #include <cmath>
 #include <cstring>
 #include <new>
+#include <type_traits>
 
 #include "pa_internal.h"
+#include "pa_bwd.cuh"
 #include "pa_fwd.cuh"
-#include "pa_simple.cuh"
 
 namespace pa {
 namespace {
@@ -211,6 +212,51 @@ int run_fwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tens
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
+// Workspace of the backward pass: packed lse and delta, then the dq sums.
+struct BwdWs {
+  size_t dq, total;
+};
+BwdWs bwd_ws(int Hq, int D, const pa_layout* L) {
+  const size_t tiles = static_cast<size_t>(Hq) * L->fwd.size();
+  BwdWs w;
+  w.dq = align256(tiles * 2 * kTile * sizeof(float));
+  w.total = w.dq + align256(tiles * kTile * D * sizeof(float)) + 256;
+  return w;
+}
+
+template <typename T, int D>
+int run_bwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, const pa_tensor* o,
+            const float* lse, int64_t ls, const pa_tensor* dO, const pa_tensor* dq, const pa_tensor* dk,
+            const pa_tensor* dv, const pa_layout* L, const DeviceTables& dc, void* ws) {
+  CUtensorMap mq, mk, mv, mdo;
+  int st, sms;
+  if ((st = map_rows(&mq, q, c, c.Hq, L->rows, kTile)) || (st = map_rows(&mk, k, c, c.Hkv, L->rows, kTile)) ||
+      (st = map_rows(&mv, v, c, c.Hkv, L->rows, kTile)) || (st = map_rows(&mdo, dO, c, c.Hq, L->rows, kTile)) ||
+      (st = sm_count(&sms)) || (st = allow_smem<pa_bwd_kernel<T, D>, BwdCfg<D>::SMEM>()))
+    return st;
+  const BwdWs w = bwd_ws(c.Hq, D, L);
+  float* ld = static_cast<float*>(ws);
+  float* sum = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.dq);
+  const unsigned tiles = static_cast<unsigned>(L->fwd.size());
+  if (static_cast<long long>(tiles) * c.Hkv > (1ll << 30)) return SA_ERR_UNSUPPORTED;  // item numbers stay in 31 bits
+  BwdArgs a;
+  a.slots = dc.bwd;
+  a.Hkv = c.Hkv;
+  a.G = c.Hq / c.Hkv;
+  a.n_items = static_cast<int>(tiles) * c.Hkv;
+  a.n_tiles = static_cast<int>(tiles);
+  a.ld = ld;
+  a.dq_sum = sum;
+  a.dk = view(dk);
+  a.dv = view(dv);
+  a.scale = c.scale;
+  a.scale_log2 = static_cast<float>(static_cast<double>(c.scale) * 1.4426950408889634);
+  pa_bwd_pre_kernel<T, D><<<dim3(tiles, c.Hq), 256, 0, c.s>>>(dc.fwd, view(o), view(dO), lse, ls, ld, sum, a.n_tiles);
+  pa_bwd_kernel<T, D><<<std::min(a.n_items, sms), BwdCfg<D>::THREADS, BwdCfg<D>::SMEM, c.s>>>(mq, mk, mv, mdo, a);
+  pa_bwd_dq_kernel<T, D><<<dim3(tiles, c.Hq), 256, 0, c.s>>>(dc.fwd, sum, view(dq), a.n_tiles, c.scale);
+  return launched();
+}
+
 template <typename F>
 int dispatch(const Call& c, F&& f) {
   auto by_d = [&](auto t) -> int {
@@ -270,7 +316,7 @@ int packed_attn_fwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, 
 size_t packed_attn_bwd_workspace_size(int Hq, int Hkv, int D, const pa_layout* L) {
   const Call c{L ? static_cast<long long>(L->rows) : 0, Hq, Hkv, D, PA_BF16, 1.f, nullptr};
   if (check_call(c, L)) return 0;
-  return align256(static_cast<size_t>(Hq) * L->rows * sizeof(float)) + 256;
+  return bwd_ws(Hq, D, L).total;
 }
 
 int packed_attn_bwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, const pa_tensor* o, const float* lse,
@@ -297,17 +343,8 @@ int packed_attn_bwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, 
     return SA_ERR_WORKSPACE;
   DeviceTables dc;
   if ((st = to_device(L, c.s, &dc))) return st;
-  float* delta = static_cast<float*>(ws);
   return dispatch(c, [&](auto t, auto d) -> int {
-    using T = decltype(t);
-    constexpr int DD = d.value;
-    const int G = Hq / Hkv;
-    simple_delta_kernel<T, DD><<<dim3((L->rows + 7) / 8, Hq), 256, 0, c.s>>>(view(o), view(dO), delta, L->rows);
-    simple_dq_kernel<T, DD><<<dim3(L->fwd.size(), Hq), 512, 0, c.s>>>(dc.fwd, view(q), view(k), view(v), view(dO),
-                                                                      view(dq), lse, lse_stride, delta, L->rows, G, scale);
-    simple_dkv_kernel<T, DD><<<dim3(L->bwd.size(), Hkv), 512, 0, c.s>>>(
-        dc.bwd, view(q), view(k), view(v), view(dO), view(dk), view(dv), lse, lse_stride, delta, L->rows, G, scale);
-    return launched();
+    return run_bwd<decltype(t), d.value>(c, q, k, v, o, lse, lse_stride, dO, dq, dk, dv, L, dc, ws);
   });
 }
 
