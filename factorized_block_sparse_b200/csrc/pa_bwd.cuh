@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(448, 1)
       const int kb = ni % C::KVB;
       uint8_t* sK = smem + C::OFF_K + kb * G::BYTES;
       uint8_t* sV = smem + C::OFF_V + kb * G::BYTES;
-      const uint32_t k_base = smem_u32(sK), v_base = smem_u32(sV);
+      const Desc k_k = G::kmajor(smem_u32(sK)), k_mn = G::mnmajor(smem_u32(sK)), v_k = G::kmajor(smem_u32(sV));
       ok = mbar_wait(bar_kv_full + kb, (ni / C::KVB) & 1, abort_flag);
       if (!ok) break;
       const int keys = it.s.len - it.s.tile * kTile;
@@ -272,11 +272,11 @@ __global__ void __launch_bounds__(448, 1)
         const int rows = it.s.len - (it.s.tile + j % it.per) * kTile;
         if (rows < kTile) zero_rows<D>(sQ, rows, lane);
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t q_base = smem_u32(sQ);
+        const Desc q_k = G::kmajor(smem_u32(sQ));
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16_ss(tmem + C::COL_S, G::kmajor(k_base, kk), G::kmajor(q_base, kk), id_s, kk > 0);
+            mma_bf16_ss(tmem + C::COL_S, k_k.at(G::kstep(kk)), q_k.at(G::kstep(kk)), id_s, kk > 0);
           mma_commit(bar_s_full);
         }
         __syncwarp();
@@ -291,11 +291,11 @@ __global__ void __launch_bounds__(448, 1)
         const int rows = it.s.len - (it.s.tile + j % it.per) * kTile;
         if (rows < kTile) zero_rows<D>(sDO, rows, lane);
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t do_base = smem_u32(sDO);
+        const Desc do_k = G::kmajor(smem_u32(sDO));
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16_ss(tmem + C::COL_DP, G::kmajor(v_base, kk), G::kmajor(do_base, kk), id_s, kk > 0);
+            mma_bf16_ss(tmem + C::COL_DP, v_k.at(G::kstep(kk)), do_k.at(G::kstep(kk)), id_s, kk > 0);
           mma_commit(bar_dp_full);
         }
         __syncwarp();
@@ -308,11 +308,11 @@ __global__ void __launch_bounds__(448, 1)
         if (ok && j == 0 && ni > 0) ok = mbar_wait(bar_dkv_free, (ni - 1) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t do_base = smem_u32(smem + C::OFF_DO + st * G::BYTES);
+        const Desc do_mn = G::mnmajor(smem_u32(smem + C::OFF_DO) + st * G::BYTES);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)  // 16 queries of P^T = 8 TMEM columns; each group's half begins at its S^T columns
-            mma_bf16_ts(tmem + C::COL_DV, tmem + C::COL_S + (kk / 4) * 64 + (kk % 4) * 8, G::mnmajor(do_base, kk), id_kv,
+            mma_bf16_ts(tmem + C::COL_DV, tmem + C::COL_S + (kk / 4) * 64 + (kk % 4) * 8, do_mn.at(G::mnstep(kk)), id_kv,
                         j > 0 || kk > 0);
           mma_commit(bar_do_free + st);
         }
@@ -323,31 +323,31 @@ __global__ void __launch_bounds__(448, 1)
         const int qb = g % C::NDQ;
         if (D < 128 && g >= C::NDQ && !(ok = mbar_wait(bar_dq_free + qb, (g / C::NDQ - 1) & 1, abort_flag))) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t ds_base = smem_u32(smem + C::OFF_DS + (g % C::NDS) * C::DS_BYTES);
-          const uint32_t q_base = smem_u32(smem + C::OFF_Q + st * G::BYTES);
+        // dS as queries x keys (M over two panels, 16 keys a k-step) and dS^T as keys x queries
+        const uint32_t ds_base = smem_u32(smem + C::OFF_DS) + (g % C::NDS) * C::DS_BYTES;
+        const Desc ds_mn(ds_base, kTile * 128, 1024, kSwizzle128), ds_k(ds_base, 16, 1024, kSwizzle128);
+        const Desc q_mn = G::mnmajor(smem_u32(smem + C::OFF_Q) + st * G::BYTES);
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)  // dS: queries as M (two panels), 16 keys a step
-            mma_bf16_ss(tmem + C::COL_DQ + qb * D, make_desc(ds_base + kk * 2048, kTile * 128, 1024, kSwizzle128),
-                        G::mnmajor(k_base, kk), id_q, kk > 0);
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_bf16_ss(tmem + C::COL_DQ + qb * D, ds_mn.at(kk * 2048), k_mn.at(G::mnstep(kk)), id_q, kk > 0);
           mma_commit(bar_dq_full + qb);
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)  // dS^T: keys as M, 16 queries a step
-            mma_bf16_ss(tmem + C::COL_DK,
-                        make_desc(ds_base + (kk / 4) * kTile * 128 + (kk % 4) * 32, 16, 1024, kSwizzle128),
-                        G::mnmajor(q_base, kk), id_kv, j > 0 || kk > 0);
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_bf16_ss(tmem + C::COL_DK, ds_k.at((kk / 4) * kTile * 128 + (kk % 4) * 32), q_mn.at(G::mnstep(kk)), id_kv,
+                        j > 0 || kk > 0);
           mma_commit(bar_q_free + st);
           mma_commit(bar_ds_free + g % C::NDS);
         }
         __syncwarp();
         if (D >= 128 && j + 1 < it.n) ok = issue_dp(j + 1, g + 1);
       }
-      if (ok && lane == 0) {
+      if (ok && elect_one()) {
         mma_commit(bar_kv_free + kb);
         mma_commit(bar_dkv_full);
       }
     }
-    if (lane == 0) {  // every MMA has completed before TMEM is released
+    if (elect_one()) {  // every MMA has completed before TMEM is released
       mma_commit(bar_drain);
       mbar_wait_drain(bar_drain, 0);
     }

@@ -53,6 +53,29 @@ __host__ __device__ constexpr uint32_t make_idesc(int M, int N, bool a_mn, bool 
          ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// A shared-memory matrix descriptor (fields as make_desc) as two words: a
+// k-step is one 32-bit addition to the low word.  One thread issues every MMA
+// of a CTA, and what it spends between two of them is time the tensor core
+// waits, so the descriptors are built once per operand and not per MMA.
+struct Desc {
+  uint32_t lo, hi;
+  __device__ __forceinline__ Desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint64_t swz)
+      : lo(((saddr >> 4) & 0x3FFF) | ((lbo >> 4) << 16)),
+        hi((sbo >> 4) | (1u << 14) | (static_cast<uint32_t>(swz) << 29)) {}
+  __device__ __forceinline__ uint64_t at(uint32_t bytes) const {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo + (bytes >> 4)), "r"(hi));
+    return d;
+  }
+};
+
+// One thread of the (converged) warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // A tile of 128 rows of D elements in shared memory: panels of up to 64
 // columns, a row of a panel 128 (D = 32: 64) bytes, swizzled over its width.
 template <int D>
@@ -63,15 +86,13 @@ struct TileGeo {
   static constexpr uint64_t SWZ = D >= 64 ? kSwizzle128 : kSwizzle64;
   static constexpr int PANEL_BYTES = kTile * ROWB;
   static constexpr int BYTES = kTile * D * 2;
-  // the rows as M or N, k-step kk = 16 of the D columns
-  static __device__ __forceinline__ uint64_t kmajor(uint32_t base, int kk) {
-    constexpr int spp = ROWB / 32;
-    return make_desc(base + (kk / spp) * PANEL_BYTES + (kk % spp) * 32, 16, 8 * ROWB, SWZ);
-  }
-  // the D columns as N, k-step kk = 16 rows
-  static __device__ __forceinline__ uint64_t mnmajor(uint32_t base, int kk) {
-    return make_desc(base + kk * 16 * ROWB, PANEL_BYTES, 8 * ROWB, SWZ);
-  }
+  // Operands of a tile at shared address `base`: the rows as M or N with the
+  // D columns as K, and the D columns as N with the rows as K.
+  static __device__ __forceinline__ Desc kmajor(uint32_t base) { return Desc(base, 16, 8 * ROWB, SWZ); }
+  static __device__ __forceinline__ Desc mnmajor(uint32_t base) { return Desc(base, PANEL_BYTES, 8 * ROWB, SWZ); }
+  // byte offset of k-step kk (16 columns, 16 rows)
+  static __device__ constexpr uint32_t kstep(int kk) { return (kk / (ROWB / 32)) * PANEL_BYTES + (kk % (ROWB / 32)) * 32; }
+  static __device__ constexpr uint32_t mnstep(int kk) { return kk * 16 * ROWB; }
 };
 
 // The 128 rows from `row` of head h (rows past the tensor's end read as zero).

@@ -175,11 +175,11 @@ __global__ void __launch_bounds__(320, 1)
     int ring = 0, nu[2] = {0, 0}, np[2] = {0, 0};  // K/V tiles, items and P tiles of each unit so far
     const uint32_t q_base = smem_u32(sQ);
     auto issue_s = [&](int u, int st) {
-      if (lane == 0) {
-        const uint32_t kb = smem_u32(sKV + st * G::BYTES);
+      const Desc qd = G::kmajor(q_base + u * G::BYTES), kd = G::kmajor(smem_u32(sKV) + st * G::BYTES);
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16_ss(tmem + u * 128, G::kmajor(q_base + u * G::BYTES, kk), G::kmajor(kb, kk), id_s, kk > 0);
+          mma_bf16_ss(tmem + u * 128, qd.at(G::kstep(kk)), kd.at(G::kstep(kk)), id_s, kk > 0);
         mma_commit(bar_s_full + u);
       }
       __syncwarp();
@@ -194,9 +194,9 @@ __global__ void __launch_bounds__(320, 1)
           if (!ok) break;
           tc_fence_after();
           issue_s(u, ring % C::STAGES);
-          if (it.n[u] == 1 && lane == 0) mma_commit(bar_q_free + u);
+          if (it.n[u] == 1 && elect_one()) mma_commit(bar_q_free + u);
         }
-      if (ok && lane == 0) mma_commit(bar_kv_free + ring % C::STAGES);
+      if (ok && elect_one()) mma_commit(bar_kv_free + ring % C::STAGES);
       for (int j = 0; ok && j < n; ++j, ring += 2) {
         const int sv = (ring + 1) % C::STAGES, sk = (ring + 2) % C::STAGES;
         ok = mbar_wait(bar_kv_full + sv, ((ring + 1) / C::STAGES) & 1, abort_flag);
@@ -212,27 +212,27 @@ __global__ void __launch_bounds__(320, 1)
           if (!ok) break;
           ++np[u];
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t vb = smem_u32(sKV + sv * G::BYTES);
+          const Desc vd = G::mnmajor(smem_u32(sKV) + sv * G::BYTES);
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_bf16_ts(tmem + C::COL_O + u * D, tmem + u * 128 + kk * 8, G::mnmajor(vb, kk), id_o, (j > 0 || kk > 0));
+              mma_bf16_ts(tmem + C::COL_O + u * D, tmem + u * 128 + kk * 8, vd.at(G::mnstep(kk)), id_o, (j > 0 || kk > 0));
             if (j + 1 == it.n[u]) mma_commit(bar_o_full + u);
           }
           __syncwarp();
           if (j + 1 < it.n[u]) {
             issue_s(u, sk);
-            if (j + 2 == it.n[u] && lane == 0) mma_commit(bar_q_free + u);
+            if (j + 2 == it.n[u] && elect_one()) mma_commit(bar_q_free + u);
           }
         }
-        if (ok && lane == 0) {
+        if (ok && elect_one()) {
           mma_commit(bar_kv_free + sv);
           if (j + 1 < n) mma_commit(bar_kv_free + sk);
         }
       }
       for (int u = 0; u < 2; ++u) nu[u] += it.n[u] > 0;
     }
-    if (lane == 0) {  // every MMA has completed before TMEM is released
+    if (elect_one()) {  // every MMA has completed before TMEM is released
       mma_commit(bar_drain);
       mbar_wait_drain(bar_drain, 0);
     }
