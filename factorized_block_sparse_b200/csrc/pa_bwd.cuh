@@ -23,9 +23,9 @@
 // columns each), so dQ lands in the dP^T columns and the next dP^T waits for
 // its read-out, which dK covers.
 //
-// Roles (448 threads): warps 0..7 two compute groups (thread = key row, 64 of
-// the step's queries each), warps 8..11 read-out of dQ and of the item's dK,
-// dV, warp 12 lane 0 the TMA producer, warp 13 TMEM and the MMAs.
+// Roles (704 threads): warps 0..15 four compute groups (thread = key row, 32 of
+// the step's queries each), warps 16..19 read-out of dQ and of the item's dK,
+// dV, warp 20 lane 0 the TMA producer, warp 21 TMEM and the MMAs.
 #pragma once
 
 #include "pa_device.cuh"
@@ -63,7 +63,7 @@ struct BwdCfg {
   static constexpr int SMEM = OFF_MISC + 16;
   static constexpr int COL_S = 0, COL_DP = 128, COL_DV = 256, COL_DK = 256 + D;
   static constexpr int COL_DQ = D >= 128 ? COL_DP : 256 + 2 * D;  // + b * D
-  static constexpr int THREADS = 448;
+  static constexpr int COMPUTE = 512, THREADS = COMPUTE + 192;
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(256)
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(448, 1)
+__global__ void __launch_bounds__(704, 1)
     pa_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const BwdArgs a) {
   using C = BwdCfg<D>;
@@ -181,9 +181,9 @@ __global__ void __launch_bounds__(448, 1)
       mbar_init(bar_do_free + b, 1);
     }
     mbar_init(bar_s_full, 1);
-    mbar_init(bar_p_full, 256);
+    mbar_init(bar_p_full, C::COMPUTE);
     mbar_init(bar_dp_full, 1);
-    mbar_init(bar_ds_full, 256);
+    mbar_init(bar_ds_full, C::COMPUTE);
     for (int b = 0; b < C::NDS; ++b) mbar_init(bar_ds_free + b, 1);
     for (int b = 0; b < C::NDQ; ++b) {
       mbar_init(bar_dq_full + b, 1);
@@ -195,13 +195,13 @@ __global__ void __launch_bounds__(448, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 13) tmem_alloc<512>(tmem_slot);
+  if (warp == 21) tmem_alloc<512>(tmem_slot);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 12) {
+  if (warp == 20) {
     // -------------------------------------------------------------- producer
     if (lane == 0) {
       bool ok = true;
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(448, 1)
           mbar_wait_drain(bar_do_full + i % C::QST, (i / C::QST) & 1);
       }
     }
-  } else if (warp == 13) {
+  } else if (warp == 21) {
     // ------------------------------------------------------------------ MMAs
     constexpr uint32_t id_s = make_idesc<T>(128, 128, false, false);
     constexpr uint32_t id_kv = make_idesc<T>(128, D, false, true);
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(448, 1)
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)  // 16 queries of P^T = 8 TMEM columns; each group's half begins at its S^T columns
-            mma_bf16_ts(tmem + C::COL_DV, tmem + C::COL_S + (kk / 4) * 64 + (kk % 4) * 8, do_mn.at(G::mnstep(kk)), id_kv,
+            mma_bf16_ts(tmem + C::COL_DV, tmem + C::COL_S + (kk / 2) * 32 + (kk % 2) * 8, do_mn.at(G::mnstep(kk)), id_kv,
                         j > 0 || kk > 0);
           mma_commit(bar_do_free + st);
         }
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(448, 1)
       mbar_wait_drain(bar_drain, 0);
     }
     __syncwarp();
-  } else if (warp >= 8) {
+  } else if (warp >= 16) {
     // ------------------------------------------- read-out of dQ, dK and dV
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
@@ -411,26 +411,28 @@ __global__ void __launch_bounds__(448, 1)
     }
   } else {
     // ------------------------------------------------------ P^T and dS^T
-    const int w = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;  // w: which 64 queries
+    const int w = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;  // w: which 32 queries
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_s = tmem + lane_base + C::COL_S + w * 64, t_dp = tmem + lane_base + C::COL_DP + w * 64;
+    const uint32_t t_s = tmem + lane_base + C::COL_S + w * 32, t_dp = tmem + lane_base + C::COL_DP + w * 32;
     const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
+    const int first = row - w * 32;  // on the diagonal: the first query at or behind the key
+    const uint32_t behind = first <= 0 ? 0xffffffffu : (first >= 32 ? 0u : 0xffffffffu << first);
     bool ok = true;
     int g = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
       const BwdItem it = bwd_item(a, item);
-      for (int j = 0; ok && j < it.n; ++j, ++g) {
+      for (int j = 0, in_head = 0; ok && j < it.n; ++j, ++g) {
         const int st = g % C::QST;
-        const bool diag = j % it.per == 0;
-        const float* ld = reinterpret_cast<const float*>(smem + C::OFF_LD + st * C::LD_BYTES) + w * 64;
+        const bool diag = in_head == 0;
+        if (++in_head == it.per) in_head = 0;
+        const float* ld = reinterpret_cast<const float*>(smem + C::OFF_LD + st * C::LD_BYTES) + w * 32;
         ok = mbar_wait(bar_q_full + st, (g / C::QST) & 1, abort_flag) && mbar_wait(bar_s_full, g & 1, abort_flag);
         tc_fence_after();
-        float p[64];
+        float p[32];
         tmem_ld32(t_s, p);
-        tmem_ld32(t_s + 32, p + 32);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        for (int c = 0; c < 8; ++c) {
           const float4 l = *reinterpret_cast<const float4*>(ld + 4 * c);
           const float2 e0 = f2_unpack(f2_fma(f2_pack(p[4 * c], p[4 * c + 1]), sc2, f2_pack(l.x, l.y)));
           const float2 e1 = f2_unpack(f2_fma(f2_pack(p[4 * c + 2], p[4 * c + 3]), sc2, f2_pack(l.z, l.w)));
@@ -439,59 +441,48 @@ __global__ void __launch_bounds__(448, 1)
           p[4 * c + 2] = ex2(e1.x);
           p[4 * c + 3] = ex2(e1.y);
         }
-        uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;  // queries at or behind the key, of each 32
         if (diag) {
-          const int first = row - w * 64;
-          m0 = first <= 0 ? m0 : (first >= 32 ? 0u : m0 << first);
-          m1 = first <= 32 ? m1 : (first >= 64 ? 0u : m1 << (first - 32));
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            p[i] = ((m0 >> i) & 1u) ? p[i] : 0.f;
-            p[32 + i] = ((m1 >> i) & 1u) ? p[32 + i] : 0.f;
-          }
+          for (int i = 0; i < 32; ++i) p[i] = ((behind >> i) & 1u) ? p[i] : 0.f;
         }
+        {
+          uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) pk[i] = Elem<T>::pack(p[c * 16 + 2 * i] * kP, p[c * 16 + 2 * i + 1] * kP);
-          tmem_st8(t_s + c * 8, pk);
+          for (int i = 0; i < 16; ++i) pk[i] = Elem<T>::pack(p[2 * i] * kP, p[2 * i + 1] * kP);
+          tmem_st8(t_s, pk);
+          tmem_st8(t_s + 8, pk + 8);
         }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar_p_full);
 
         ok = ok && mbar_wait(bar_dp_full, g & 1, abort_flag);
-        if (g >= C::NDS) ok = ok && mbar_wait(bar_ds_free + g % C::NDS, (g / C::NDS - 1) & 1, abort_flag);
         tc_fence_after();
-        uint8_t* ds = smem + C::OFF_DS + (g % C::NDS) * C::DS_BYTES + w * kTile * 128;
+        float dp[32];
+        tmem_ld32(t_dp, dp);
+        tmem_wait_ld();
+        uint32_t pk[16];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float dp[32];
-          tmem_ld32(t_dp + hf * 32, dp);
-          tmem_wait_ld();
-          uint32_t pk[16];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float4 dl = *reinterpret_cast<const float4*>(ld + kTile + hf * 32 + 4 * c);
-            const float* pp = p + hf * 32 + 4 * c;
-            float s0 = pp[0] * (dp[4 * c] - dl.x), s1 = pp[1] * (dp[4 * c + 1] - dl.y);
-            float s2 = pp[2] * (dp[4 * c + 2] - dl.z), s3 = pp[3] * (dp[4 * c + 3] - dl.w);
-            if (diag) {  // a masked place stays 0 whatever dP holds there
-              const uint32_t m = (hf ? m1 : m0) >> (4 * c);
-              s0 = (m & 1u) ? s0 : 0.f;
-              s1 = (m & 2u) ? s1 : 0.f;
-              s2 = (m & 4u) ? s2 : 0.f;
-              s3 = (m & 8u) ? s3 : 0.f;
-            }
-            pk[2 * c] = Elem<T>::pack(s0, s1);
-            pk[2 * c + 1] = Elem<T>::pack(s2, s3);
+        for (int c = 0; c < 8; ++c) {
+          const float4 dl = *reinterpret_cast<const float4*>(ld + kTile + 4 * c);
+          float s0 = p[4 * c] * (dp[4 * c] - dl.x), s1 = p[4 * c + 1] * (dp[4 * c + 1] - dl.y);
+          float s2 = p[4 * c + 2] * (dp[4 * c + 2] - dl.z), s3 = p[4 * c + 3] * (dp[4 * c + 3] - dl.w);
+          if (diag) {  // a masked place stays 0 whatever dP holds there
+            const uint32_t m = behind >> (4 * c);
+            s0 = (m & 1u) ? s0 : 0.f;
+            s1 = (m & 2u) ? s1 : 0.f;
+            s2 = (m & 4u) ? s2 : 0.f;
+            s3 = (m & 8u) ? s3 : 0.f;
           }
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4*>(ds + sw128_offset(row, hf * 4 + c)) =
-                make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+          pk[2 * c] = Elem<T>::pack(s0, s1);
+          pk[2 * c + 1] = Elem<T>::pack(s2, s3);
         }
+        if (g >= C::NDS) ok = ok && mbar_wait(bar_ds_free + g % C::NDS, (g / C::NDS - 1) & 1, abort_flag);
+        uint8_t* ds = smem + C::OFF_DS + (g % C::NDS) * C::DS_BYTES + (w >> 1) * kTile * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(ds + sw128_offset(row, (w & 1) * 4 + c)) =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(bar_ds_full);
@@ -500,7 +491,7 @@ __global__ void __launch_bounds__(448, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 13) {
+  if (warp == 21) {
     tc_fence_after();
     tmem_dealloc<512>(tmem);
   }
