@@ -37,7 +37,7 @@ struct BwdArgs {
   int n_items, Hkv, G;
   int n_tiles;          // 128-row tiles of all sequences
   const float* ld;      // [Hq][n_tiles][2][128]: -lse log2 e (padding -inf), delta (padding 0)
-  float* dq_sum;        // [Hq][n_tiles][D / 4][128][4]
+  float* dq_sum;        // [Hq][n_tiles][4 row quarters][D / 32][8][32 rows][4 columns]
   View dk, dv;
   float scale, scale_log2;
 };
@@ -46,7 +46,8 @@ template <int D>
 struct BwdCfg {
   using G = TileGeo<D>;
   static constexpr int KVB = D >= 128 ? 1 : 2;   // K/V buffers
-  static constexpr int QST = 2;                  // Q and dO stages
+  static constexpr int QST = 2;                  // Q stages (with lse and delta)
+  static constexpr int OST = D >= 128 ? 1 : 2;   // dO stages
   static constexpr int NDS = D >= 128 ? 1 : 2;   // dS^T buffers
   static constexpr int NDQ = D >= 128 ? 1 : 2;   // dQ buffers in TMEM
   static constexpr int DS_BYTES = 2 * kTile * 128;
@@ -55,10 +56,12 @@ struct BwdCfg {
   static constexpr int OFF_V = OFF_K + KVB * G::BYTES;
   static constexpr int OFF_Q = OFF_V + KVB * G::BYTES;
   static constexpr int OFF_DO = OFF_Q + QST * G::BYTES;
-  static constexpr int OFF_DS = OFF_DO + QST * G::BYTES;
-  static constexpr int OFF_LD = OFF_DS + NDS * DS_BYTES;
+  static constexpr int OFF_DS = OFF_DO + OST * G::BYTES;
+  static constexpr int OFF_STG = OFF_DS + NDS * DS_BYTES;  // dQ on its way out: two pieces a read-out warp
+  static constexpr int STG_BYTES = 32 * 32 * 4;
+  static constexpr int OFF_LD = OFF_STG + 8 * STG_BYTES;
   static constexpr int OFF_BAR = OFF_LD + QST * LD_BYTES;
-  static constexpr int N_BARS = 2 * KVB + 4 * QST + 4 + NDS + 2 * NDQ + 2 + 1;
+  static constexpr int N_BARS = 2 * KVB + 2 * QST + 2 * OST + 4 + NDS + 2 * NDQ + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
   static constexpr int SMEM = OFF_MISC + 16;
   static constexpr int COL_S = 0, COL_DP = 128, COL_DV = 256, COL_DK = 256 + D;
@@ -131,7 +134,8 @@ __global__ void __launch_bounds__(256)
   for (int i = threadIdx.x; i < kTile * D / 8; i += 256) {
     const int r = i % kTile, c = i / kTile;  // 8 columns from 8 c
     if (r >= rows) continue;
-    const float4 a = in[(2 * c) * kTile + r], b = in[(2 * c + 1) * kTile + r];
+    const float4* p = in + (r / 32) * (8 * D) + (c / 4) * 256 + (c % 4) * 64 + r % 32;
+    const float4 a = p[0], b = p[32];
     *reinterpret_cast<uint4*>(out + r * dq.rs + c * 8) =
         make_uint4(Elem<T>::pack(a.x * scale, a.y * scale), Elem<T>::pack(a.z * scale, a.w * scale),
                    Elem<T>::pack(b.x * scale, b.y * scale), Elem<T>::pack(b.z * scale, b.w * scale));
@@ -152,9 +156,9 @@ __global__ void __launch_bounds__(704, 1)
   uint64_t* bar_kv_free = bar_kv_full + C::KVB;        // [KVB]
   uint64_t* bar_q_full = bar_kv_free + C::KVB;         // [QST] Q, lse and delta of a step
   uint64_t* bar_q_free = bar_q_full + C::QST;          // [QST]
-  uint64_t* bar_do_full = bar_q_free + C::QST;         // [QST]
-  uint64_t* bar_do_free = bar_do_full + C::QST;        // [QST]
-  uint64_t* bar_s_full = bar_do_free + C::QST;         // S^T of a step
+  uint64_t* bar_do_full = bar_q_free + C::QST;         // [OST]
+  uint64_t* bar_do_free = bar_do_full + C::OST;        // [OST]
+  uint64_t* bar_s_full = bar_do_free + C::OST;         // S^T of a step
   uint64_t* bar_p_full = bar_s_full + 1;               // P^T of a step written
   uint64_t* bar_dp_full = bar_p_full + 1;              // dP^T of a step
   uint64_t* bar_ds_full = bar_dp_full + 1;             // dS^T of a step written
@@ -177,6 +181,8 @@ __global__ void __launch_bounds__(704, 1)
     for (int b = 0; b < C::QST; ++b) {
       mbar_init(bar_q_full + b, 1);
       mbar_init(bar_q_free + b, 1);
+    }
+    for (int b = 0; b < C::OST; ++b) {
       mbar_init(bar_do_full + b, 1);
       mbar_init(bar_do_free + b, 1);
     }
@@ -217,8 +223,7 @@ __global__ void __launch_bounds__(704, 1)
         ++ni;
         for (int j = 0; ok && j < it.n; ++j) {
           const int st = g % C::QST, h = it.hk * a.G + j / it.per, qt = it.s.tile + j % it.per;
-          const uint32_t ph = (g / C::QST - 1) & 1;
-          if (g >= C::QST && !mbar_wait(bar_q_free + st, ph, abort_flag)) {
+          if (g >= C::QST && !mbar_wait(bar_q_free + st, (g / C::QST - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -228,20 +233,21 @@ __global__ void __launch_bounds__(704, 1)
           bulk_load(smem + C::OFF_LD + st * C::LD_BYTES,
                     a.ld + (static_cast<long long>(h) * a.n_tiles + it.s.base + qt) * 2 * kTile, C::LD_BYTES, bar_q_full + st);
           ++g;
-          if (n_do >= C::QST && !mbar_wait(bar_do_free + st, ph, abort_flag)) {
+          const int so = n_do % C::OST;
+          if (n_do >= C::OST && !mbar_wait(bar_do_free + so, (n_do / C::OST - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(bar_do_full + st, G::BYTES);
-          load_tile<D>(smem + C::OFF_DO + st * G::BYTES, &mdo, bar_do_full + st, h, row);
+          mbar_arrive_expect_tx(bar_do_full + so, G::BYTES);
+          load_tile<D>(smem + C::OFF_DO + so * G::BYTES, &mdo, bar_do_full + so, h, row);
           ++n_do;
         }
       }
       if (*(volatile int*)abort_flag) {  // no copy may land after the CTA has gone
         for (int i = ni > C::KVB ? ni - C::KVB : 0; i < ni; ++i) mbar_wait_drain(bar_kv_full + i % C::KVB, (i / C::KVB) & 1);
         for (int i = g > C::QST ? g - C::QST : 0; i < g; ++i) mbar_wait_drain(bar_q_full + i % C::QST, (i / C::QST) & 1);
-        for (int i = n_do > C::QST ? n_do - C::QST : 0; i < n_do; ++i)
-          mbar_wait_drain(bar_do_full + i % C::QST, (i / C::QST) & 1);
+        for (int i = n_do > C::OST ? n_do - C::OST : 0; i < n_do; ++i)
+          mbar_wait_drain(bar_do_full + i % C::OST, (i / C::OST) & 1);
       }
     }
   } else if (warp == 21) {
@@ -283,11 +289,11 @@ __global__ void __launch_bounds__(704, 1)
         return true;
       };
       auto issue_dp = [&](int j, int gg) -> bool {
-        const int st = gg % C::QST;
-        if (!mbar_wait(bar_do_full + st, (gg / C::QST) & 1, abort_flag)) return false;
+        const int so = gg % C::OST;
+        if (!mbar_wait(bar_do_full + so, (gg / C::OST) & 1, abort_flag)) return false;
         // D = 128: the columns are free once the last dQ in them has been read
         if (D >= 128 && gg > 0 && !mbar_wait(bar_dq_free, (gg - 1) & 1, abort_flag)) return false;
-        uint8_t* sDO = smem + C::OFF_DO + st * G::BYTES;
+        uint8_t* sDO = smem + C::OFF_DO + so * G::BYTES;
         const int rows = it.s.len - (it.s.tile + j % it.per) * kTile;
         if (rows < kTile) zero_rows<D>(sDO, rows, lane);
         tc_fence_after();
@@ -308,13 +314,13 @@ __global__ void __launch_bounds__(704, 1)
         if (ok && j == 0 && ni > 0) ok = mbar_wait(bar_dkv_free, (ni - 1) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        const Desc do_mn = G::mnmajor(smem_u32(smem + C::OFF_DO) + st * G::BYTES);
+        const Desc do_mn = G::mnmajor(smem_u32(smem + C::OFF_DO) + (g % C::OST) * G::BYTES);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)  // 16 queries of P^T = 8 TMEM columns; each group's half begins at its S^T columns
             mma_bf16_ts(tmem + C::COL_DV, tmem + C::COL_S + (kk / 2) * 32 + (kk % 2) * 8, do_mn.at(G::mnstep(kk)), id_kv,
                         j > 0 || kk > 0);
-          mma_commit(bar_do_free + st);
+          mma_commit(bar_do_free + g % C::OST);
         }
         __syncwarp();
         if (j + 1 < it.n && !(ok = issue_s(j + 1, g + 1))) break;
@@ -357,12 +363,12 @@ __global__ void __launch_bounds__(704, 1)
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     bool ok = true;
-    int g = 0, ni = 0;
+    int g = 0, ni = 0, pieces = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
       const BwdItem it = bwd_item(a, item);
       for (int j = 0; ok && j < it.n; ++j, ++g) {
         const int qb = g % C::NDQ, h = it.hk * a.G + j / it.per, qt = it.s.tile + j % it.per;
-        float* dst = a.dq_sum + (static_cast<long long>(h) * a.n_tiles + it.s.base + qt) * kTile * D + row * 4;
+        float* dst = a.dq_sum + (static_cast<long long>(h) * a.n_tiles + it.s.base + qt) * kTile * D + quarter * 32 * D;
         ok = mbar_wait(bar_dq_full + qb, (g / C::NDQ) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -375,9 +381,19 @@ __global__ void __launch_bounds__(704, 1)
             tc_fence_before();
             mbar_arrive(bar_dq_free + qb);
           }
+          // 32 rows x 32 columns go out as one bulk reduction of 4 KiB
+          float4* stg = reinterpret_cast<float4*>(smem + C::OFF_STG + (quarter * 2 + (pieces & 1)) * C::STG_BYTES);
+          if (lane == 0 && pieces >= 2) bulk_wait_read<1>();  // the piece two before has been read
+          ++pieces;
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i)  // 32 rows x 16 bytes a warp and instruction
-            red_add_v4(dst + (c * 8 + i) * kTile * 4, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          for (int i = 0; i < 8; ++i) stg[i * 32 + lane] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            bulk_reduce_add(dst + c * 32 * 32, stg, C::STG_BYTES);
+            bulk_commit_group();
+          }
         }
       }
       ok = ok && mbar_wait(bar_dkv_full, ni & 1, abort_flag);
@@ -409,6 +425,7 @@ __global__ void __launch_bounds__(704, 1)
         }
       }
     }
+    if (lane == 0) bulk_wait_all();  // no reduction may read shared memory after the CTA has gone
   } else {
     // ------------------------------------------------------ P^T and dS^T
     const int w = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;  // w: which 32 queries
