@@ -212,16 +212,9 @@ int run_fwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tens
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Workspace of the backward pass: packed lse and delta, then the dq sums.
-struct BwdWs {
-  size_t dq, total;
-};
-BwdWs bwd_ws(int Hq, int D, const pa_layout* L) {
-  const size_t tiles = static_cast<size_t>(Hq) * L->fwd.size();
-  BwdWs w;
-  w.dq = align256(tiles * 2 * kTile * sizeof(float));
-  w.total = w.dq + align256(tiles * kTile * D * sizeof(float)) + 256;
-  return w;
+// Workspace of the backward pass: packed lse and delta of every (head, tile).
+size_t bwd_ws(int Hq, const pa_layout* L) {
+  return align256(static_cast<size_t>(Hq) * L->fwd.size() * 2 * kTile * sizeof(float)) + 256;
 }
 
 template <typename T, int D>
@@ -232,28 +225,37 @@ int run_bwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tens
   int st, sms;
   if ((st = map_rows(&mq, q, c, c.Hq, L->rows, kTile)) || (st = map_rows(&mk, k, c, c.Hkv, L->rows, kTile)) ||
       (st = map_rows(&mv, v, c, c.Hkv, L->rows, kTile)) || (st = map_rows(&mdo, dO, c, c.Hq, L->rows, kTile)) ||
-      (st = sm_count(&sms)) || (st = allow_smem<pa_bwd_kernel<T, D>, BwdCfg<D>::SMEM>()))
+      (st = sm_count(&sms)) || (st = allow_smem<pa_bwd_dkv_kernel<T, D>, DkvCfg<D>::SMEM>()) ||
+      (st = allow_smem<pa_bwd_dq_kernel<T, D>, DqCfg<D>::SMEM>()))
     return st;
-  const BwdWs w = bwd_ws(c.Hq, D, L);
-  float* ld = static_cast<float*>(ws);
-  float* sum = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.dq);
   const unsigned tiles = static_cast<unsigned>(L->fwd.size());
-  if (static_cast<long long>(tiles) * c.Hkv > (1ll << 30)) return SA_ERR_UNSUPPORTED;  // item numbers stay in 31 bits
-  BwdArgs a;
+  if (static_cast<long long>(tiles) * c.Hq > (1ll << 30)) return SA_ERR_UNSUPPORTED;  // item numbers stay in 31 bits
+  float* ld = static_cast<float*>(ws);
+  const float scale_log2 = static_cast<float>(static_cast<double>(c.scale) * 1.4426950408889634);
+  DkvArgs a;
   a.slots = dc.bwd;
   a.Hkv = c.Hkv;
   a.G = c.Hq / c.Hkv;
   a.n_items = static_cast<int>(tiles) * c.Hkv;
   a.n_tiles = static_cast<int>(tiles);
   a.ld = ld;
-  a.dq_sum = sum;
   a.dk = view(dk);
   a.dv = view(dv);
   a.scale = c.scale;
-  a.scale_log2 = static_cast<float>(static_cast<double>(c.scale) * 1.4426950408889634);
-  pa_bwd_pre_kernel<T, D><<<dim3(tiles, c.Hq), 256, 0, c.s>>>(dc.fwd, view(o), view(dO), lse, ls, ld, sum, a.n_tiles);
-  pa_bwd_kernel<T, D><<<std::min(a.n_items, sms), BwdCfg<D>::THREADS, BwdCfg<D>::SMEM, c.s>>>(mq, mk, mv, mdo, a);
-  pa_bwd_dq_kernel<T, D><<<dim3(tiles, c.Hq), 256, 0, c.s>>>(dc.fwd, sum, view(dq), a.n_tiles, c.scale);
+  a.scale_log2 = scale_log2;
+  DqArgs b;
+  b.slots = dc.fwd;
+  b.Hq = c.Hq;
+  b.G = a.G;
+  b.n_items = static_cast<int>(tiles) * c.Hq;
+  b.n_tiles = a.n_tiles;
+  b.ld = ld;
+  b.dq = view(dq);
+  b.scale = c.scale;
+  b.scale_log2 = scale_log2;
+  pa_bwd_pre_kernel<T, D><<<dim3(tiles, c.Hq), 256, 0, c.s>>>(dc.fwd, view(o), view(dO), lse, ls, ld, a.n_tiles);
+  pa_bwd_dkv_kernel<T, D><<<std::min(a.n_items, sms), kBwdThreads, DkvCfg<D>::SMEM, c.s>>>(mq, mk, mv, mdo, a);
+  pa_bwd_dq_kernel<T, D><<<std::min(b.n_items, sms), kBwdThreads, DqCfg<D>::SMEM, c.s>>>(mq, mk, mv, mdo, b);
   return launched();
 }
 
@@ -316,7 +318,7 @@ int packed_attn_fwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, 
 size_t packed_attn_bwd_workspace_size(int Hq, int Hkv, int D, const pa_layout* L) {
   const Call c{L ? static_cast<long long>(L->rows) : 0, Hq, Hkv, D, PA_BF16, 1.f, nullptr};
   if (check_call(c, L)) return 0;
-  return bwd_ws(Hq, D, L).total;
+  return bwd_ws(Hq, L);
 }
 
 int packed_attn_bwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, const pa_tensor* o, const float* lse,

@@ -1,100 +1,53 @@
 // Backward kernels of packed causal attention on tcgen05.
 //
-// pa_bwd_pre_kernel   per (query tile, head): delta_i = <dO_i, o_i>, packed
-//                     with -lse log2 e for the main kernel, and zeros for the
-//                     tile's dq sum.
-// pa_bwd_kernel       persistent; an item is a tile of 128 keys of one K/V
-//                     head and all query tiles of all query heads that see it
-//                     (diagonal first, head by head).  Per step of 128 queries,
-//                     keys on TMEM lanes:
-//   S^T = K Q^T                       P^T = 2^(S^T c - lse log2 e), over S^T
-//   dP^T = V dO^T                     dS^T = P^T (dP^T - delta), to shared memory
-//   dV += P^T dO                      A from TMEM
-//   dK += dS^T Q,  dQ = dS K          A from shared memory, dS^T read K-major
-//                                     and MN-major
-//                     dV and dK stay in TMEM for the whole item, so their sums
-//                     run in a fixed order over the group's heads; dQ is
-//                     added to a float32 sum per tile in global memory.
-// pa_bwd_dq_kernel    dq = scale * sum, rounded once.
+// pa_bwd_pre_kernel   per (query tile, head): delta_i = <dO_i, o_i> and
+//                     -lse_i log2 e, padded to whole tiles.
+// pa_bwd_dkv_kernel   an item is a tile of 128 keys of one K/V head and all
+//                     query tiles of all query heads that see it (head by
+//                     head, diagonal first).  Per step of 128 queries, keys on
+//                     TMEM lanes:
+//                       S^T = K Q^T,    P^T = 2^(S^T c - lse log2 e)
+//                       dP^T = V dO^T,  dS^T = P^T (dP^T - delta)
+//                       dV += P^T dO,   dK += dS^T Q
+// pa_bwd_dq_kernel    an item is a tile of 128 queries of one head and the key
+//                     tiles before it; per step S, dP and dS with queries on
+//                     TMEM lanes, and dQ += dS K.
 //
-// The S^T product of the next step is issued behind dV (which frees its
-// columns) and so runs under this step's dS; the next step's dP^T runs under
-// the products of dS.  With D = 128 TMEM is full (S^T, dP^T, dV, dK of 128
-// columns each), so dQ lands in the dP^T columns and the next dP^T waits for
-// its read-out, which dK covers.
+// The scores are computed twice (7 products of 128 x 128 x D a tile pair in
+// place of 5).  The other way, dQ of every tile pair added to a float32 sum in
+// global memory by the kernel that holds the keys, was built and measured: it
+// moves 512 D bytes of float32 reductions a tile pair, ran into them (12.9 ms
+// against 9.8 ms without, one sequence of 32768, 16 heads of 128), needs the
+// sums zeroed and converted, and leaves dq's last bits to their order.  Here
+// every sum has a fixed order, so the gradients are the same bits every time.
 //
-// Roles (704 threads): warps 0..15 four compute groups (thread = key row, 32 of
-// the step's queries each), warps 16..19 read-out of dQ and of the item's dK,
-// dV, warp 20 lane 0 the TMA producer, warp 21 TMEM and the MMAs.
+// P^T (dS^T, dS) goes back into TMEM over the scores (over dP), rounded, and
+// is the A operand of its product from there, so shared memory only holds
+// what TMA brings.  One thread issues all MMAs of a CTA; they execute in
+// order, so a product behind another that reads its destination columns needs
+// no wait.
+//
+// Roles of both (704 threads): warps 0..15 four compute groups (thread = row
+// of the tile, 32 columns of the step each), warps 16..19 the read-out of an
+// item's result, warp 20 lane 0 the TMA producer, warp 21 TMEM and the MMAs.
 #pragma once
+
+#include <type_traits>
 
 #include "pa_device.cuh"
 
 namespace pa {
 
-struct BwdArgs {
-  const Slot* slots;
-  int n_items, Hkv, G;
-  int n_tiles;          // 128-row tiles of all sequences
-  const float* ld;      // [Hq][n_tiles][2][128]: -lse log2 e (padding -inf), delta (padding 0)
-  float* dq_sum;        // [Hq][n_tiles][4 row quarters][D / 32][8][32 rows][4 columns]
-  View dk, dv;
-  float scale, scale_log2;
-};
+constexpr int kBwdThreads = 704, kBwdComputeWarps = 16;
 
-template <int D>
-struct BwdCfg {
-  using G = TileGeo<D>;
-  static constexpr int KVB = D >= 128 ? 1 : 2;   // K/V buffers
-  static constexpr int QST = 2;                  // Q stages (with lse and delta)
-  static constexpr int OST = D >= 128 ? 1 : 2;   // dO stages
-  static constexpr int NDS = D >= 128 ? 1 : 2;   // dS^T buffers
-  static constexpr int NDQ = D >= 128 ? 1 : 2;   // dQ buffers in TMEM
-  static constexpr int DS_BYTES = 2 * kTile * 128;
-  static constexpr int LD_BYTES = 2 * kTile * 4;
-  static constexpr int OFF_K = 0;
-  static constexpr int OFF_V = OFF_K + KVB * G::BYTES;
-  static constexpr int OFF_Q = OFF_V + KVB * G::BYTES;
-  static constexpr int OFF_DO = OFF_Q + QST * G::BYTES;
-  static constexpr int OFF_DS = OFF_DO + OST * G::BYTES;
-  static constexpr int OFF_STG = OFF_DS + NDS * DS_BYTES;  // dQ on its way out: two pieces a read-out warp
-  static constexpr int STG_BYTES = 32 * 32 * 4;
-  static constexpr int OFF_LD = OFF_STG + 8 * STG_BYTES;
-  static constexpr int OFF_BAR = OFF_LD + QST * LD_BYTES;
-  static constexpr int N_BARS = 2 * KVB + 2 * QST + 2 * OST + 4 + NDS + 2 * NDQ + 2 + 1;
-  static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
-  static constexpr int SMEM = OFF_MISC + 16;
-  static constexpr int COL_S = 0, COL_DP = 128, COL_DV = 256, COL_DK = 256 + D;
-  static constexpr int COL_DQ = D >= 128 ? COL_DP : 256 + 2 * D;  // + b * D
-  static constexpr int COMPUTE = 512, THREADS = COMPUTE + 192;
-  static_assert(SMEM <= 227 * 1024, "shared memory");
-};
-
-struct BwdItem {
-  Slot s;
-  int hk, n, per;  // K/V head, steps, steps of one query head
-};
-
-__device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, int item) {
-  BwdItem it;
-  const int slot = item / a.Hkv;
-  it.hk = item - slot * a.Hkv;
-  it.s = a.slots[slot];
-  it.per = (it.s.len + kTile - 1) / kTile - it.s.tile;
-  it.n = it.per * a.G;
-  return it;
-}
-
-// 32 rows of two threads' worth: D / 8 threads a row, 8 columns each.
+// TPR threads a row, 8 columns each.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
-    pa_bwd_pre_kernel(const Slot* slots, View o, View dO, const float* lse, long long ls, float* ld, float* dq_sum,
-                      int n_tiles) {
-  constexpr int TPR = D / 8, RPI = 256 / TPR;  // threads a row, rows a turn
+    pa_bwd_pre_kernel(const Slot* slots, View o, View dO, const float* lse, long long ls, float* ld, int n_tiles) {
+  constexpr int TPR = D / 8, RPI = 256 / TPR;
   const Slot s = slots[blockIdx.x];
   const int h = blockIdx.y, tid = threadIdx.x;
-  const long long tile = static_cast<long long>(h) * n_tiles + s.base + s.tile;
-  float* out = ld + tile * 2 * kTile;
+  float* out = ld + (static_cast<long long>(h) * n_tiles + s.base + s.tile) * 2 * kTile;
   for (int r = tid / TPR; r < kTile; r += RPI) {
     const int i = s.tile * kTile + r;
     const bool in = i < s.len;
@@ -117,86 +70,107 @@ __global__ void __launch_bounds__(256)
       out[kTile + r] = d;
     }
   }
-  float4* z = reinterpret_cast<float4*>(dq_sum + tile * kTile * D);
-  for (int i = tid; i < kTile * D / 4; i += 256) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
+// Writes one row's D float32 values from TMEM, times f, as T.
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
-    pa_bwd_dq_kernel(const Slot* slots, const float* dq_sum, View dq, int n_tiles, float scale) {
-  const Slot s = slots[blockIdx.x];
-  const int h = blockIdx.y;
-  const long long tile = static_cast<long long>(h) * n_tiles + s.base + s.tile;
-  const float4* in = reinterpret_cast<const float4*>(dq_sum + tile * kTile * D);
-  const int rows = min(kTile, s.len - s.tile * kTile);
-  T* out = static_cast<T*>(const_cast<void*>(dq.p)) + (static_cast<long long>(s.start) + s.tile * kTile) * dq.rs + h * dq.hs;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < kTile * D / 8; i += 256) {
-    const int r = i % kTile, c = i / kTile;  // 8 columns from 8 c
-    if (r >= rows) continue;
-    const float4* p = in + (r / 32) * (8 * D) + (c / 4) * 256 + (c % 4) * 64 + r % 32;
-    const float4 a = p[0], b = p[32];
-    *reinterpret_cast<uint4*>(out + r * dq.rs + c * 8) =
-        make_uint4(Elem<T>::pack(a.x * scale, a.y * scale), Elem<T>::pack(a.z * scale, a.w * scale),
-                   Elem<T>::pack(b.x * scale, b.y * scale), Elem<T>::pack(b.z * scale, b.w * scale));
+__device__ __forceinline__ void row_out(T* out, uint32_t taddr, bool in, float f) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    float x[32];
+    tmem_ld32(taddr + c * 32, x);
+    tmem_wait_ld();
+    if (in)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(out + c * 32 + i * 8) =
+            make_uint4(Elem<T>::pack(x[8 * i] * f, x[8 * i + 1] * f), Elem<T>::pack(x[8 * i + 2] * f, x[8 * i + 3] * f),
+                       Elem<T>::pack(x[8 * i + 4] * f, x[8 * i + 5] * f), Elem<T>::pack(x[8 * i + 6] * f, x[8 * i + 7] * f));
   }
 }
 
+// ------------------------------------------------------------------ dK, dV
+struct DkvArgs {
+  const Slot* slots;
+  int n_items, Hkv, G;
+  int n_tiles;      // 128-row tiles of all sequences
+  const float* ld;  // [Hq][n_tiles][2][128]: -lse log2 e (padding -inf), delta (padding 0)
+  View dk, dv;
+  float scale, scale_log2;
+};
+
+template <int D>
+struct DkvCfg {
+  using G = TileGeo<D>;
+  static constexpr int KVB = D >= 128 ? 1 : 2;  // K/V buffers
+  static constexpr int QST = D >= 128 ? 3 : 5;  // Q stages, with delta
+  static constexpr int OST = D >= 128 ? 2 : 4;  // dO stages, with lse
+  static constexpr int NS = D >= 128 ? 1 : 2;   // S^T buffers in TMEM
+  static constexpr int VEC = kTile * 4;         // a tile's lse or delta
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_V = OFF_K + KVB * G::BYTES;
+  static constexpr int OFF_Q = OFF_V + KVB * G::BYTES;
+  static constexpr int OFF_DO = OFF_Q + QST * G::BYTES;
+  static constexpr int OFF_DELTA = OFF_DO + OST * G::BYTES;
+  static constexpr int OFF_LSE = OFF_DELTA + QST * VEC;
+  static constexpr int OFF_BAR = OFF_LSE + OST * VEC;
+  static constexpr int N_BARS = 2 * KVB + 2 * QST + 2 * OST + NS + 3 + 2 + 1;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
+  static constexpr int SMEM = OFF_MISC + 16;
+  static constexpr int COL_DP = NS * 128, COL_DV = COL_DP + 128, COL_DK = COL_DV + D;
+  static_assert(SMEM <= 227 * 1024 && COL_DK + D <= 512, "shared memory and TMEM");
+};
+
+struct DkvItem {
+  Slot s;
+  int hk, n, per;  // K/V head, steps, steps of one query head
+};
+
+__device__ __forceinline__ DkvItem dkv_item(const DkvArgs& a, int item) {
+  DkvItem it;
+  const int slot = item / a.Hkv;
+  it.hk = item - slot * a.Hkv;
+  it.s = a.slots[slot];
+  it.per = (it.s.len + kTile - 1) / kTile - it.s.tile;
+  it.n = it.per * a.G;
+  return it;
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(704, 1)
-    pa_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const BwdArgs a) {
-  using C = BwdCfg<D>;
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    pa_bwd_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const DkvArgs a) {
+  using C = DkvCfg<D>;
   using G = TileGeo<D>;
   // fp16's P (at most 1) is scaled up for its product, away from the type's subnormals; dV is scaled back
   constexpr float kP = std::is_same<T, __half>::value ? 4096.f : 1.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* bar_kv_full = bars;                        // [KVB]
-  uint64_t* bar_kv_free = bar_kv_full + C::KVB;        // [KVB]
-  uint64_t* bar_q_full = bar_kv_free + C::KVB;         // [QST] Q, lse and delta of a step
-  uint64_t* bar_q_free = bar_q_full + C::QST;          // [QST]
-  uint64_t* bar_do_full = bar_q_free + C::QST;         // [OST]
-  uint64_t* bar_do_free = bar_do_full + C::OST;        // [OST]
-  uint64_t* bar_s_full = bar_do_free + C::OST;         // S^T of a step
-  uint64_t* bar_p_full = bar_s_full + 1;               // P^T of a step written
-  uint64_t* bar_dp_full = bar_p_full + 1;              // dP^T of a step
-  uint64_t* bar_ds_full = bar_dp_full + 1;             // dS^T of a step written
-  uint64_t* bar_ds_free = bar_ds_full + 1;             // [NDS]
-  uint64_t* bar_dq_full = bar_ds_free + C::NDS;        // [NDQ]
-  uint64_t* bar_dq_free = bar_dq_full + C::NDQ;        // [NDQ]
-  uint64_t* bar_dkv_full = bar_dq_free + C::NDQ;       // the item's dK, dV
-  uint64_t* bar_dkv_free = bar_dkv_full + 1;
-  uint64_t* bar_drain = bar_dkv_free + 1;
+  uint64_t* bar_kv_full = bars;                      // [KVB]
+  uint64_t* bar_kv_free = bar_kv_full + C::KVB;      // [KVB]
+  uint64_t* bar_q_full = bar_kv_free + C::KVB;       // [QST]
+  uint64_t* bar_q_free = bar_q_full + C::QST;        // [QST]
+  uint64_t* bar_do_full = bar_q_free + C::QST;       // [OST]
+  uint64_t* bar_do_free = bar_do_full + C::OST;      // [OST]
+  uint64_t* bar_s_full = bar_do_free + C::OST;       // [NS] S^T of a step
+  uint64_t* bar_p_full = bar_s_full + C::NS;         // P^T of a step written
+  uint64_t* bar_dp_full = bar_p_full + 1;            // dP^T of a step
+  uint64_t* bar_ds_full = bar_dp_full + 1;           // dS^T of a step written
+  uint64_t* bar_out_full = bar_ds_full + 1;          // the item's dK, dV
+  uint64_t* bar_out_free = bar_out_full + 1;
+  uint64_t* bar_drain = bar_out_free + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, n_ctas = gridDim.x;
   if (threadIdx.x == 0) {
-    for (int b = 0; b < C::KVB; ++b) {
-      mbar_init(bar_kv_full + b, 1);
-      mbar_init(bar_kv_free + b, 1);
-    }
-    for (int b = 0; b < C::QST; ++b) {
-      mbar_init(bar_q_full + b, 1);
-      mbar_init(bar_q_free + b, 1);
-    }
-    for (int b = 0; b < C::OST; ++b) {
-      mbar_init(bar_do_full + b, 1);
-      mbar_init(bar_do_free + b, 1);
-    }
-    mbar_init(bar_s_full, 1);
-    mbar_init(bar_p_full, C::COMPUTE);
+    for (int b = 0; b < 2 * C::KVB + 2 * C::QST + 2 * C::OST + C::NS; ++b) mbar_init(bars + b, 1);
+    mbar_init(bar_p_full, kBwdComputeWarps);
     mbar_init(bar_dp_full, 1);
-    mbar_init(bar_ds_full, C::COMPUTE);
-    for (int b = 0; b < C::NDS; ++b) mbar_init(bar_ds_free + b, 1);
-    for (int b = 0; b < C::NDQ; ++b) {
-      mbar_init(bar_dq_full + b, 1);
-      mbar_init(bar_dq_free + b, 128);
-    }
-    mbar_init(bar_dkv_full, 1);
-    mbar_init(bar_dkv_free, 128);
+    mbar_init(bar_ds_full, kBwdComputeWarps);
+    mbar_init(bar_out_full, 1);
+    mbar_init(bar_out_free, 4);
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -213,7 +187,7 @@ __global__ void __launch_bounds__(704, 1)
       bool ok = true;
       int g = 0, ni = 0, n_do = 0;
       for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-        const BwdItem it = bwd_item(a, item);
+        const DkvItem it = dkv_item(a, item);
         const int kb = ni % C::KVB;
         if (ni >= C::KVB && !mbar_wait(bar_kv_free + kb, (ni / C::KVB - 1) & 1, abort_flag)) break;
         const int key0 = it.s.start + it.s.tile * kTile;
@@ -222,24 +196,25 @@ __global__ void __launch_bounds__(704, 1)
         load_tile<D>(smem + C::OFF_V + kb * G::BYTES, &mv, bar_kv_full + kb, it.hk, key0);
         ++ni;
         for (int j = 0; ok && j < it.n; ++j) {
-          const int st = g % C::QST, h = it.hk * a.G + j / it.per, qt = it.s.tile + j % it.per;
-          if (g >= C::QST && !mbar_wait(bar_q_free + st, (g / C::QST - 1) & 1, abort_flag)) {
+          const int h = it.hk * a.G + j / it.per, qt = it.s.tile + j % it.per, row = it.s.start + qt * kTile;
+          const float* ld = a.ld + (static_cast<long long>(h) * a.n_tiles + it.s.base + qt) * 2 * kTile;
+          const int sq = g % C::QST;
+          if (g >= C::QST && !mbar_wait(bar_q_free + sq, (g / C::QST - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          const int row = it.s.start + qt * kTile;
-          mbar_arrive_expect_tx(bar_q_full + st, G::BYTES + C::LD_BYTES);
-          load_tile<D>(smem + C::OFF_Q + st * G::BYTES, &mq, bar_q_full + st, h, row);
-          bulk_load(smem + C::OFF_LD + st * C::LD_BYTES,
-                    a.ld + (static_cast<long long>(h) * a.n_tiles + it.s.base + qt) * 2 * kTile, C::LD_BYTES, bar_q_full + st);
+          mbar_arrive_expect_tx(bar_q_full + sq, G::BYTES + C::VEC);
+          load_tile<D>(smem + C::OFF_Q + sq * G::BYTES, &mq, bar_q_full + sq, h, row);
+          bulk_load(smem + C::OFF_DELTA + sq * C::VEC, ld + kTile, C::VEC, bar_q_full + sq);
           ++g;
           const int so = n_do % C::OST;
           if (n_do >= C::OST && !mbar_wait(bar_do_free + so, (n_do / C::OST - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(bar_do_full + so, G::BYTES);
+          mbar_arrive_expect_tx(bar_do_full + so, G::BYTES + C::VEC);
           load_tile<D>(smem + C::OFF_DO + so * G::BYTES, &mdo, bar_do_full + so, h, row);
+          bulk_load(smem + C::OFF_LSE + so * C::VEC, ld, C::VEC, bar_do_full + so);
           ++n_do;
         }
       }
@@ -253,16 +228,15 @@ __global__ void __launch_bounds__(704, 1)
   } else if (warp == 21) {
     // ------------------------------------------------------------------ MMAs
     constexpr uint32_t id_s = make_idesc<T>(128, 128, false, false);
-    constexpr uint32_t id_kv = make_idesc<T>(128, D, false, true);
-    constexpr uint32_t id_q = make_idesc<T>(128, D, true, true);
+    constexpr uint32_t id_o = make_idesc<T>(128, D, false, true);
     bool ok = true;
     int g = 0, ni = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
-      const BwdItem it = bwd_item(a, item);
+      const DkvItem it = dkv_item(a, item);
       const int kb = ni % C::KVB;
       uint8_t* sK = smem + C::OFF_K + kb * G::BYTES;
       uint8_t* sV = smem + C::OFF_V + kb * G::BYTES;
-      const Desc k_k = G::kmajor(smem_u32(sK)), k_mn = G::mnmajor(smem_u32(sK)), v_k = G::kmajor(smem_u32(sV));
+      const Desc k_k = G::kmajor(smem_u32(sK)), v_k = G::kmajor(smem_u32(sV));
       ok = mbar_wait(bar_kv_full + kb, (ni / C::KVB) & 1, abort_flag);
       if (!ok) break;
       const int keys = it.s.len - it.s.tile * kTile;
@@ -270,32 +244,33 @@ __global__ void __launch_bounds__(704, 1)
         zero_rows<D>(sK, keys, lane);
         zero_rows<D>(sV, keys, lane);
       }
-      // S^T and dP^T of step j (global step gg); a last, partial query tile is zeroed behind its rows first
-      auto issue_s = [&](int j, int gg) -> bool {
-        const int st = gg % C::QST;
+      int rows_s = it.s.len - it.s.tile * kTile, left_s = it.per, rows_p = rows_s, left_p = it.per;  // of the next query tile
+      // S^T (dP^T) of the item's next step, global step gg; a last, partial query tile is zeroed behind its rows first
+      auto issue_s = [&](int gg) -> bool {
+        const int st = gg % C::QST, sb = gg % C::NS;
         if (!mbar_wait(bar_q_full + st, (gg / C::QST) & 1, abort_flag)) return false;
         uint8_t* sQ = smem + C::OFF_Q + st * G::BYTES;
-        const int rows = it.s.len - (it.s.tile + j % it.per) * kTile;
-        if (rows < kTile) zero_rows<D>(sQ, rows, lane);
+        if (rows_s < kTile) zero_rows<D>(sQ, rows_s, lane);
+        rows_s -= kTile;
+        if (--left_s == 0) rows_s = keys, left_s = it.per;
         tc_fence_after();
         const Desc q_k = G::kmajor(smem_u32(sQ));
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16_ss(tmem + C::COL_S, k_k.at(G::kstep(kk)), q_k.at(G::kstep(kk)), id_s, kk > 0);
-          mma_commit(bar_s_full);
+            mma_bf16_ss(tmem + sb * 128, k_k.at(G::kstep(kk)), q_k.at(G::kstep(kk)), id_s, kk > 0);
+          mma_commit(bar_s_full + sb);
         }
         __syncwarp();
         return true;
       };
-      auto issue_dp = [&](int j, int gg) -> bool {
-        const int so = gg % C::OST;
-        if (!mbar_wait(bar_do_full + so, (gg / C::OST) & 1, abort_flag)) return false;
-        // D = 128: the columns are free once the last dQ in them has been read
-        if (D >= 128 && gg > 0 && !mbar_wait(bar_dq_free, (gg - 1) & 1, abort_flag)) return false;
-        uint8_t* sDO = smem + C::OFF_DO + so * G::BYTES;
-        const int rows = it.s.len - (it.s.tile + j % it.per) * kTile;
-        if (rows < kTile) zero_rows<D>(sDO, rows, lane);
+      auto issue_dp = [&](int gg) -> bool {
+        const int st = gg % C::OST;
+        if (!mbar_wait(bar_do_full + st, (gg / C::OST) & 1, abort_flag)) return false;
+        uint8_t* sDO = smem + C::OFF_DO + st * G::BYTES;
+        if (rows_p < kTile) zero_rows<D>(sDO, rows_p, lane);
+        rows_p -= kTile;
+        if (--left_p == 0) rows_p = keys, left_p = it.per;
         tc_fence_after();
         const Desc do_k = G::kmajor(smem_u32(sDO));
         if (elect_one()) {
@@ -307,50 +282,39 @@ __global__ void __launch_bounds__(704, 1)
         __syncwarp();
         return true;
       };
-      ok = issue_s(0, g) && issue_dp(0, g);
+      ok = issue_s(g) && issue_dp(g) && (C::NS == 1 || it.n == 1 || issue_s(g + 1));
       for (int j = 0; ok && j < it.n; ++j, ++g) {
-        const int st = g % C::QST;
+        const int sq = g % C::QST, so = g % C::OST;
         ok = mbar_wait(bar_p_full, g & 1, abort_flag);
-        if (ok && j == 0 && ni > 0) ok = mbar_wait(bar_dkv_free, (ni - 1) & 1, abort_flag);
+        if (ok && j == 0 && ni > 0) ok = mbar_wait(bar_out_free, (ni - 1) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        const Desc do_mn = G::mnmajor(smem_u32(smem + C::OFF_DO) + (g % C::OST) * G::BYTES);
+        const Desc do_mn = G::mnmajor(smem_u32(smem + C::OFF_DO) + so * G::BYTES);
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)  // 16 queries of P^T = 8 TMEM columns; each group's half begins at its S^T columns
-            mma_bf16_ts(tmem + C::COL_DV, tmem + C::COL_S + (kk / 2) * 32 + (kk % 2) * 8, do_mn.at(G::mnstep(kk)), id_kv,
-                        j > 0 || kk > 0);
-          mma_commit(bar_do_free + g % C::OST);
+          for (int kk = 0; kk < kTile / 16; ++kk)  // 16 queries = 8 TMEM columns of P^T, each group's from its first column on
+            mma_bf16_ts(tmem + C::COL_DV, tmem + (g % C::NS) * 128 + (kk / 2) * 32 + (kk % 2) * 8, do_mn.at(G::mnstep(kk)),
+                        id_o, j > 0 || kk > 0);
+          mma_commit(bar_do_free + so);
         }
         __syncwarp();
-        if (j + 1 < it.n && !(ok = issue_s(j + 1, g + 1))) break;
+        if (j + C::NS < it.n && !(ok = issue_s(g + C::NS))) break;  // over the columns of P^T, behind its product
         if (!(ok = mbar_wait(bar_ds_full, g & 1, abort_flag))) break;
-        if (D < 128 && j + 1 < it.n && !(ok = issue_dp(j + 1, g + 1))) break;
-        const int qb = g % C::NDQ;
-        if (D < 128 && g >= C::NDQ && !(ok = mbar_wait(bar_dq_free + qb, (g / C::NDQ - 1) & 1, abort_flag))) break;
         tc_fence_after();
-        // dS as queries x keys (M over two panels, 16 keys a k-step) and dS^T as keys x queries
-        const uint32_t ds_base = smem_u32(smem + C::OFF_DS) + (g % C::NDS) * C::DS_BYTES;
-        const Desc ds_mn(ds_base, kTile * 128, 1024, kSwizzle128), ds_k(ds_base, 16, 1024, kSwizzle128);
-        const Desc q_mn = G::mnmajor(smem_u32(smem + C::OFF_Q) + st * G::BYTES);
+        const Desc q_mn = G::mnmajor(smem_u32(smem + C::OFF_Q) + sq * G::BYTES);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_bf16_ss(tmem + C::COL_DQ + qb * D, ds_mn.at(kk * 2048), k_mn.at(G::mnstep(kk)), id_q, kk > 0);
-          mma_commit(bar_dq_full + qb);
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_bf16_ss(tmem + C::COL_DK, ds_k.at((kk / 4) * kTile * 128 + (kk % 4) * 32), q_mn.at(G::mnstep(kk)), id_kv,
+            mma_bf16_ts(tmem + C::COL_DK, tmem + C::COL_DP + (kk / 2) * 32 + (kk % 2) * 8, q_mn.at(G::mnstep(kk)), id_o,
                         j > 0 || kk > 0);
-          mma_commit(bar_q_free + st);
-          mma_commit(bar_ds_free + g % C::NDS);
+          mma_commit(bar_q_free + sq);
         }
         __syncwarp();
-        if (D >= 128 && j + 1 < it.n) ok = issue_dp(j + 1, g + 1);
+        if (j + 1 < it.n) ok = issue_dp(g + 1);
       }
       if (ok && elect_one()) {
         mma_commit(bar_kv_free + kb);
-        mma_commit(bar_dkv_full);
+        mma_commit(bar_out_full);
       }
     }
     if (elect_one()) {  // every MMA has completed before TMEM is released
@@ -359,98 +323,54 @@ __global__ void __launch_bounds__(704, 1)
     }
     __syncwarp();
   } else if (warp >= 16) {
-    // ------------------------------------------- read-out of dQ, dK and dV
+    // --------------------------------------------------- read-out of dK, dV
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     bool ok = true;
-    int g = 0, ni = 0, pieces = 0;
+    int ni = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
-      const BwdItem it = bwd_item(a, item);
-      for (int j = 0; ok && j < it.n; ++j, ++g) {
-        const int qb = g % C::NDQ, h = it.hk * a.G + j / it.per, qt = it.s.tile + j % it.per;
-        float* dst = a.dq_sum + (static_cast<long long>(h) * a.n_tiles + it.s.base + qt) * kTile * D + quarter * 32 * D;
-        ok = mbar_wait(bar_dq_full + qb, (g / C::NDQ) & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          float v[32];
-          tmem_ld32(tmem + lane_base + C::COL_DQ + qb * D + c * 32, v);
-          tmem_wait_ld();
-          if (c == D / 32 - 1) {
-            tc_fence_before();
-            mbar_arrive(bar_dq_free + qb);
-          }
-          // 32 rows x 32 columns go out as one bulk reduction of 4 KiB
-          float4* stg = reinterpret_cast<float4*>(smem + C::OFF_STG + (quarter * 2 + (pieces & 1)) * C::STG_BYTES);
-          if (lane == 0 && pieces >= 2) bulk_wait_read<1>();  // the piece two before has been read
-          ++pieces;
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) stg[i * 32 + lane] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            bulk_reduce_add(dst + c * 32 * 32, stg, C::STG_BYTES);
-            bulk_commit_group();
-          }
-        }
-      }
-      ok = ok && mbar_wait(bar_dkv_full, ni & 1, abort_flag);
+      const DkvItem it = dkv_item(a, item);
+      ok = mbar_wait(bar_out_full, ni & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
       const int key = it.s.tile * kTile + row;
-      const bool in = key < it.s.len;
       const long long krow = static_cast<long long>(it.s.start) + key;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const View& v = half ? a.dk : a.dv;
-        const float f = half ? a.scale : 1.f / kP;
-        T* out = static_cast<T*>(const_cast<void*>(v.p)) + krow * v.rs + it.hk * v.hs;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          float x[32];
-          tmem_ld32(tmem + lane_base + (half ? C::COL_DK : C::COL_DV) + c * 32, x);
-          tmem_wait_ld();
-          if (half == 1 && c == D / 32 - 1) {
-            tc_fence_before();
-            mbar_arrive(bar_dkv_free);
-          }
-          if (in)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(out + c * 32 + i * 8) =
-                  make_uint4(Elem<T>::pack(x[8 * i] * f, x[8 * i + 1] * f), Elem<T>::pack(x[8 * i + 2] * f, x[8 * i + 3] * f),
-                             Elem<T>::pack(x[8 * i + 4] * f, x[8 * i + 5] * f), Elem<T>::pack(x[8 * i + 6] * f, x[8 * i + 7] * f));
-        }
-      }
+      const bool in = key < it.s.len;
+      row_out<T, D>(static_cast<T*>(const_cast<void*>(a.dv.p)) + krow * a.dv.rs + it.hk * a.dv.hs,
+                    tmem + lane_base + C::COL_DV, in, 1.f / kP);
+      row_out<T, D>(static_cast<T*>(const_cast<void*>(a.dk.p)) + krow * a.dk.rs + it.hk * a.dk.hs,
+                    tmem + lane_base + C::COL_DK, in, a.scale);
+      tc_fence_before();
+      warp_arrive(bar_out_free, lane);
     }
-    if (lane == 0) bulk_wait_all();  // no reduction may read shared memory after the CTA has gone
   } else {
     // ------------------------------------------------------ P^T and dS^T
     const int w = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;  // w: which 32 queries
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_s = tmem + lane_base + C::COL_S + w * 32, t_dp = tmem + lane_base + C::COL_DP + w * 32;
+    const uint32_t t_dp = tmem + lane_base + C::COL_DP + w * 32;
     const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
     const int first = row - w * 32;  // on the diagonal: the first query at or behind the key
     const uint32_t behind = first <= 0 ? 0xffffffffu : (first >= 32 ? 0u : 0xffffffffu << first);
     bool ok = true;
     int g = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-      const BwdItem it = bwd_item(a, item);
+      const DkvItem it = dkv_item(a, item);
       for (int j = 0, in_head = 0; ok && j < it.n; ++j, ++g) {
-        const int st = g % C::QST;
+        const int sq = g % C::QST, so = g % C::OST, sb = g % C::NS;
         const bool diag = in_head == 0;
         if (++in_head == it.per) in_head = 0;
-        const float* ld = reinterpret_cast<const float*>(smem + C::OFF_LD + st * C::LD_BYTES) + w * 32;
-        ok = mbar_wait(bar_q_full + st, (g / C::QST) & 1, abort_flag) && mbar_wait(bar_s_full, g & 1, abort_flag);
+        const uint32_t t_s = tmem + lane_base + sb * 128 + w * 32;
+        const float* lse = reinterpret_cast<const float*>(smem + C::OFF_LSE + so * C::VEC) + w * 32;
+        const float* delta = reinterpret_cast<const float*>(smem + C::OFF_DELTA + sq * C::VEC) + w * 32;
+        ok = mbar_wait(bar_do_full + so, (g / C::OST) & 1, abort_flag) &&
+             mbar_wait(bar_s_full + sb, (g / C::NS) & 1, abort_flag);
         tc_fence_after();
         float p[32];
         tmem_ld32(t_s, p);
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const float4 l = *reinterpret_cast<const float4*>(ld + 4 * c);
+          const float4 l = *reinterpret_cast<const float4*>(lse + 4 * c);
           const float2 e0 = f2_unpack(f2_fma(f2_pack(p[4 * c], p[4 * c + 1]), sc2, f2_pack(l.x, l.y)));
           const float2 e1 = f2_unpack(f2_fma(f2_pack(p[4 * c + 2], p[4 * c + 3]), sc2, f2_pack(l.z, l.w)));
           p[4 * c] = ex2(e0.x);
@@ -462,26 +382,23 @@ __global__ void __launch_bounds__(704, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) p[i] = ((behind >> i) & 1u) ? p[i] : 0.f;
         }
-        {
-          uint32_t pk[16];
+        uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) pk[i] = Elem<T>::pack(p[2 * i] * kP, p[2 * i + 1] * kP);
-          tmem_st8(t_s, pk);
-          tmem_st8(t_s + 8, pk + 8);
-        }
+        for (int i = 0; i < 16; ++i) pk[i] = Elem<T>::pack(p[2 * i] * kP, p[2 * i + 1] * kP);
+        tmem_st8(t_s, pk);
+        tmem_st8(t_s + 8, pk + 8);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar_p_full);
+        warp_arrive(bar_p_full, lane);
 
-        ok = ok && mbar_wait(bar_dp_full, g & 1, abort_flag);
+        ok = ok && mbar_wait(bar_q_full + sq, (g / C::QST) & 1, abort_flag) && mbar_wait(bar_dp_full, g & 1, abort_flag);
         tc_fence_after();
         float dp[32];
         tmem_ld32(t_dp, dp);
         tmem_wait_ld();
-        uint32_t pk[16];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const float4 dl = *reinterpret_cast<const float4*>(ld + kTile + 4 * c);
+          const float4 dl = *reinterpret_cast<const float4*>(delta + 4 * c);
           float s0 = p[4 * c] * (dp[4 * c] - dl.x), s1 = p[4 * c + 1] * (dp[4 * c + 1] - dl.y);
           float s2 = p[4 * c + 2] * (dp[4 * c + 2] - dl.z), s3 = p[4 * c + 3] * (dp[4 * c + 3] - dl.w);
           if (diag) {  // a masked place stays 0 whatever dP holds there
@@ -494,15 +411,271 @@ __global__ void __launch_bounds__(704, 1)
           pk[2 * c] = Elem<T>::pack(s0, s1);
           pk[2 * c + 1] = Elem<T>::pack(s2, s3);
         }
-        if (g >= C::NDS) ok = ok && mbar_wait(bar_ds_free + g % C::NDS, (g / C::NDS - 1) & 1, abort_flag);
-        uint8_t* ds = smem + C::OFF_DS + (g % C::NDS) * C::DS_BYTES + (w >> 1) * kTile * 128;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(ds + sw128_offset(row, (w & 1) * 4 + c)) =
-              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-        fence_proxy_async_smem();
+        tmem_st8(t_dp, pk);
+        tmem_st8(t_dp + 8, pk + 8);
+        tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar_ds_full);
+        warp_arrive(bar_ds_full, lane);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 21) {
+    tc_fence_after();
+    tmem_dealloc<512>(tmem);
+  }
+}
+
+// ---------------------------------------------------------------------- dQ
+struct DqArgs {
+  const Slot* slots;
+  int n_items, Hq, G;
+  int n_tiles;
+  const float* ld;  // as DkvArgs
+  View dq;
+  float scale, scale_log2;
+};
+
+template <int D>
+struct DqCfg {
+  using G = TileGeo<D>;
+  static constexpr int QB = D >= 128 ? 1 : 2;   // Q/dO buffers
+  static constexpr int KST = D >= 128 ? 3 : 5;  // K stages
+  static constexpr int VST = D >= 128 ? 2 : 4;  // V stages
+  static constexpr int OB = D >= 128 ? 1 : 2;   // dQ buffers in TMEM
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_DO = OFF_Q + QB * G::BYTES;
+  static constexpr int OFF_K = OFF_DO + QB * G::BYTES;
+  static constexpr int OFF_V = OFF_K + KST * G::BYTES;
+  static constexpr int OFF_BAR = OFF_V + VST * G::BYTES;
+  static constexpr int N_BARS = 2 * QB + 2 * KST + 2 * VST + 2 + 2 + 2 * OB + 1;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
+  static constexpr int SMEM = OFF_MISC + 16;
+  static constexpr int COL_DP = 256, COL_DQ = 384;  // S: two buffers from 0; dQ + b * D
+  static_assert(SMEM <= 227 * 1024 && COL_DQ + OB * D <= 512, "shared memory and TMEM");
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    pa_bwd_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const DqArgs a) {
+  using C = DqCfg<D>;
+  using G = TileGeo<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* bar_q_full = bars;                     // [QB] Q and dO of an item
+  uint64_t* bar_q_free = bar_q_full + C::QB;       // [QB]
+  uint64_t* bar_k_full = bar_q_free + C::QB;       // [KST]
+  uint64_t* bar_k_free = bar_k_full + C::KST;      // [KST]
+  uint64_t* bar_v_full = bar_k_free + C::KST;      // [VST]
+  uint64_t* bar_v_free = bar_v_full + C::VST;      // [VST]
+  uint64_t* bar_s_full = bar_v_free + C::VST;      // [2]
+  uint64_t* bar_dp_full = bar_s_full + 2;
+  uint64_t* bar_ds_full = bar_dp_full + 1;
+  uint64_t* bar_out_full = bar_ds_full + 1;        // [OB]
+  uint64_t* bar_out_free = bar_out_full + C::OB;   // [OB]
+  uint64_t* bar_drain = bar_out_free + C::OB;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x, n_ctas = gridDim.x;
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < 2 * C::QB + 2 * C::KST + 2 * C::VST + 3; ++b) mbar_init(bars + b, 1);
+    mbar_init(bar_ds_full, kBwdComputeWarps);
+    for (int b = 0; b < C::OB; ++b) {
+      mbar_init(bar_out_full + b, 1);
+      mbar_init(bar_out_free + b, 4);
+    }
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 21) tmem_alloc<512>(tmem_slot);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 20) {
+    // -------------------------------------------------------------- producer
+    if (lane == 0) {
+      bool ok = true;
+      int g = 0, ni = 0, nv = 0;
+      for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
+        const int slot = item / a.Hq, h = item - slot * a.Hq;
+        const Slot s = a.slots[slot];
+        const int qb = ni % C::QB;
+        if (ni >= C::QB && !mbar_wait(bar_q_free + qb, (ni / C::QB - 1) & 1, abort_flag)) break;
+        mbar_arrive_expect_tx(bar_q_full + qb, 2 * G::BYTES);
+        load_tile<D>(smem + C::OFF_Q + qb * G::BYTES, &mq, bar_q_full + qb, h, s.start + s.tile * kTile);
+        load_tile<D>(smem + C::OFF_DO + qb * G::BYTES, &mdo, bar_q_full + qb, h, s.start + s.tile * kTile);
+        ++ni;
+        for (int j = 0; ok && j <= s.tile; ++j) {
+          const int row = s.start + j * kTile, sk = g % C::KST;
+          if (g >= C::KST && !mbar_wait(bar_k_free + sk, (g / C::KST - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar_k_full + sk, G::BYTES);
+          load_tile<D>(smem + C::OFF_K + sk * G::BYTES, &mk, bar_k_full + sk, h / a.G, row);
+          ++g;
+          const int sv = nv % C::VST;
+          if (nv >= C::VST && !mbar_wait(bar_v_free + sv, (nv / C::VST - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar_v_full + sv, G::BYTES);
+          load_tile<D>(smem + C::OFF_V + sv * G::BYTES, &mv, bar_v_full + sv, h / a.G, row);
+          ++nv;
+        }
+      }
+      if (*(volatile int*)abort_flag) {  // no copy may land after the CTA has gone
+        for (int i = ni > C::QB ? ni - C::QB : 0; i < ni; ++i) mbar_wait_drain(bar_q_full + i % C::QB, (i / C::QB) & 1);
+        for (int i = g > C::KST ? g - C::KST : 0; i < g; ++i) mbar_wait_drain(bar_k_full + i % C::KST, (i / C::KST) & 1);
+        for (int i = nv > C::VST ? nv - C::VST : 0; i < nv; ++i) mbar_wait_drain(bar_v_full + i % C::VST, (i / C::VST) & 1);
+      }
+    }
+  } else if (warp == 21) {
+    // ------------------------------------------------------------------ MMAs
+    constexpr uint32_t id_s = make_idesc<T>(128, 128, false, false);
+    constexpr uint32_t id_o = make_idesc<T>(128, D, false, true);
+    bool ok = true;
+    int g = 0, ni = 0;
+    for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
+      const Slot s = a.slots[item / a.Hq];
+      const int n = s.tile + 1, qb = ni % C::QB, ob = ni % C::OB;
+      ok = mbar_wait(bar_q_full + qb, (ni / C::QB) & 1, abort_flag);
+      if (!ok) break;
+      const Desc q_k = G::kmajor(smem_u32(smem + C::OFF_Q) + qb * G::BYTES);
+      const Desc do_k = G::kmajor(smem_u32(smem + C::OFF_DO) + qb * G::BYTES);
+      auto issue_s = [&](int j, int gg) -> bool {
+        const int st = gg % C::KST;
+        if (!mbar_wait(bar_k_full + st, (gg / C::KST) & 1, abort_flag)) return false;
+        // keys behind the sequence's last: masked in S, but dS = 0 must not meet a NaN in dS K
+        if (s.len - j * kTile < kTile) zero_rows<D>(smem + C::OFF_K + st * G::BYTES, s.len - j * kTile, lane);
+        tc_fence_after();
+        const Desc k_k = G::kmajor(smem_u32(smem + C::OFF_K) + st * G::BYTES);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16_ss(tmem + (gg & 1) * 128, q_k.at(G::kstep(kk)), k_k.at(G::kstep(kk)), id_s, kk > 0);
+          mma_commit(bar_s_full + (gg & 1));
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_dp = [&](int gg) -> bool {
+        const int st = gg % C::VST;
+        if (!mbar_wait(bar_v_full + st, (gg / C::VST) & 1, abort_flag)) return false;
+        tc_fence_after();
+        const Desc v_k = G::kmajor(smem_u32(smem + C::OFF_V) + st * G::BYTES);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16_ss(tmem + C::COL_DP, do_k.at(G::kstep(kk)), v_k.at(G::kstep(kk)), id_s, kk > 0);
+          mma_commit(bar_dp_full);
+          mma_commit(bar_v_free + st);
+        }
+        __syncwarp();
+        return true;
+      };
+      ok = issue_s(0, g) && issue_dp(g) && (n == 1 || issue_s(1, g + 1));
+      for (int j = 0; ok && j < n; ++j, ++g) {
+        ok = mbar_wait(bar_ds_full, g & 1, abort_flag);
+        if (ok && j == 0 && ni >= C::OB) ok = mbar_wait(bar_out_free + ob, (ni / C::OB - 1) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const int sk = g % C::KST;
+        const Desc k_mn = G::mnmajor(smem_u32(smem + C::OFF_K) + sk * G::BYTES);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_bf16_ts(tmem + C::COL_DQ + ob * D, tmem + C::COL_DP + (kk / 2) * 32 + (kk % 2) * 8, k_mn.at(G::mnstep(kk)),
+                        id_o, j > 0 || kk > 0);
+          mma_commit(bar_k_free + sk);
+        }
+        __syncwarp();
+        if (j + 1 < n && !(ok = issue_dp(g + 1))) break;     // over dS, behind its product
+        if (j + 2 < n && !(ok = issue_s(j + 2, g + 2))) break;  // dS of this step: its S has been read
+      }
+      if (ok && elect_one()) {
+        mma_commit(bar_q_free + qb);
+        mma_commit(bar_out_full + ob);
+      }
+    }
+    if (elect_one()) {  // every MMA has completed before TMEM is released
+      mma_commit(bar_drain);
+      mbar_wait_drain(bar_drain, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 16) {
+    // ------------------------------------------------------ read-out of dQ
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    bool ok = true;
+    int ni = 0;
+    for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
+      const int slot = item / a.Hq, h = item - slot * a.Hq, ob = ni % C::OB;
+      const Slot s = a.slots[slot];
+      ok = mbar_wait(bar_out_full + ob, (ni / C::OB) & 1, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const int i = s.tile * kTile + row;
+      row_out<T, D>(static_cast<T*>(const_cast<void*>(a.dq.p)) + (static_cast<long long>(s.start) + i) * a.dq.rs + h * a.dq.hs,
+                    tmem + lane_base + C::COL_DQ + ob * D, i < s.len, a.scale);
+      tc_fence_before();
+      warp_arrive(bar_out_free + ob, lane);
+    }
+  } else {
+    // ---------------------------------------------------------- P and dS
+    const int w = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;  // w: which 32 keys
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t t_dp = tmem + lane_base + C::COL_DP + w * 32;
+    const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
+    const int last = row - w * 32;  // on the diagonal: the last key that the query sees
+    const uint32_t before = last < 0 ? 0u : (last >= 31 ? 0xffffffffu : (2u << last) - 1u);
+    bool ok = true;
+    int g = 0;
+    for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
+      const int slot = item / a.Hq, h = item - slot * a.Hq;
+      const Slot s = a.slots[slot];
+      const float* ld = a.ld + (static_cast<long long>(h) * a.n_tiles + s.base + s.tile) * 2 * kTile;
+      const float neg_lse = ld[row], delta = ld[kTile + row];
+      const uint64_t l2 = f2_pack(neg_lse, neg_lse);
+      for (int j = 0; ok && j <= s.tile; ++j, ++g) {
+        const bool diag = j == s.tile;
+        ok = mbar_wait(bar_s_full + (g & 1), (g >> 1) & 1, abort_flag);
+        tc_fence_after();
+        float p[32];
+        tmem_ld32(tmem + lane_base + (g & 1) * 128 + w * 32, p);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 e = f2_unpack(f2_fma(f2_pack(p[2 * i], p[2 * i + 1]), sc2, l2));
+          p[2 * i] = ex2(e.x);
+          p[2 * i + 1] = ex2(e.y);
+        }
+        ok = ok && mbar_wait(bar_dp_full, g & 1, abort_flag);
+        tc_fence_after();
+        float dp[32];
+        tmem_ld32(t_dp, dp);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) dp[i] = p[i] * (dp[i] - delta);
+        if (diag) {  // a masked place is 0 whatever S and dP hold there
+#pragma unroll
+          for (int i = 0; i < 32; ++i) dp[i] = ((before >> i) & 1u) ? dp[i] : 0.f;
+        }
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk[i] = Elem<T>::pack(dp[2 * i], dp[2 * i + 1]);
+        tmem_st8(t_dp, pk);
+        tmem_st8(t_dp + 8, pk + 8);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(bar_ds_full, lane);
       }
     }
   }

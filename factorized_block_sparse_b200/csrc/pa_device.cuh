@@ -76,6 +76,13 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// One arrival for a warp, behind what every lane did before it (an arrival of
+// every lane would be 32 updates of one word in shared memory, one by one).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
 // A tile of 128 rows of D elements in shared memory: panels of up to 64
 // columns, a row of a panel 128 (D = 32: 64) bytes, swizzled over its width.
 template <int D>

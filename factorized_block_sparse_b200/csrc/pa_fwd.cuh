@@ -116,9 +116,9 @@ __global__ void __launch_bounds__(320, 1)
       mbar_init(bar_q_full + u, 1);
       mbar_init(bar_q_free + u, 1);
       mbar_init(bar_s_full + u, 1);
-      mbar_init(bar_p_full + u, 128);
+      mbar_init(bar_p_full + u, 4);
       mbar_init(bar_o_full + u, 1);
-      mbar_init(bar_o_free + u, 128);
+      mbar_init(bar_o_free + u, 4);
     }
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(bar_kv_full + s, 1);
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(320, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar_p_full + u);
+        warp_arrive(bar_p_full + u, lane);
         const float2 r0 = f2_unpack(f2_add(f2_add(rs[0], rs[1]), f2_add(rs[2], rs[3])));
         l_sum = l_sum * factor + (r0.x + r0.y);
       }
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(320, 1)
           tmem_wait_ld();
           if (p == G::PANELS - 1 && i == G::BOXW / 16 - 1) {
             tc_fence_before();
-            mbar_arrive(bar_o_free + u);
+            warp_arrive(bar_o_free + u, lane);
           }
           uint32_t w[8];
 #pragma unroll
