@@ -21,8 +21,8 @@
 // sums zeroed and converted, and leaves dq's last bits to their order.  Here
 // every sum has a fixed order, so the gradients are the same bits every time.
 //
-// P^T (dS^T, dS) goes back into TMEM over the scores (over dP), rounded, and
-// is the A operand of its product from there, so shared memory only holds
+// P^T, dS^T and dS go back into TMEM, rounded, over columns that have been
+// read, and are the A operand of their products from there, so shared memory only holds
 // what TMA brings.  One thread issues all MMAs of a CTA; they execute in
 // order, so a product behind another that reads its destination columns needs
 // no wait.
@@ -118,6 +118,11 @@ struct DkvCfg {
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
   static constexpr int SMEM = OFF_MISC + 16;
   static constexpr int COL_DP = NS * 128, COL_DV = COL_DP + 128, COL_DK = COL_DV + D;
+  // P^T takes the first 16 of each group's 32 columns of its S^T buffer.  With
+  // two buffers dS^T takes the other 16, so dP^T is free once it has been read
+  // and the next one is under way before dK; with one buffer dS^T goes over
+  // dP^T, so that the next S^T only waits for dV.
+  static constexpr bool DS_IN_S = NS == 2;
   static_assert(SMEM <= 227 * 1024 && COL_DK + D <= 512, "shared memory and TMEM");
 };
 
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int cta = blockIdx.x, n_ctas = gridDim.x;
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2 * C::KVB + 2 * C::QST + 2 * C::OST + C::NS; ++b) mbar_init(bars + b, 1);
@@ -232,12 +237,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     int g = 0, ni = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
-      const DkvItem it = dkv_item(a, item);
+      DkvItem it = dkv_item(a, item);
+      it.s = uniform(it.s);
+      it.per = uniform(it.per);
+      it.n = uniform(it.n);
       const int kb = ni % C::KVB;
       uint8_t* sK = smem + C::OFF_K + kb * G::BYTES;
       uint8_t* sV = smem + C::OFF_V + kb * G::BYTES;
       const Desc k_k = G::kmajor(smem_u32(sK)), v_k = G::kmajor(smem_u32(sV));
-      ok = mbar_wait(bar_kv_full + kb, (ni / C::KVB) & 1, abort_flag);
+      ok = mbar_wait_warp(bar_kv_full + kb, (ni / C::KVB) & 1, abort_flag);
       if (!ok) break;
       const int keys = it.s.len - it.s.tile * kTile;
       if (keys < kTile) {
@@ -248,7 +256,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // S^T (dP^T) of the item's next step, global step gg; a last, partial query tile is zeroed behind its rows first
       auto issue_s = [&](int gg) -> bool {
         const int st = gg % C::QST, sb = gg % C::NS;
-        if (!mbar_wait(bar_q_full + st, (gg / C::QST) & 1, abort_flag)) return false;
+        if (!mbar_wait_warp(bar_q_full + st, (gg / C::QST) & 1, abort_flag)) return false;
         uint8_t* sQ = smem + C::OFF_Q + st * G::BYTES;
         if (rows_s < kTile) zero_rows<D>(sQ, rows_s, lane);
         rows_s -= kTile;
@@ -266,7 +274,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       };
       auto issue_dp = [&](int gg) -> bool {
         const int st = gg % C::OST;
-        if (!mbar_wait(bar_do_full + st, (gg / C::OST) & 1, abort_flag)) return false;
+        if (!mbar_wait_warp(bar_do_full + st, (gg / C::OST) & 1, abort_flag)) return false;
         uint8_t* sDO = smem + C::OFF_DO + st * G::BYTES;
         if (rows_p < kTile) zero_rows<D>(sDO, rows_p, lane);
         rows_p -= kTile;
@@ -285,8 +293,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       ok = issue_s(g) && issue_dp(g) && (C::NS == 1 || it.n == 1 || issue_s(g + 1));
       for (int j = 0; ok && j < it.n; ++j, ++g) {
         const int sq = g % C::QST, so = g % C::OST;
-        ok = mbar_wait(bar_p_full, g & 1, abort_flag);
-        if (ok && j == 0 && ni > 0) ok = mbar_wait(bar_out_free, (ni - 1) & 1, abort_flag);
+        ok = mbar_wait_warp(bar_p_full, g & 1, abort_flag);
+        if (ok && j == 0 && ni > 0) ok = mbar_wait_warp(bar_out_free, (ni - 1) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         const Desc do_mn = G::mnmajor(smem_u32(smem + C::OFF_DO) + so * G::BYTES);
@@ -298,19 +306,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           mma_commit(bar_do_free + so);
         }
         __syncwarp();
-        if (j + C::NS < it.n && !(ok = issue_s(g + C::NS))) break;  // over the columns of P^T, behind its product
-        if (!(ok = mbar_wait(bar_ds_full, g & 1, abort_flag))) break;
+        if (!C::DS_IN_S && j + 1 < it.n && !(ok = issue_s(g + 1))) break;  // over P^T, behind its product
+        if (!(ok = mbar_wait_warp(bar_ds_full, g & 1, abort_flag))) break;
+        if (C::DS_IN_S && j + 1 < it.n && !(ok = issue_dp(g + 1))) break;
         tc_fence_after();
         const Desc q_mn = G::mnmajor(smem_u32(smem + C::OFF_Q) + sq * G::BYTES);
+        const uint32_t t_ds = tmem + (C::DS_IN_S ? (g % C::NS) * 128 + 16 : C::COL_DP);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_bf16_ts(tmem + C::COL_DK, tmem + C::COL_DP + (kk / 2) * 32 + (kk % 2) * 8, q_mn.at(G::mnstep(kk)), id_o,
+            mma_bf16_ts(tmem + C::COL_DK, t_ds + (kk / 2) * 32 + (kk % 2) * 8, q_mn.at(G::mnstep(kk)), id_o,
                         j > 0 || kk > 0);
           mma_commit(bar_q_free + sq);
         }
         __syncwarp();
-        if (j + 1 < it.n) ok = issue_dp(g + 1);
+        if (C::DS_IN_S) {
+          if (j + 2 < it.n) ok = issue_s(g + 2);  // over P^T and dS^T, behind their products
+        } else if (j + 1 < it.n) {
+          ok = issue_dp(g + 1);  // over dS^T, behind its product
+        }
       }
       if (ok && elect_one()) {
         mma_commit(bar_kv_free + kb);
@@ -411,8 +425,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           pk[2 * c] = Elem<T>::pack(s0, s1);
           pk[2 * c + 1] = Elem<T>::pack(s2, s3);
         }
-        tmem_st8(t_dp, pk);
-        tmem_st8(t_dp + 8, pk + 8);
+        const uint32_t t_ds = C::DS_IN_S ? t_s + 16 : t_dp;
+        tmem_st8(t_ds, pk);
+        tmem_st8(t_ds + 8, pk + 8);
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(bar_ds_full, lane);
@@ -479,7 +494,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int cta = blockIdx.x, n_ctas = gridDim.x;
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2 * C::QB + 2 * C::KST + 2 * C::VST + 3; ++b) mbar_init(bars + b, 1);
@@ -544,15 +559,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     int g = 0, ni = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
-      const Slot s = a.slots[item / a.Hq];
+      const Slot s = uniform(a.slots[item / a.Hq]);
       const int n = s.tile + 1, qb = ni % C::QB, ob = ni % C::OB;
-      ok = mbar_wait(bar_q_full + qb, (ni / C::QB) & 1, abort_flag);
+      ok = mbar_wait_warp(bar_q_full + qb, (ni / C::QB) & 1, abort_flag);
       if (!ok) break;
       const Desc q_k = G::kmajor(smem_u32(smem + C::OFF_Q) + qb * G::BYTES);
       const Desc do_k = G::kmajor(smem_u32(smem + C::OFF_DO) + qb * G::BYTES);
       auto issue_s = [&](int j, int gg) -> bool {
         const int st = gg % C::KST;
-        if (!mbar_wait(bar_k_full + st, (gg / C::KST) & 1, abort_flag)) return false;
+        if (!mbar_wait_warp(bar_k_full + st, (gg / C::KST) & 1, abort_flag)) return false;
         // keys behind the sequence's last: masked in S, but dS = 0 must not meet a NaN in dS K
         if (s.len - j * kTile < kTile) zero_rows<D>(smem + C::OFF_K + st * G::BYTES, s.len - j * kTile, lane);
         tc_fence_after();
@@ -568,7 +583,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       };
       auto issue_dp = [&](int gg) -> bool {
         const int st = gg % C::VST;
-        if (!mbar_wait(bar_v_full + st, (gg / C::VST) & 1, abort_flag)) return false;
+        if (!mbar_wait_warp(bar_v_full + st, (gg / C::VST) & 1, abort_flag)) return false;
         tc_fence_after();
         const Desc v_k = G::kmajor(smem_u32(smem + C::OFF_V) + st * G::BYTES);
         if (elect_one()) {
@@ -583,22 +598,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       };
       ok = issue_s(0, g) && issue_dp(g) && (n == 1 || issue_s(1, g + 1));
       for (int j = 0; ok && j < n; ++j, ++g) {
-        ok = mbar_wait(bar_ds_full, g & 1, abort_flag);
-        if (ok && j == 0 && ni >= C::OB) ok = mbar_wait(bar_out_free + ob, (ni / C::OB - 1) & 1, abort_flag);
+        ok = mbar_wait_warp(bar_ds_full, g & 1, abort_flag);
+        if (ok && j == 0 && ni >= C::OB) ok = mbar_wait_warp(bar_out_free + ob, (ni / C::OB - 1) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
+        if (j + 1 < n && !(ok = issue_dp(g + 1))) break;
         const int sk = g % C::KST;
         const Desc k_mn = G::mnmajor(smem_u32(smem + C::OFF_K) + sk * G::BYTES);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_bf16_ts(tmem + C::COL_DQ + ob * D, tmem + C::COL_DP + (kk / 2) * 32 + (kk % 2) * 8, k_mn.at(G::mnstep(kk)),
+            mma_bf16_ts(tmem + C::COL_DQ + ob * D, tmem + (g & 1) * 128 + (kk / 2) * 32 + (kk % 2) * 8, k_mn.at(G::mnstep(kk)),
                         id_o, j > 0 || kk > 0);
           mma_commit(bar_k_free + sk);
         }
         __syncwarp();
-        if (j + 1 < n && !(ok = issue_dp(g + 1))) break;     // over dS, behind its product
-        if (j + 2 < n && !(ok = issue_s(j + 2, g + 2))) break;  // dS of this step: its S has been read
+        if (j + 2 < n && !(ok = issue_s(j + 2, g + 2))) break;  // over dS, behind its product
       }
       if (ok && elect_one()) {
         mma_commit(bar_q_free + qb);
@@ -649,7 +664,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ok = mbar_wait(bar_s_full + (g & 1), (g >> 1) & 1, abort_flag);
         tc_fence_after();
         float p[32];
-        tmem_ld32(tmem + lane_base + (g & 1) * 128 + w * 32, p);
+        const uint32_t t_s = tmem + lane_base + (g & 1) * 128 + w * 32;
+        tmem_ld32(t_s, p);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -671,8 +687,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) pk[i] = Elem<T>::pack(dp[2 * i], dp[2 * i + 1]);
-        tmem_st8(t_dp, pk);
-        tmem_st8(t_dp + 8, pk + 8);
+        tmem_st8(t_s, pk);
+        tmem_st8(t_s + 8, pk + 8);
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(bar_ds_full, lane);

@@ -76,6 +76,34 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// mbar_wait by a whole warp, with one answer for all lanes that the compiler
+// knows to be one: what follows it stays in uniform registers, which the
+// MMA instructions take their operands from.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  uint32_t spins = 0;
+  for (;;) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_hint(bar, parity, 20000u))) return true;
+    if (((++spins) & 15u) == 0) {
+      bool stop = *(volatile int*)abort || *(volatile int*)&g_status == kStatusTimeout;
+      if (!stop && clock64() - t0 > kWaitCycles) {
+        atomicExch(&g_status, kStatusTimeout);
+        stop = true;
+      }
+      if (__any_sync(0xffffffffu, stop)) {
+        *(volatile int*)abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ Slot uniform(const Slot& s) {
+  return Slot{uniform(s.start), uniform(s.len), uniform(s.tile), uniform(s.base)};
+}
+
 // One arrival for a warp, behind what every lane did before it (an arrival of
 // every lane would be 32 updates of one word in shared memory, one by one).
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {

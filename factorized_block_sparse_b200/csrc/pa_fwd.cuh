@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(320, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int cta = blockIdx.x, n_ctas = gridDim.x;
   if (threadIdx.x == 0) {
     for (int u = 0; u < 2; ++u) {
@@ -185,12 +185,15 @@ __global__ void __launch_bounds__(320, 1)
       __syncwarp();
     };
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-      const FwdItem it = fwd_item(a, item);
+      FwdItem it = fwd_item(a, item);
+      it.s = uniform(it.s);
+      it.n[0] = uniform(it.n[0]);
+      it.n[1] = uniform(it.n[1]);
       const int n = max(it.n[0], it.n[1]);
-      ok = mbar_wait(bar_kv_full + ring % C::STAGES, (ring / C::STAGES) & 1, abort_flag);
+      ok = mbar_wait_warp(bar_kv_full + ring % C::STAGES, (ring / C::STAGES) & 1, abort_flag);
       for (int u = 0; ok && u < 2; ++u)
         if (it.n[u] > 0) {
-          ok = mbar_wait(bar_q_full + u, nu[u] & 1, abort_flag);
+          ok = mbar_wait_warp(bar_q_full + u, nu[u] & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
           issue_s(u, ring % C::STAGES);
@@ -199,16 +202,16 @@ __global__ void __launch_bounds__(320, 1)
       if (ok && elect_one()) mma_commit(bar_kv_free + ring % C::STAGES);
       for (int j = 0; ok && j < n; ++j, ring += 2) {
         const int sv = (ring + 1) % C::STAGES, sk = (ring + 2) % C::STAGES;
-        ok = mbar_wait(bar_kv_full + sv, ((ring + 1) / C::STAGES) & 1, abort_flag);
+        ok = mbar_wait_warp(bar_kv_full + sv, ((ring + 1) / C::STAGES) & 1, abort_flag);
         if (!ok) break;
         const int tail = it.s.len - j * kTile;  // keys of this tile
         if (tail < kTile) zero_rows<D>(sKV + sv * G::BYTES, tail, lane);
-        if (j + 1 < n) ok = mbar_wait(bar_kv_full + sk, ((ring + 2) / C::STAGES) & 1, abort_flag);
+        if (j + 1 < n) ok = mbar_wait_warp(bar_kv_full + sk, ((ring + 2) / C::STAGES) & 1, abort_flag);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           if (!ok || j >= it.n[u]) continue;
-          ok = mbar_wait(bar_p_full + u, np[u] & 1, abort_flag);
-          if (ok && j == 0 && nu[u] > 0) ok = mbar_wait(bar_o_free + u, (nu[u] - 1) & 1, abort_flag);
+          ok = mbar_wait_warp(bar_p_full + u, np[u] & 1, abort_flag);
+          if (ok && j == 0 && nu[u] > 0) ok = mbar_wait_warp(bar_o_free + u, (nu[u] - 1) & 1, abort_flag);
           if (!ok) break;
           ++np[u];
           tc_fence_after();
