@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "pa_internal.h"
 #include "sa_device.cuh"
 
@@ -182,6 +184,50 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// 2^x of a pair on the FMA pipe: x = n + f with n the nearest integer, |f| <=
+// 1/2, and 2^f by the polynomial of least relative error (Remez) of degree 3
+// for bf16 weights (7.5e-5, next to their rounding of 2^-8) and 4 for fp16
+// (2.6e-6, next to 2^-11).  n + 127 sits in the low bits of x + 1.5 2^23 + 127,
+// which shifted up are the float 2^n; at n = -127 they are 0, so everything
+// below 2^-126.5, and a masked -inf, gives exactly 0.  NaN stays NaN.
+template <typename T>
+__device__ __forceinline__ float2 ex2_fma(uint64_t x2) {
+  constexpr float kMagic = 12582912.f + 127.f;
+  const float2 xi = f2_unpack(x2);
+  float2 x;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x.x) : "f"(xi.x), "f"(-127.f));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x.y) : "f"(xi.y), "f"(-127.f));
+  const uint64_t xp = f2_pack(x.x, x.y);
+  const uint64_t t = f2_add(xp, f2_pack(kMagic, kMagic));
+  const uint64_t r = f2_add(t, f2_pack(-kMagic, -kMagic));
+  const uint64_t f = f2_fma(r, f2_pack(-1.f, -1.f), xp);
+  auto c = [](float v) { return f2_pack(v, v); };
+  uint64_t p;
+  if constexpr (std::is_same<T, __half>::value) {
+    p = f2_fma(f, c(0.009570102207362652f), c(0.05591785907745361f));
+    p = f2_fma(p, f, c(0.240247443318367f));
+    p = f2_fma(p, f, c(0.6931217908859253f));
+    p = f2_fma(p, f, c(0.9999992847442627f));
+  } else {
+    p = f2_fma(f, c(0.0551716685295105f), c(0.2426111251115799f));
+    p = f2_fma(p, f, c(0.6932609677314758f));
+    p = f2_fma(p, f, c(0.9999280571937561f));
+  }
+  const float2 tf = f2_unpack(t);
+  const float s0 = __uint_as_float(__float_as_uint(tf.x) << 23), s1 = __uint_as_float(__float_as_uint(tf.y) << 23);
+  return f2_unpack(f2_mul(p, f2_pack(s0, s1)));
+}
+
+// 2^x of pair i of a row's run of pairs: POLY of every 8 pairs on the FMA
+// pipe, the others by ex2 (16 a clock and SM).
+template <typename T, int POLY>
+__device__ __forceinline__ float2 ex2_pair(uint64_t x2, int i) {
+  constexpr uint32_t kPick = POLY == 0 ? 0u : (POLY == 1 ? 0x10u : (POLY == 2 ? 0x44u : (POLY == 3 ? 0x92u : 0xaau)));
+  if ((kPick >> (i & 7)) & 1u) return ex2_fma<T>(x2);
+  const float2 x = f2_unpack(x2);
+  return make_float2(ex2(x.x), ex2(x.y));
 }
 
 // Keeps v[i] for i <= last (i in [0, 32)), sets the others to `fill`.

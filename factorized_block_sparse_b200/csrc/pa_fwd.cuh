@@ -26,6 +26,8 @@
 
 namespace pa {
 
+constexpr int kFwdPoly = 2;
+
 enum Pairing : int { kSingle = 0, kHeads = 1, kTiles = 2 };
 
 struct FwdArgs {
@@ -296,10 +298,9 @@ __global__ void __launch_bounds__(320, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 e = f2_unpack(f2_fma(f2_pack(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc2, ng2));
-            const float p0 = ex2(e.x), p1 = ex2(e.y);
-            rs[i & 3] = f2_add(rs[i & 3], f2_pack(p0, p1));
-            pk[i] = Elem<T>::pack(p0, p1);
+            const float2 e = ex2_pair<T, kFwdPoly>(f2_fma(f2_pack(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc2, ng2), i);
+            rs[i & 3] = f2_add(rs[i & 3], f2_pack(e.x, e.y));
+            pk[i] = Elem<T>::pack(e.x, e.y);
           }
           tmem_st8(t_s + c * 16, pk);
           tmem_st8(t_s + c * 16 + 8, pk + 8);
