@@ -38,7 +38,10 @@
 
 namespace pa {
 
-constexpr int kDkvPoly = 2, kDqPoly = 2;
+template <int D>
+constexpr int kDkvPoly = D <= 64 ? 1 : 3;
+template <int D>
+constexpr int kDqPoly = D <= 64 ? 1 : 0;
 constexpr int kBwdThreads = 704, kBwdComputeWarps = 16;
 
 // TPR threads a row, 8 columns each.
@@ -386,9 +389,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const float4 l = *reinterpret_cast<const float4*>(lse + 4 * c);
-          const float2 e0 = ex2_pair<T, kDkvPoly>(f2_fma(f2_pack(p[4 * c], p[4 * c + 1]), sc2, f2_pack(l.x, l.y)), 2 * c);
+          const float2 e0 = ex2_pair<T, kDkvPoly<D>>(f2_fma(f2_pack(p[4 * c], p[4 * c + 1]), sc2, f2_pack(l.x, l.y)), 2 * c);
           const float2 e1 =
-              ex2_pair<T, kDkvPoly>(f2_fma(f2_pack(p[4 * c + 2], p[4 * c + 3]), sc2, f2_pack(l.z, l.w)), 2 * c + 1);
+              ex2_pair<T, kDkvPoly<D>>(f2_fma(f2_pack(p[4 * c + 2], p[4 * c + 3]), sc2, f2_pack(l.z, l.w)), 2 * c + 1);
           p[4 * c] = e0.x;
           p[4 * c + 1] = e0.y;
           p[4 * c + 2] = e1.x;
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float2 e = ex2_pair<T, kDqPoly>(f2_fma(f2_pack(p[2 * i], p[2 * i + 1]), sc2, l2), i);
+          const float2 e = ex2_pair<T, kDqPoly<D>>(f2_fma(f2_pack(p[2 * i], p[2 * i + 1]), sc2, l2), i);
           p[2 * i] = e.x;
           p[2 * i + 1] = e.y;
         }

@@ -10,23 +10,28 @@
 //   O_u += P V        P read from TMEM, fp32 accumulator in TMEM
 // and o = O / sum at the end.  While one unit's softmax runs, the tensor core
 // works on the other unit.  The running maximum moves only when it grows by
-// more than 2^8, so O is rescaled rarely; numerator and denominator use the
-// same maximum, so the quotient is exact up to rounding.
+// more than 2^8, so O is rescaled rarely; numerator and
+// denominator use the same maximum, so the quotient is exact up to rounding.
 //
-// Roles (320 threads): warps 0..3 the softmax and epilogue of unit 0, warps
+// TMEM columns: S_u at 128 u.  D <= 64: P_u at 256 + 64 u and O_u at 384 + D u,
+// so the next S is computed while the softmax works on this one (which is in
+// registers by then), and each unit has an issuing warp of its own.  D = 128 has no room for that: P_u over S_u, O_u at 256
+// + 128 u.  There order makes waits unnecessary: one thread's MMAs execute in
+// order, so S_u(j+1) behind PV_u(j) cannot overwrite a P_u(j) still being read,
+// and the commit behind S_u(j+1) also says that O_u holds PV_u(j), which is
+// what a rescale needs.
+//
+// Roles (352 threads): warps 0..3 the softmax and epilogue of unit 0, warps
 // 4..7 of unit 1 (thread = query row = TMEM lane 32 (w mod 4) + lane), warp 8
-// lane 0 the TMA producer, warp 9 TMEM and the MMAs.  TMEM columns: S_u (and
-// P_u) at 128 u, O_u at 256 + D u.  Order makes three waits unnecessary: MMAs
-// of one thread execute in order, so S_u(j+1) after PV_u(j) cannot overwrite
-// a P_u(j) still being read, and the commit behind S_u(j+1) also says that O_u
-// holds PV_u(j), which is what a rescale needs.
+// lane 0 the TMA producer, warps 9 and 10 the MMAs of units 0 and 1.
 #pragma once
 
 #include "pa_device.cuh"
 
 namespace pa {
 
-constexpr int kFwdPoly = 2;
+template <int D>
+constexpr int kFwdPoly = D <= 64 ? 2 : 0;
 
 enum Pairing : int { kSingle = 0, kHeads = 1, kTiles = 2 };
 
@@ -51,11 +56,13 @@ struct FwdCfg {
   static constexpr int OFF_KV = 2 * G::BYTES;
   static constexpr int OFF_STG = OFF_KV + STAGES * G::BYTES;
   static constexpr int OFF_BAR = OFF_STG + 8 * STG_BYTES;
-  static constexpr int N_BARS = 2 + 2 + 2 * STAGES + 2 * 4 + 1;
+  static constexpr int N_BARS = 2 + 2 + 2 * STAGES + 2 * 5 + 2;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
   static constexpr int SMEM = OFF_MISC + 16;
-  static constexpr int COL_O = 256;
-  static constexpr int THREADS = 320;
+  static constexpr bool SEP = D <= 64;  // P in columns of its own
+  static constexpr int COL_P = SEP ? 256 : 0, P_STRIDE = SEP ? 64 : 128;
+  static constexpr int COL_O = SEP ? 384 : 256;
+  static constexpr int THREADS = 352;
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -90,7 +97,7 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int item) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(352, 1)
     pa_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, const FwdArgs a) {
   using C = FwdCfg<D>;
@@ -103,11 +110,12 @@ __global__ void __launch_bounds__(320, 1)
   uint64_t* bar_q_free = bars + 2;                    // [2]
   uint64_t* bar_kv_full = bars + 4;                   // [STAGES]
   uint64_t* bar_kv_free = bar_kv_full + C::STAGES;    // [STAGES]
-  uint64_t* bar_s_full = bar_kv_free + C::STAGES;     // [2] S of a tile (and PV of the tile before)
-  uint64_t* bar_p_full = bar_s_full + 2;              // [2] P of a tile
-  uint64_t* bar_o_full = bar_p_full + 2;              // [2] the item's last PV
-  uint64_t* bar_o_free = bar_o_full + 2;              // [2] the epilogue has read O
-  uint64_t* bar_drain = bar_o_free + 2;
+  uint64_t* bar_s_full = bar_kv_free + C::STAGES;     // [2] S of a tile
+  uint64_t* bar_s_free = bar_s_full + 2;              // [2] S has been read (SEP)
+  uint64_t* bar_p_full = bar_s_free + 2;              // [2] P of a tile
+  uint64_t* bar_pv_done = bar_p_full + 2;             // [2] PV of a tile
+  uint64_t* bar_o_free = bar_pv_done + 2;             // [2] the epilogue has read O
+  uint64_t* bar_drain = bar_o_free + 2;               // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
 
@@ -118,15 +126,16 @@ __global__ void __launch_bounds__(320, 1)
       mbar_init(bar_q_full + u, 1);
       mbar_init(bar_q_free + u, 1);
       mbar_init(bar_s_full + u, 1);
+      mbar_init(bar_s_free + u, 4);
       mbar_init(bar_p_full + u, 4);
-      mbar_init(bar_o_full + u, 1);
+      mbar_init(bar_pv_done + u, 1);
       mbar_init(bar_o_free + u, 4);
+      mbar_init(bar_drain + u, 1);
     }
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(bar_kv_full + s, 1);
-      mbar_init(bar_kv_free + s, 1);
+      mbar_init(bar_kv_free + s, C::SEP ? 2 : 1);  // commits of each issuing warp
     }
-    mbar_init(bar_drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -169,77 +178,142 @@ __global__ void __launch_bounds__(320, 1)
           mbar_wait_drain(bar_kv_full + h % C::STAGES, (h / C::STAGES) & 1);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp >= 9) {
     // ------------------------------------------------------------------ MMAs
     constexpr uint32_t id_s = make_idesc<T>(128, 128, false, false);
     constexpr uint32_t id_o = make_idesc<T>(128, D, false, true);
     bool ok = true;
-    int ring = 0, nu[2] = {0, 0}, np[2] = {0, 0};  // K/V tiles, items and P tiles of each unit so far
-    const uint32_t q_base = smem_u32(sQ);
-    auto issue_s = [&](int u, int st) {
-      const Desc qd = G::kmajor(q_base + u * G::BYTES), kd = G::kmajor(smem_u32(sKV) + st * G::BYTES);
+    int ring = 0;  // K/V tiles so far
+    auto full = [&](int r) { return mbar_wait_warp(bar_kv_full + r % C::STAGES, (r / C::STAGES) & 1, abort_flag); };
+    auto q_desc = [&](int u) { return G::kmajor(smem_u32(sQ) + u * G::BYTES); };
+    // S of unit u's next tile from the K tile at ring position r
+    auto issue_s = [&](int u, int r) {
+      const Desc q_k = q_desc(u), k_k = G::kmajor(smem_u32(sKV) + r % C::STAGES * G::BYTES);
+      tc_fence_after();
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16_ss(tmem + u * 128, qd.at(G::kstep(kk)), kd.at(G::kstep(kk)), id_s, kk > 0);
+          mma_bf16_ss(tmem + u * 128, q_k.at(G::kstep(kk)), k_k.at(G::kstep(kk)), id_s, kk > 0);
         mma_commit(bar_s_full + u);
       }
       __syncwarp();
     };
-    for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-      FwdItem it = fwd_item(a, item);
-      it.s = uniform(it.s);
-      it.n[0] = uniform(it.n[0]);
-      it.n[1] = uniform(it.n[1]);
-      const int n = max(it.n[0], it.n[1]);
-      ok = mbar_wait_warp(bar_kv_full + ring % C::STAGES, (ring / C::STAGES) & 1, abort_flag);
-      for (int u = 0; ok && u < 2; ++u)
-        if (it.n[u] > 0) {
-          ok = mbar_wait_warp(bar_q_full + u, nu[u] & 1, abort_flag);
+    // O of unit u, from the V tile at ring position r; keys behind the sequence's last are zeroed in it
+    auto issue_pv = [&](int u, int r, bool first) {
+      const Desc v_mn = G::mnmajor(smem_u32(sKV) + r % C::STAGES * G::BYTES);
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_bf16_ts(tmem + C::COL_O + u * D, tmem + C::COL_P + u * C::P_STRIDE + kk * 8, v_mn.at(G::mnstep(kk)), id_o,
+                      (!first || kk > 0));
+        mma_commit(bar_pv_done + u);
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) mma_commit(bar);
+      __syncwarp();
+    };
+    if constexpr (C::SEP) {
+      const int u = warp - 9;
+      int ni = 0, ns = 0, np = 0;  // items, S and PV products of this unit so far
+      // a tile that only the other unit needs
+      auto skip = [&](int r) -> bool {
+        if (!full(r)) return false;
+        if (lane == 0) mbar_arrive(bar_kv_free + r % C::STAGES);
+        __syncwarp();
+        return true;
+      };
+      for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
+        const FwdItem it = fwd_item(a, item);
+        const int n = uniform(it.n[u]), n_all = uniform(max(it.n[0], it.n[1])), len = uniform(it.s.len);
+        if (n > 0) {
+          ok = full(ring) && mbar_wait_warp(bar_q_full + u, ni & 1, abort_flag) &&
+               (ns == 0 || mbar_wait_warp(bar_s_free + u, (ns - 1) & 1, abort_flag));
           if (!ok) break;
-          tc_fence_after();
-          issue_s(u, ring % C::STAGES);
-          if (it.n[u] == 1 && elect_one()) mma_commit(bar_q_free + u);
+          issue_s(u, ring);
+          ++ns;
+          commit(bar_kv_free + ring % C::STAGES);
+          if (n == 1) commit(bar_q_free + u);
+        } else {
+          ok = skip(ring);
         }
-      if (ok && elect_one()) mma_commit(bar_kv_free + ring % C::STAGES);
-      for (int j = 0; ok && j < n; ++j, ring += 2) {
-        const int sv = (ring + 1) % C::STAGES, sk = (ring + 2) % C::STAGES;
-        ok = mbar_wait_warp(bar_kv_full + sv, ((ring + 1) / C::STAGES) & 1, abort_flag);
-        if (!ok) break;
-        const int tail = it.s.len - j * kTile;  // keys of this tile
-        if (tail < kTile) zero_rows<D>(sKV + sv * G::BYTES, tail, lane);
-        if (j + 1 < n) ok = mbar_wait_warp(bar_kv_full + sk, ((ring + 2) / C::STAGES) & 1, abort_flag);
+        for (int j = 0; ok && j < n_all; ++j, ring += 2) {
+          const int sv = (ring + 1) % C::STAGES;
+          if (j < n) {
+            if (j + 1 < n) {
+              ok = full(ring + 2) && mbar_wait_warp(bar_s_free + u, (ns - 1) & 1, abort_flag);
+              if (!ok) break;
+              issue_s(u, ring + 2);
+              ++ns;
+              commit(bar_kv_free + (ring + 2) % C::STAGES);
+              if (j + 2 == n) commit(bar_q_free + u);
+            }
+            if (!(ok = full(ring + 1))) break;
+            if (len - j * kTile < kTile) zero_rows<D>(sKV + sv * G::BYTES, len - j * kTile, lane);
+            ok = mbar_wait_warp(bar_p_full + u, np & 1, abort_flag) &&
+                 (j > 0 || ni == 0 || mbar_wait_warp(bar_o_free + u, (ni - 1) & 1, abort_flag));
+            if (!ok) break;
+            ++np;
+            issue_pv(u, ring + 1, j == 0);
+            commit(bar_kv_free + sv);
+          } else {
+            ok = skip(ring + 1);
+          }
+          if (ok && j + 1 < n_all && j + 1 >= n) ok = skip(ring + 2);
+        }
+        if (n > 0) ++ni;
+      }
+    } else if (warp == 9) {
+      // One warp for both units, in strict turn: with a warp each (measured: 0.43 -> 0.52 ms for ten ragged sequences,
+      // 32 / 8 heads of 128) their products mix, both finish late and both softmaxes then run at the same time.
+      int ni[2] = {0, 0}, np[2] = {0, 0};  // items and PV products of each unit so far
+      for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
+        const FwdItem it = fwd_item(a, item);
+        const int n0 = uniform(it.n[0]), n1 = uniform(it.n[1]), n = max(n0, n1), len = uniform(it.s.len);
+        ok = full(ring);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          if (!ok || j >= it.n[u]) continue;
-          ok = mbar_wait_warp(bar_p_full + u, np[u] & 1, abort_flag);
-          if (ok && j == 0 && nu[u] > 0) ok = mbar_wait_warp(bar_o_free + u, (nu[u] - 1) & 1, abort_flag);
+          const int nu = u ? n1 : n0;
+          if (!ok || nu == 0) continue;
+          ok = mbar_wait_warp(bar_q_full + u, ni[u] & 1, abort_flag);
           if (!ok) break;
-          ++np[u];
-          tc_fence_after();
-          const Desc vd = G::mnmajor(smem_u32(sKV) + sv * G::BYTES);
-          if (elect_one()) {
+          issue_s(u, ring);
+          if (nu == 1) commit(bar_q_free + u);
+        }
+        if (!ok) break;
+        commit(bar_kv_free + ring % C::STAGES);
+        for (int j = 0; ok && j < n; ++j, ring += 2) {
+          const int sv = (ring + 1) % C::STAGES, sk = (ring + 2) % C::STAGES;
+          ok = full(ring + 1) && (j + 1 == n || full(ring + 2));
+          if (!ok) break;
+          if (len - j * kTile < kTile) zero_rows<D>(sKV + sv * G::BYTES, len - j * kTile, lane);
 #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_bf16_ts(tmem + C::COL_O + u * D, tmem + u * 128 + kk * 8, vd.at(G::mnstep(kk)), id_o, (j > 0 || kk > 0));
-            if (j + 1 == it.n[u]) mma_commit(bar_o_full + u);
+          for (int u = 0; u < 2; ++u) {
+            const int nu = u ? n1 : n0;
+            if (!ok || j >= nu) continue;
+            ok = mbar_wait_warp(bar_p_full + u, np[u] & 1, abort_flag) &&
+                 (j > 0 || ni[u] == 0 || mbar_wait_warp(bar_o_free + u, (ni[u] - 1) & 1, abort_flag));
+            if (!ok) break;
+            ++np[u];
+            issue_pv(u, ring + 1, j == 0);
+            if (j + 1 < nu) {
+              issue_s(u, ring + 2);
+              if (j + 2 == nu) commit(bar_q_free + u);
+            }
           }
-          __syncwarp();
-          if (j + 1 < it.n[u]) {
-            issue_s(u, sk);
-            if (j + 2 == it.n[u] && elect_one()) mma_commit(bar_q_free + u);
-          }
+          if (!ok) break;
+          commit(bar_kv_free + sv);
+          if (j + 1 < n) commit(bar_kv_free + sk);
         }
-        if (ok && elect_one()) {
-          mma_commit(bar_kv_free + sv);
-          if (j + 1 < n) mma_commit(bar_kv_free + sk);
-        }
+        ni[0] += n0 > 0;
+        ni[1] += n1 > 0;
       }
-      for (int u = 0; u < 2; ++u) nu[u] += it.n[u] > 0;
     }
     if (elect_one()) {  // every MMA has completed before TMEM is released
-      mma_commit(bar_drain);
-      mbar_wait_drain(bar_drain, 0);
+      mma_commit(bar_drain + (warp - 9));
+      mbar_wait_drain(bar_drain + (warp - 9), 0);
     }
     __syncwarp();
   } else {
@@ -247,9 +321,10 @@ __global__ void __launch_bounds__(320, 1)
     const int u = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lane_base + u * 128, t_o = tmem + lane_base + C::COL_O + u * D;
+    const uint32_t t_p = tmem + lane_base + C::COL_P + u * C::P_STRIDE;
     uint8_t* stg = smem + C::OFF_STG + warp * C::STG_BYTES;
     bool ok = true;
-    int ns = 0, nu = 0;
+    int ns = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
       const FwdItem it = fwd_item(a, item);
       const int n = it.n[u];
@@ -262,6 +337,10 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, s + c * 32);
         tmem_wait_ld();
+        if (C::SEP) {
+          tc_fence_before();
+          warp_arrive(bar_s_free + u, lane);
+        }
         if (j + 1 == n) {  // the diagonal tile: keys up to the row itself
 #pragma unroll
           for (int c = 0; c < 4; ++c) mask_after32(s + c * 32, row - c * 32, -INFINITY);
@@ -278,6 +357,10 @@ __global__ void __launch_bounds__(320, 1)
         if (m_tile > m_used + 8.f) {
           factor = ex2(m_used - m_tile);  // 0 for the first tile
           m_used = m_tile;
+        }
+        if (C::SEP && j > 0) {  // P's columns are free, and O holds every tile before this one
+          ok = ok && mbar_wait(bar_pv_done + u, (ns - 1) & 1, abort_flag);
+          tc_fence_after();
         }
         if (j > 0 && __any_sync(0xffffffffu, factor != 1.f)) {
 #pragma unroll
@@ -298,12 +381,12 @@ __global__ void __launch_bounds__(320, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 e = ex2_pair<T, kFwdPoly>(f2_fma(f2_pack(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc2, ng2), i);
+            const float2 e = ex2_pair<T, kFwdPoly<D>>(f2_fma(f2_pack(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc2, ng2), i);
             rs[i & 3] = f2_add(rs[i & 3], f2_pack(e.x, e.y));
             pk[i] = Elem<T>::pack(e.x, e.y);
           }
-          tmem_st8(t_s + c * 16, pk);
-          tmem_st8(t_s + c * 16 + 8, pk + 8);
+          tmem_st8(t_p + c * 16, pk);
+          tmem_st8(t_p + c * 16 + 8, pk + 8);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -312,8 +395,7 @@ __global__ void __launch_bounds__(320, 1)
         l_sum = l_sum * factor + (r0.x + r0.y);
       }
       // ------------------------------------------------------------ epilogue
-      ok = ok && mbar_wait(bar_o_full + u, nu & 1, abort_flag);
-      ++nu;
+      ok = ok && mbar_wait(bar_pv_done + u, (ns - 1) & 1, abort_flag);
       tc_fence_after();
       const float inv = 1.f / l_sum;
       const int r0 = it.qt[u] * kTile + quarter * 32;  // the warp's first row in the sequence
