@@ -21,9 +21,14 @@
 // and the commit behind S_u(j+1) also says that O_u holds PV_u(j), which is
 // what a rescale needs.
 //
-// Roles (352 threads): warps 0..3 the softmax and epilogue of unit 0, warps
-// 4..7 of unit 1 (thread = query row = TMEM lane 32 (w mod 4) + lane), warp 8
-// lane 0 the TMA producer, warps 9 and 10 the MMAs of units 0 and 1.
+// Roles: the softmax and epilogue of a unit in 4 NH warps, NH threads a query
+// row (TMEM lane 32 (w mod 4) + lane) with 128 / NH keys and D / NH output
+// columns each; one warp whose lane 0 is the TMA producer; two for the MMAs.
+// D <= 64 takes NH = 2 (the two threads agree on the row's maximum through
+// shared memory): it is bound by the softmax, and two warps a scheduler do not
+// hide its latencies (2 x 12288 rows, 8 heads of 64: 389 us, 417 with NH = 1).
+// D = 128 takes NH = 1: there the exchange only lengthens the chain S ->
+// softmax -> PV (ten ragged sequences, 32 / 8 heads: 426 us, 466 with NH = 2).
 #pragma once
 
 #include "pa_device.cuh"
@@ -31,7 +36,7 @@
 namespace pa {
 
 template <int D>
-constexpr int kFwdPoly = D <= 64 ? 2 : 0;
+constexpr int kFwdPoly = D <= 64 ? 1 : 0;
 
 enum Pairing : int { kSingle = 0, kHeads = 1, kTiles = 2 };
 
@@ -50,19 +55,23 @@ template <int D>
 struct FwdCfg {
   using G = TileGeo<D>;
   static constexpr int STAGES = D >= 128 ? 4 : 6;  // K and V tiles in turn
-  static constexpr int STG_ROWB = G::ROWB;         // staging: 32 rows of up to 64 columns per warp
+  static constexpr int NH = D <= 64 ? 2 : 1;       // threads a query row
+  static constexpr int SOFT_WARPS = 8 * NH;
+  static constexpr int STG_COLS = D >= 64 ? 32 : 16;  // staging: 32 rows of so many columns per warp
+  static constexpr int STG_ROWB = 2 * STG_COLS;
   static constexpr int STG_BYTES = 32 * STG_ROWB;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = 2 * G::BYTES;
   static constexpr int OFF_STG = OFF_KV + STAGES * G::BYTES;
-  static constexpr int OFF_BAR = OFF_STG + 8 * STG_BYTES;
+  static constexpr int OFF_RED = OFF_STG + SOFT_WARPS * STG_BYTES;  // [2 tiles in turn][2 units][2 halves][128 rows]
+  static constexpr int OFF_BAR = OFF_RED + (NH - 1) * 8 * kTile * 4;
   static constexpr int N_BARS = 2 + 2 + 2 * STAGES + 2 * 5 + 2;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
   static constexpr int SMEM = OFF_MISC + 16;
   static constexpr bool SEP = D <= 64;  // P in columns of its own
   static constexpr int COL_P = SEP ? 256 : 0, P_STRIDE = SEP ? 64 : 128;
   static constexpr int COL_O = SEP ? 384 : 256;
-  static constexpr int THREADS = 352;
+  static constexpr int THREADS = 32 * (SOFT_WARPS + 3);
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -75,7 +84,9 @@ struct FwdItem {
   int h[2];   // query head
 };
 
-__device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int item) {
+// An item of one unit alone takes the units in turn (k counts the CTA's
+// items), so that one's epilogue runs beside the next one's softmax.
+__device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int item, int k) {
   FwdItem it;
   const int slot = item / a.heads, hi = item - slot * a.heads;
   it.s = a.slots[slot];
@@ -93,11 +104,17 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int item) {
     it.n[1] = a.pairing == kHeads ? it.n[0] : 0;
   }
   it.hk = it.h[0] / a.G;
+  if (it.n[1] == 0 && (k & 1)) {
+    it.n[1] = it.n[0];
+    it.n[0] = 0;
+    it.qt[1] = it.qt[0];
+    it.h[1] = it.h[0];
+  }
   return it;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
     pa_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, const FwdArgs a) {
   using C = FwdCfg<D>;
@@ -126,10 +143,10 @@ __global__ void __launch_bounds__(352, 1)
       mbar_init(bar_q_full + u, 1);
       mbar_init(bar_q_free + u, 1);
       mbar_init(bar_s_full + u, 1);
-      mbar_init(bar_s_free + u, 4);
-      mbar_init(bar_p_full + u, 4);
+      mbar_init(bar_s_free + u, 4 * C::NH);
+      mbar_init(bar_p_full + u, 4 * C::NH);
       mbar_init(bar_pv_done + u, 1);
-      mbar_init(bar_o_free + u, 4);
+      mbar_init(bar_o_free + u, 4 * C::NH);
       mbar_init(bar_drain + u, 1);
     }
     for (int s = 0; s < C::STAGES; ++s) {
@@ -139,19 +156,19 @@ __global__ void __launch_bounds__(352, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 9) tmem_alloc<512>(tmem_slot);
+  if (warp == C::SOFT_WARPS + 1) tmem_alloc<512>(tmem_slot);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 8) {
+  if (warp == C::SOFT_WARPS) {
     // -------------------------------------------------------------- producer
     if (lane == 0) {
       bool ok = true;
       int ring = 0, nq[2] = {0, 0};
       for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-        const FwdItem it = fwd_item(a, item);
+        const FwdItem it = fwd_item(a, item, k);
         for (int u = 0; ok && u < 2; ++u) {
           if (it.n[u] == 0) continue;
           if (nq[u] > 0) ok = mbar_wait(bar_q_free + u, (nq[u] - 1) & 1, abort_flag);
@@ -178,7 +195,7 @@ __global__ void __launch_bounds__(352, 1)
           mbar_wait_drain(bar_kv_full + h % C::STAGES, (h / C::STAGES) & 1);
       }
     }
-  } else if (warp >= 9) {
+  } else if (warp > C::SOFT_WARPS) {
     // ------------------------------------------------------------------ MMAs
     constexpr uint32_t id_s = make_idesc<T>(128, 128, false, false);
     constexpr uint32_t id_o = make_idesc<T>(128, D, false, true);
@@ -216,7 +233,7 @@ __global__ void __launch_bounds__(352, 1)
       __syncwarp();
     };
     if constexpr (C::SEP) {
-      const int u = warp - 9;
+      const int u = warp - C::SOFT_WARPS - 1;
       int ni = 0, ns = 0, np = 0;  // items, S and PV products of this unit so far
       // a tile that only the other unit needs
       auto skip = [&](int r) -> bool {
@@ -226,7 +243,7 @@ __global__ void __launch_bounds__(352, 1)
         return true;
       };
       for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-        const FwdItem it = fwd_item(a, item);
+        const FwdItem it = fwd_item(a, item, k);
         const int n = uniform(it.n[u]), n_all = uniform(max(it.n[0], it.n[1])), len = uniform(it.s.len);
         if (n > 0) {
           ok = full(ring) && mbar_wait_warp(bar_q_full + u, ni & 1, abort_flag) &&
@@ -265,12 +282,12 @@ __global__ void __launch_bounds__(352, 1)
         }
         if (n > 0) ++ni;
       }
-    } else if (warp == 9) {
+    } else if (warp == C::SOFT_WARPS + 1) {
       // One warp for both units, in strict turn: with a warp each (measured: 0.43 -> 0.52 ms for ten ragged sequences,
       // 32 / 8 heads of 128) their products mix, both finish late and both softmaxes then run at the same time.
       int ni[2] = {0, 0}, np[2] = {0, 0};  // items and PV products of each unit so far
       for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-        const FwdItem it = fwd_item(a, item);
+        const FwdItem it = fwd_item(a, item, k);
         const int n0 = uniform(it.n[0]), n1 = uniform(it.n[1]), n = max(n0, n1), len = uniform(it.s.len);
         ok = full(ring);
 #pragma unroll
@@ -312,30 +329,43 @@ __global__ void __launch_bounds__(352, 1)
       }
     }
     if (elect_one()) {  // every MMA has completed before TMEM is released
-      mma_commit(bar_drain + (warp - 9));
-      mbar_wait_drain(bar_drain + (warp - 9), 0);
+      mma_commit(bar_drain + (warp - C::SOFT_WARPS - 1));
+      mbar_wait_drain(bar_drain + (warp - C::SOFT_WARPS - 1), 0);
     }
     __syncwarp();
   } else {
     // ---------------------------------------------------- softmax, epilogue
-    const int u = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    constexpr int NH = C::NH, KPT = kTile / NH;  // threads a row, keys a thread
+    const int u = warp / (4 * NH), half = (warp >> 2) & (NH - 1), quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_s = tmem + lane_base + u * 128, t_o = tmem + lane_base + C::COL_O + u * D;
-    const uint32_t t_p = tmem + lane_base + C::COL_P + u * C::P_STRIDE;
+    const uint32_t t_s = tmem + lane_base + u * 128 + half * KPT;
+    const uint32_t t_p = tmem + lane_base + C::COL_P + u * C::P_STRIDE + half * (KPT / 2);
+    const uint32_t t_o = tmem + lane_base + C::COL_O + u * D + half * (D / NH);
     uint8_t* stg = smem + C::OFF_STG + warp * C::STG_BYTES;
+    // what the two threads of a row tell one another: [turn][unit][half][row]
+    float* mine = reinterpret_cast<float*>(smem + C::OFF_RED) + (u * 2 + half) * kTile + row;
+    const float* other = reinterpret_cast<float*>(smem + C::OFF_RED) + (u * 2 + (half ^ 1)) * kTile + row;
+    int turn = 0;
+    auto exchange = [&](float v) -> float {  // the other thread's value: one barrier of the two warps, buffers in turn
+      mine[turn * 4 * kTile] = v;
+      asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + u * 4 + quarter) : "memory");
+      const float r = other[turn * 4 * kTile];
+      turn ^= 1;
+      return r;
+    };
     bool ok = true;
     int ns = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-      const FwdItem it = fwd_item(a, item);
+      const FwdItem it = fwd_item(a, item, k);
       const int n = it.n[u];
       if (n == 0) continue;
       float m_used = -INFINITY, l_sum = 0.f;
       for (int j = 0; j < n; ++j, ++ns) {
         ok = ok && mbar_wait(bar_s_full + u, ns & 1, abort_flag);
         tc_fence_after();
-        float s[128];
+        float s[KPT];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, s + c * 32);
+        for (int c = 0; c < KPT / 32; ++c) tmem_ld32(t_s + c * 32, s + c * 32);
         tmem_wait_ld();
         if (C::SEP) {
           tc_fence_before();
@@ -343,16 +373,20 @@ __global__ void __launch_bounds__(352, 1)
         }
         if (j + 1 == n) {  // the diagonal tile: keys up to the row itself
 #pragma unroll
-          for (int c = 0; c < 4; ++c) mask_after32(s + c * 32, row - c * 32, -INFINITY);
+          for (int c = 0; c < KPT / 32; ++c) mask_after32(s + c * 32, row - half * KPT - c * 32, -INFINITY);
         }
         float mx[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx[i] = s[i];
+        for (int x = 0; x < 8; ++x) mx[x] = max3(s[x], s[8 + x], s[16 + x]);
 #pragma unroll
-        for (int i = 8; i < 128; i += 16)
+        for (int i = 24; i + 16 < KPT; i += 16)
 #pragma unroll
-          for (int x = 0; x < 8; ++x) mx[x] = i + 8 + x < 128 ? max3(mx[x], s[i + x], s[i + 8 + x]) : fmaxf(mx[x], s[i + x]);
-        const float m_tile = a.scale_log2 * max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+          for (int x = 0; x < 8; ++x) mx[x] = max3(mx[x], s[i + x], s[i + 8 + x]);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) mx[x] = fmaxf(mx[x], s[KPT - 8 + x]);
+        float m_tile = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+        if constexpr (NH == 2) m_tile = fmaxf(m_tile, exchange(m_tile));
+        m_tile *= a.scale_log2;
         float factor = 1.f;
         if (m_tile > m_used + 8.f) {
           factor = ex2(m_used - m_tile);  // 0 for the first tile
@@ -362,9 +396,9 @@ __global__ void __launch_bounds__(352, 1)
           ok = ok && mbar_wait(bar_pv_done + u, (ns - 1) & 1, abort_flag);
           tc_fence_after();
         }
-        if (j > 0 && __any_sync(0xffffffffu, factor != 1.f)) {
+        if (j > 0 && __any_sync(0xffffffffu, factor != 1.f)) {  // each thread its columns of O
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
+          for (int i = 0; i < D / NH / 16; ++i) {
             float ov[16];
             tmem_ld16(t_o + i * 16, ov);
             tmem_wait_ld();
@@ -377,11 +411,12 @@ __global__ void __launch_bounds__(352, 1)
         const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), ng2 = f2_pack(neg, neg);
         uint64_t rs[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < KPT / 32; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 e = ex2_pair<T, kFwdPoly<D>>(f2_fma(f2_pack(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc2, ng2), i);
+            const float2 e =
+                ex2_pair<T, kFwdPoly<D>>(f2_fma(f2_pack(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc2, ng2), i);
             rs[i & 3] = f2_add(rs[i & 3], f2_pack(e.x, e.y));
             pk[i] = Elem<T>::pack(e.x, e.y);
           }
@@ -395,22 +430,25 @@ __global__ void __launch_bounds__(352, 1)
         l_sum = l_sum * factor + (r0.x + r0.y);
       }
       // ------------------------------------------------------------ epilogue
+      if constexpr (NH == 2) l_sum += exchange(l_sum);
       ok = ok && mbar_wait(bar_pv_done + u, (ns - 1) & 1, abort_flag);
       tc_fence_after();
       const float inv = 1.f / l_sum;
       const int r0 = it.qt[u] * kTile + quarter * 32;  // the warp's first row in the sequence
       const long long row0 = static_cast<long long>(it.s.start) + r0;
       const int rows = min(32, it.s.len - r0);
-      T* out = static_cast<T*>(const_cast<void*>(a.o.p)) + row0 * a.o.rs + static_cast<long long>(it.h[u]) * a.o.hs;
+      T* out = static_cast<T*>(const_cast<void*>(a.o.p)) + row0 * a.o.rs + static_cast<long long>(it.h[u]) * a.o.hs +
+               half * (D / NH);
       constexpr int CHUNKS = C::STG_ROWB / 16;  // 16-byte chunks of a staged row
+      constexpr int PASSES = D / NH / C::STG_COLS;
 #pragma unroll
-      for (int p = 0; p < G::PANELS; ++p) {
+      for (int p = 0; p < PASSES; ++p) {
 #pragma unroll
-        for (int i = 0; i < G::BOXW / 16; ++i) {
+        for (int i = 0; i < C::STG_COLS / 16; ++i) {
           float ov[16];
-          tmem_ld16(t_o + p * 64 + i * 16, ov);
+          tmem_ld16(t_o + p * C::STG_COLS + i * 16, ov);
           tmem_wait_ld();
-          if (p == G::PANELS - 1 && i == G::BOXW / 16 - 1) {
+          if (p == PASSES - 1 && i == C::STG_COLS / 16 - 1) {
             tc_fence_before();
             warp_arrive(bar_o_free + u, lane);
           }
@@ -419,28 +457,28 @@ __global__ void __launch_bounds__(352, 1)
           for (int x = 0; x < 8; ++x) w[x] = Elem<T>::pack(ov[2 * x] * inv, ov[2 * x + 1] * inv);
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            *reinterpret_cast<uint4*>(stg + lane * C::STG_ROWB + (((2 * i + x) ^ (lane & (CHUNKS - 1))) << 4)) =
+            *reinterpret_cast<uint4*>(stg + lane * C::STG_ROWB + (((2 * i + x) ^ ((lane >> 1) & (CHUNKS - 1))) << 4)) =
                 make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
         }
         __syncwarp();
-        // whole rows leave together: CHUNKS lanes a row
+        // whole runs of a row leave together: CHUNKS lanes a row
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
           const int r = i * (32 / CHUNKS) + lane / CHUNKS, c = lane % CHUNKS;
           if (r < rows)
-            *reinterpret_cast<uint4*>(out + r * a.o.rs + p * 64 + c * 8) =
-                *reinterpret_cast<const uint4*>(stg + r * C::STG_ROWB + ((c ^ (r & (CHUNKS - 1))) << 4));
+            *reinterpret_cast<uint4*>(out + r * a.o.rs + p * C::STG_COLS + c * 8) =
+                *reinterpret_cast<const uint4*>(stg + r * C::STG_ROWB + ((c ^ ((r >> 1) & (CHUNKS - 1))) << 4));
         }
         __syncwarp();
       }
-      if (lane < rows)
+      if (half == 0 && lane < rows)
         a.lse[static_cast<long long>(it.h[u]) * a.ls + row0 + lane] =
             (m_used + lg2(l_sum) - Elem<T>::kBias) * 0.6931471805599453f;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == C::SOFT_WARPS + 1) {
     tc_fence_after();
     tmem_dealloc<512>(tmem);
   }
