@@ -135,11 +135,10 @@ struct DkvItem {
   int hk, n, per;  // K/V head, steps, steps of one query head
 };
 
-__device__ __forceinline__ DkvItem dkv_item(const DkvArgs& a, int item) {
+__device__ __forceinline__ DkvItem dkv_item(const DkvArgs& a, const Slot& s, int item) {
   DkvItem it;
-  const int slot = item / a.Hkv;
-  it.hk = item - slot * a.Hkv;
-  it.s = a.slots[slot];
+  it.hk = item % a.Hkv;
+  it.s = s;
   it.per = (it.s.len + kTile - 1) / kTile - it.s.tile;
   it.n = it.per * a.G;
   return it;
@@ -189,6 +188,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const SlotWalk walk(a.slots, a.n_items, a.Hkv);
 
   if (warp == 20) {
     // -------------------------------------------------------------- producer
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       bool ok = true;
       int g = 0, ni = 0, n_do = 0;
       for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-        const DkvItem it = dkv_item(a, item);
+        const DkvItem it = dkv_item(a, walk.take(item, k), item);
         const int kb = ni % C::KVB;
         if (ni >= C::KVB && !mbar_wait(bar_kv_free + kb, (ni / C::KVB - 1) & 1, abort_flag)) break;
         const int key0 = it.s.start + it.s.tile * kTile;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     int g = 0, ni = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
-      DkvItem it = dkv_item(a, item);
+      DkvItem it = dkv_item(a, walk.take(item, k), item);
       it.s = uniform(it.s);
       it.per = uniform(it.per);
       it.n = uniform(it.n);
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     int ni = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
-      const DkvItem it = dkv_item(a, item);
+      const DkvItem it = dkv_item(a, walk.take(item, k), item);
       ok = mbar_wait(bar_out_full, ni & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     int g = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-      const DkvItem it = dkv_item(a, item);
+      const DkvItem it = dkv_item(a, walk.take(item, k), item);
       for (int j = 0, in_head = 0; ok && j < it.n; ++j, ++g) {
         const int sq = g % C::QST, so = g % C::OST, sb = g % C::NS;
         const bool diag = in_head == 0;
@@ -517,6 +517,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const SlotWalk walk(a.slots, a.n_items, a.Hq);
 
   if (warp == 20) {
     // -------------------------------------------------------------- producer
@@ -524,8 +525,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       bool ok = true;
       int g = 0, ni = 0, nv = 0;
       for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-        const int slot = item / a.Hq, h = item - slot * a.Hq;
-        const Slot s = a.slots[slot];
+        const int h = item % a.Hq;
+        const Slot s = walk.take(item, k);
         const int qb = ni % C::QB;
         if (ni >= C::QB && !mbar_wait(bar_q_free + qb, (ni / C::QB - 1) & 1, abort_flag)) break;
         mbar_arrive_expect_tx(bar_q_full + qb, 2 * G::BYTES);
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     int g = 0, ni = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
-      const Slot s = uniform(a.slots[item / a.Hq]);
+      const Slot s = uniform(walk.take(item, k));
       const int n = s.tile + 1, qb = ni % C::QB, ob = ni % C::OB;
       ok = mbar_wait_warp(bar_q_full + qb, (ni / C::QB) & 1, abort_flag);
       if (!ok) break;
@@ -637,8 +638,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     int ni = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
-      const int slot = item / a.Hq, h = item - slot * a.Hq, ob = ni % C::OB;
-      const Slot s = a.slots[slot];
+      const int h = item % a.Hq, ob = ni % C::OB;
+      const Slot s = walk.take(item, k);
       ok = mbar_wait(bar_out_full + ob, (ni / C::OB) & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
@@ -659,8 +660,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     int g = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-      const int slot = item / a.Hq, h = item - slot * a.Hq;
-      const Slot s = a.slots[slot];
+      const int h = item % a.Hq;
+      const Slot s = walk.take(item, k);
       const float* ld = a.ld + (static_cast<long long>(h) * a.n_tiles + s.base + s.tile) * 2 * kTile;
       const float neg_lse = ld[row], delta = ld[kTile + row];
       const uint64_t l2 = f2_pack(neg_lse, neg_lse);

@@ -243,4 +243,21 @@ __device__ __forceinline__ int zigzag(int k, int cta, int n_ctas) {
   return k * n_ctas + ((k & 1) ? (n_ctas - 1 - cta) : cta);
 }
 
+// The slots of a CTA's items in order, the next one requested into L1 while
+// this one is worked on: a slot comes from global memory, and every role would
+// wait for it at every item.  (Held in registers one item ahead it cost the
+// forward spills: 2 x 12288 rows, 8 heads of 64, 404 -> 474 us.)
+struct SlotWalk {
+  const Slot* slots;
+  int n_items, per;  // items, items a slot
+  __device__ __forceinline__ SlotWalk(const Slot* p, int items, int per_slot) : slots(p), n_items(items), per(per_slot) {}
+  // the slot of item k of the share, item number `item`
+  __device__ __forceinline__ Slot take(int item, int k) const {
+    const int4 v = __ldg(reinterpret_cast<const int4*>(slots + item / per));
+    const int next = zigzag(k + 1, blockIdx.x, gridDim.x);
+    if (next < n_items) asm volatile("prefetch.global.L1 [%0];" ::"l"(slots + next / per));
+    return Slot{v.x, v.y, v.z, v.w};
+  }
+};
+
 }  // namespace pa

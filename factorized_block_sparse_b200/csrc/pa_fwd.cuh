@@ -86,10 +86,10 @@ struct FwdItem {
 
 // An item of one unit alone takes the units in turn (k counts the CTA's
 // items), so that one's epilogue runs beside the next one's softmax.
-__device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int item, int k) {
+__device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, const Slot& s, int item, int k) {
   FwdItem it;
-  const int slot = item / a.heads, hi = item - slot * a.heads;
-  it.s = a.slots[slot];
+  const int hi = item % a.heads;
+  it.s = s;
   if (a.pairing == kTiles) {
     it.h[0] = it.h[1] = hi;
     it.qt[0] = 2 * it.s.tile;
@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const SlotWalk walk(a.slots, a.n_items, a.heads);
 
   if (warp == C::SOFT_WARPS) {
     // -------------------------------------------------------------- producer
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       bool ok = true;
       int ring = 0, nq[2] = {0, 0};
       for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-        const FwdItem it = fwd_item(a, item, k);
+        const FwdItem it = fwd_item(a, walk.take(item, k), item, k);
         for (int u = 0; ok && u < 2; ++u) {
           if (it.n[u] == 0) continue;
           if (nq[u] > 0) ok = mbar_wait(bar_q_free + u, (nq[u] - 1) & 1, abort_flag);
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         return true;
       };
       for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-        const FwdItem it = fwd_item(a, item, k);
+        const FwdItem it = fwd_item(a, walk.take(item, k), item, k);
         const int n = uniform(it.n[u]), n_all = uniform(max(it.n[0], it.n[1])), len = uniform(it.s.len);
         if (n > 0) {
           ok = full(ring) && mbar_wait_warp(bar_q_full + u, ni & 1, abort_flag) &&
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       // 32 / 8 heads of 128) their products mix, both finish late and both softmaxes then run at the same time.
       int ni[2] = {0, 0}, np[2] = {0, 0};  // items and PV products of each unit so far
       for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-        const FwdItem it = fwd_item(a, item, k);
+        const FwdItem it = fwd_item(a, walk.take(item, k), item, k);
         const int n0 = uniform(it.n[0]), n1 = uniform(it.n[1]), n = max(n0, n1), len = uniform(it.s.len);
         ok = full(ring);
 #pragma unroll
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
     bool ok = true;
     int ns = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
-      const FwdItem it = fwd_item(a, item, k);
+      const FwdItem it = fwd_item(a, walk.take(item, k), item, k);
       const int n = it.n[u];
       if (n == 0) continue;
       float m_used = -INFINITY, l_sum = 0.f;
