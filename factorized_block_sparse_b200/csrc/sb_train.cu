@@ -5,10 +5,12 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <new>
 #include <type_traits>
+#include <utility>
 #include <vector>
 
 #include "sparse_block.h"
@@ -23,28 +25,19 @@ __device__ __forceinline__ float to_f(T v) {
   return static_cast<float>(v);
 }
 
-// VEC consecutive elements as one word: 16 bytes, or one element.
-template <typename T, int VEC>
-struct Word {
-  using type = uint4;
-};
-template <typename T>
-struct Word<T, 1> {
-  using type = T;
-};
-
-template <typename T, int VEC>
-__device__ __forceinline__ void unpack(const typename Word<T, VEC>::type& w, float* f) {
+// The N elements of a 16-byte word.
+template <typename T, int N>
+__device__ __forceinline__ void unpack(const uint4& w, float* f) {
   const T* e = reinterpret_cast<const T*>(&w);
 #pragma unroll
-  for (int u = 0; u < VEC; ++u) f[u] = to_f(e[u]);
+  for (int u = 0; u < N; ++u) f[u] = to_f(e[u]);
 }
-template <typename T, int VEC>
-__device__ __forceinline__ typename Word<T, VEC>::type pack(const float* f) {
-  typename Word<T, VEC>::type w;
+template <typename T, int N>
+__device__ __forceinline__ uint4 pack(const float* f) {
+  uint4 w;
   T* e = reinterpret_cast<T*>(&w);
 #pragma unroll
-  for (int u = 0; u < VEC; ++u) e[u] = static_cast<T>(f[u]);
+  for (int u = 0; u < N; ++u) e[u] = static_cast<T>(f[u]);
   return w;
 }
 
@@ -54,13 +47,15 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the threads of a row: a warp, or the block (slots: 2 x 32 floats
-// used in turn, so that one barrier a sum is enough).
-template <bool WARP, int N>
+// Sums over the threads of a row: TPR lanes of a warp, or the block (TPR = 0;
+// slots: 2 x 32 N floats used in turn, so that one barrier a sum is enough).
+template <int TPR, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float* slots, int& turn) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = warp_sum(v[k]);
-  if constexpr (!WARP) {
+  for (int w = (TPR ? TPR : 32) / 2; w >= 1; w >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], w);
+  if constexpr (TPR == 0) {
     float* s = slots + turn * 32 * N;
     turn ^= 1;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -73,81 +68,179 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* slots, int& turn)
   }
 }
 
-// A row is cut into words of VEC elements; thread i of the row's n threads
-// (a warp's 32, or the block's) holds words i, i + n, ..., NV of them at most.
-template <typename T, int VEC, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 512)
+// ------------------------------------------- rows as aligned 16-byte words
+// A row is the words that it overlaps, the first and last one perhaps in
+// part: word w holds channels w N - shift .. w N - shift + N - 1.  A thread
+// visits rows a multiple of 8 apart, so its shift, and with it the channels of
+// its words, are the same in every row whatever the stride (8 rows of 2-byte
+// elements are a multiple of 16 bytes): gains and sums stay in registers.
+// Words come through a ring in shared memory of the thread's own (cp.async, kDepth rows
+// in flight, no barrier); a word is read whole where it lies inside the
+// tensor's first and last byte, and written element by element where it
+// holds another row's elements.
+constexpr int kDepth = 4;
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// The library's second kernels start while the first one drains (programmatic
+// stream serialisation) and wait here before they read what it wrote.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename T>
+struct Rows {
+  const char* base;  // the tensor's first element
+  const char* end;   // behind its last
+  long long ld;      // bytes from a row to the next
+  __device__ __forceinline__ Rows(const T* p, long long ldx, long long M, int C)
+      : base(reinterpret_cast<const char*>(p)),
+        end(reinterpret_cast<const char*>(p + (M - 1) * ldx + C)),
+        ld(ldx * static_cast<long long>(sizeof(T))) {}
+};
+
+// The thread's words of a row: w = i0 + j n for j < NV.
+template <typename T, int NV>
+struct Words {
+  static constexpr int N = 16 / sizeof(T);
+  int i0, n, words, shift, C;
+  __device__ __forceinline__ Words(const Rows<T>& x, long long r0, int C_, int i0_, int n_) : i0(i0_), n(n_), C(C_) {
+    shift = static_cast<int>((reinterpret_cast<uintptr_t>(x.base) + static_cast<uintptr_t>(r0 * x.ld)) & 15) / static_cast<int>(sizeof(T));
+    words = (shift + C + N - 1) / N;
+  }
+  __device__ __forceinline__ bool has(int j) const { return i0 + j * n < words; }
+  __device__ __forceinline__ int channel(int j, int u) const { return (i0 + j * n) * N - shift + u; }
+  __device__ __forceinline__ bool in(int j, int u) const { return static_cast<unsigned>(channel(j, u)) < static_cast<unsigned>(C); }
+  __device__ __forceinline__ bool whole(int j) const { return channel(j, 0) >= 0 && channel(j, N - 1) < C; }
+  __device__ __forceinline__ const char* at(const Rows<T>& x, long long r, int j) const {
+    return x.base + r * x.ld + static_cast<long long>(channel(j, 0)) * static_cast<long long>(sizeof(T));
+  }
+  // row r's words on their way into the ring slot (NV words, blockDim.x threads)
+  __device__ __forceinline__ void request(uint4* slot, const Rows<T>& x, long long r) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!has(j)) continue;
+      const char* p = at(x, r, j);
+      uint4* d = slot + j * blockDim.x + threadIdx.x;
+      if (p >= x.base && p + 16 <= x.end) {
+        cp_async16(d, p);
+      } else {  // at the tensor's very ends
+        T* e = reinterpret_cast<T*>(d);
+        for (int u = 0; u < N; ++u)
+          if (in(j, u)) e[u] = reinterpret_cast<const T*>(p)[u];
+      }
+    }
+  }
+  // values of word j, zero outside the row
+  __device__ __forceinline__ void values(const uint4* slot, int j, float* f) const {
+    const uint4 w = slot[j * blockDim.x + threadIdx.x];
+    unpack<T, N>(w, f);
+    if (!whole(j))
+#pragma unroll
+      for (int u = 0; u < N; ++u) f[u] = in(j, u) ? f[u] : 0.f;
+  }
+  __device__ __forceinline__ void store(T* y, long long ldy, long long r, int j, const float* f) const {
+    T* p = y + r * ldy + channel(j, 0);
+    if (whole(j)) {
+      *reinterpret_cast<uint4*>(p) = pack<T, N>(f);
+    } else {
+#pragma unroll
+      for (int u = 0; u < N; ++u)
+        if (in(j, u)) p[u] = static_cast<T>(f[u]);
+    }
+  }
+};
+
+// y = (x - mean) rstd g + b, and the row's mean and rstd.  TPR threads a row (0: the block).
+template <typename T, int NV, int TPR>
+__global__ void __launch_bounds__(TPR ? 256 : 512)
     norm_fwd_kernel(const T* x, long long ldx, const float* __restrict__ g, const float* __restrict__ b, T* y,
                     long long ldy, float* mean_out, float* rstd_out, long long M, int C, float eps) {
-  using W = typename Word<T, VEC>::type;
+  constexpr int N = 16 / sizeof(T);
+  extern __shared__ uint4 ring[];  // [kDepth][NV][threads]
   __shared__ float slots[64];
   int turn = 0;
-  const int i0 = WARP ? (threadIdx.x & 31) : threadIdx.x, n = WARP ? 32 : blockDim.x;
-  const int words = C / VEC;
-  const long long r0 = WARP ? ((static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5) : blockIdx.x;
-  const long long step = WARP ? ((static_cast<long long>(gridDim.x) * blockDim.x) >> 5) : gridDim.x;
-  float gv[NV * VEC], bv[NV * VEC];
+  constexpr int kPer = TPR ? TPR : 1;
+  const long long gid = TPR ? (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / kPer : blockIdx.x;
+  const long long step = TPR ? static_cast<long long>(gridDim.x) * blockDim.x / kPer : gridDim.x;
+  const long long warp0 = TPR ? gid - (threadIdx.x & 31) / kPer : gid;  // the warp's first row
+  const Rows<T> xr(x, ldx, M, C);
+  const Words<T, NV> ws(xr, gid, C, TPR ? threadIdx.x % kPer : threadIdx.x, TPR ? kPer : blockDim.x);
+  const int slot_words = NV * blockDim.x;
+#pragma unroll
+  for (int d = 0; d < kDepth - 1; ++d) {
+    if (gid + d * step < M) ws.request(ring + d * slot_words, xr, gid + d * step);
+    cp_commit();
+  }
+  float gv[NV * N], bv[NV * N];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int u = 0; u < VEC; ++u) {
-      const int w = i0 + j * n;
-      gv[j * VEC + u] = w < words ? g[w * VEC + u] : 0.f;
-      bv[j * VEC + u] = (b && w < words) ? b[w * VEC + u] : 0.f;
+    for (int u = 0; u < N; ++u) {
+      const bool in = ws.in(j, u);
+      gv[j * N + u] = in ? g[ws.channel(j, u)] : 0.f;
+      bv[j * N + u] = (b && in) ? b[ws.channel(j, u)] : 0.f;
     }
-  W cur[NV], nxt[NV];
-  auto load = [&](W* raw, long long r) {
-    const W* p = reinterpret_cast<const W*>(x + r * ldx);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (i0 + j * n < words) raw[j] = p[i0 + j * n];
-  };
-  if (r0 < M) load(cur, r0);
   const float inv = 1.f / C;
-  for (long long r = r0; r < M; r += step) {
-    if (r + step < M) load(nxt, r + step);
-    float f[NV * VEC], s[1] = {0.f};
+  int at = 0;
+  for (long long r = gid, w0 = warp0; w0 < M; r += step, w0 += step) {
+    const bool live = r < M;
+    {
+      const long long ahead = r + (kDepth - 1) * step;
+      const int s = at == 0 ? kDepth - 1 : at - 1;
+      if (ahead < M) ws.request(ring + s * slot_words, xr, ahead);
+      cp_commit();
+    }
+    cp_wait<kDepth - 1>();
+    float f[NV * N], s[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (i0 + j * n < words) unpack<T, VEC>(cur[j], f + j * VEC);
+      if (live && ws.has(j)) ws.values(ring + at * slot_words, j, f + j * N);
       else
 #pragma unroll
-        for (int u = 0; u < VEC; ++u) f[j * VEC + u] = 0.f;
+        for (int u = 0; u < N; ++u) f[j * N + u] = 0.f;
 #pragma unroll
-      for (int u = 0; u < VEC; ++u) s[0] += f[j * VEC + u];
+      for (int u = 0; u < N; ++u) s[0] += f[j * N + u];
     }
-    row_sums<WARP>(s, slots, turn);
+    row_sums<TPR>(s, slots, turn);
     const float mean = s[0] * inv;
     float q[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (i0 + j * n < words)
 #pragma unroll
-        for (int u = 0; u < VEC; ++u) {
-          f[j * VEC + u] -= mean;
-          q[0] += f[j * VEC + u] * f[j * VEC + u];
-        }
-    row_sums<WARP>(q, slots, turn);
+      for (int u = 0; u < N; ++u) {
+        f[j * N + u] -= mean;
+        if (ws.in(j, u)) q[0] += f[j * N + u] * f[j * N + u];
+      }
+    row_sums<TPR>(q, slots, turn);
     const float rstd = 1.f / sqrtf(q[0] * inv + eps);
-    if (i0 == 0) {
-      if (mean_out) mean_out[r] = mean;
-      if (rstd_out) rstd_out[r] = rstd;
-    }
-    W* p = reinterpret_cast<W*>(y + r * ldy);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (i0 + j * n < words) {
-        float o[VEC];
-#pragma unroll
-        for (int u = 0; u < VEC; ++u) o[u] = f[j * VEC + u] * rstd * gv[j * VEC + u] + bv[j * VEC + u];
-        p[i0 + j * n] = pack<T, VEC>(o);
+    if (live) {
+      if (ws.i0 == 0) {
+        if (mean_out) mean_out[r] = mean;
+        if (rstd_out) rstd_out[r] = rstd;
       }
 #pragma unroll
-    for (int j = 0; j < NV; ++j) cur[j] = nxt[j];
+      for (int j = 0; j < NV; ++j)
+        if (ws.has(j)) {
+          float o[N];
+#pragma unroll
+          for (int u = 0; u < N; ++u) o[u] = f[j * N + u] * rstd * gv[j * N + u] + bv[j * N + u];
+          ws.store(y, ldy, r, j, o);
+        }
+    }
+    at = at + 1 == kDepth ? 0 : at + 1;
   }
 }
 
-// Rows too wide for the registers of a block: read again for each pass.
+// Rows too wide for the registers of a block, and tensors whose rows lie at
+// different offsets from 16 bytes: one element at a time, read again for each pass.
 template <typename T>
 __global__ void __launch_bounds__(512)
     norm_fwd_wide_kernel(const T* x, long long ldx, const float* g, const float* b, T* y, long long ldy,
@@ -159,10 +252,10 @@ __global__ void __launch_bounds__(512)
     const T* p = x + r * ldx;
     float s[1] = {0.f}, q[1] = {0.f};
     for (int i = threadIdx.x; i < C; i += blockDim.x) s[0] += to_f(p[i]);
-    row_sums<false>(s, slots, turn);
+    row_sums<0>(s, slots, turn);
     const float mean = s[0] * inv;
     for (int i = threadIdx.x; i < C; i += blockDim.x) q[0] += (to_f(p[i]) - mean) * (to_f(p[i]) - mean);
-    row_sums<false>(q, slots, turn);
+    row_sums<0>(q, slots, turn);
     const float rstd = 1.f / sqrtf(q[0] * inv + eps);
     if (threadIdx.x == 0) {
       if (mean_out) mean_out[r] = mean;
@@ -173,108 +266,132 @@ __global__ void __launch_bounds__(512)
   }
 }
 
+// Rows in flight of the backward kernel (x and dy; four words a thread fill shared memory with two).
+__host__ __device__ constexpr int bwd_depth(int nv) { return nv >= 4 ? 2 : kDepth; }
+
 // dx per row, and this block's sums of dy xh and dy per channel into
 // part[blockIdx.x][2][C].
-template <typename T, int VEC, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 512)
+template <typename T, int NV, int TPR>
+__global__ void __launch_bounds__(TPR ? 256 : 512)
     norm_bwd_kernel(const T* x, long long ldx, const float* __restrict__ g, const T* dy, long long lddy,
                     const float* __restrict__ mean_in, const float* __restrict__ rstd_in, T* dx, long long lddx,
                     float* part, long long M, int C) {
-  using W = typename Word<T, VEC>::type;
-  extern __shared__ float sums[];  // WARP: [8 warps][2][C], else none
+  constexpr int N = 16 / sizeof(T);
+  constexpr int kRing = bwd_depth(NV);
+  extern __shared__ uint4 ring[];  // [kRing][x, dy][NV][threads]; then the row groups' sums [groups][2][C]
   __shared__ float slots[128];
+  pdl_trigger();
   int turn = 0;
-  const int i0 = WARP ? (threadIdx.x & 31) : threadIdx.x, n = WARP ? 32 : blockDim.x;
-  const int words = C / VEC;
-  const long long r0 = WARP ? ((static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5) : blockIdx.x;
-  const long long step = WARP ? ((static_cast<long long>(gridDim.x) * blockDim.x) >> 5) : gridDim.x;
-  float gv[NV * VEC], sg[NV * VEC] = {}, sb[NV * VEC] = {};
+  constexpr int kPer = TPR ? TPR : 1;
+  const long long gid = TPR ? (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / kPer : blockIdx.x;
+  const long long step = TPR ? static_cast<long long>(gridDim.x) * blockDim.x / kPer : gridDim.x;
+  const long long warp0 = TPR ? gid - (threadIdx.x & 31) / kPer : gid;
+  const Rows<T> xr(x, ldx, M, C), dr(dy, lddy, M, C);
+  const Words<T, NV> ws(xr, gid, C, TPR ? threadIdx.x % kPer : threadIdx.x, TPR ? kPer : blockDim.x);
+  const int slot_words = NV * blockDim.x;
+  float m_next[kRing - 1], r_next[kRing - 1];  // statistics of the rows in flight
+#pragma unroll
+  for (int d = 0; d < kRing - 1; ++d) {
+    const long long r = gid + d * step;
+    m_next[d] = r_next[d] = 0.f;
+    if (r < M) {
+      ws.request(ring + 2 * d * slot_words, xr, r);
+      ws.request(ring + (2 * d + 1) * slot_words, dr, r);
+      m_next[d] = mean_in[r];
+      r_next[d] = rstd_in[r];
+    }
+    cp_commit();
+  }
+  float gv[NV * N], sg[NV * N] = {}, sb[NV * N] = {};
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int u = 0; u < VEC; ++u) gv[j * VEC + u] = i0 + j * n < words ? g[(i0 + j * n) * VEC + u] : 0.f;
-  W xc[NV], dc[NV], xn[NV], dn[NV];
-  float mc = 0.f, rc = 0.f, mn = 0.f, rn = 0.f;
-  auto load = [&](W* xr, W* dr, float& m, float& rs, long long r) {
-    const W* px = reinterpret_cast<const W*>(x + r * ldx);
-    const W* pd = reinterpret_cast<const W*>(dy + r * lddy);
-    m = mean_in[r];
-    rs = rstd_in[r];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (i0 + j * n < words) {
-        xr[j] = px[i0 + j * n];
-        dr[j] = pd[i0 + j * n];
-      }
-  };
-  if (r0 < M) load(xc, dc, mc, rc, r0);
+    for (int u = 0; u < N; ++u) gv[j * N + u] = ws.in(j, u) ? g[ws.channel(j, u)] : 0.f;
   const float inv = 1.f / C;
-  for (long long r = r0; r < M; r += step) {
-    if (r + step < M) load(xn, dn, mn, rn, r + step);
-    float xh[NV * VEC], t[NV * VEC], s[2] = {0.f, 0.f};
+  int at = 0;
+  for (long long r = gid, w0 = warp0; w0 < M; r += step, w0 += step) {
+    const bool live = r < M;
+    const float mc = m_next[0], rc = r_next[0];
+#pragma unroll
+    for (int d = 0; d + 1 < kRing - 1; ++d) {
+      m_next[d] = m_next[d + 1];
+      r_next[d] = r_next[d + 1];
+    }
+    {
+      const long long ahead = r + (kRing - 1) * step;
+      const int s = at == 0 ? kRing - 1 : at - 1;
+      if (ahead < M) {
+        ws.request(ring + 2 * s * slot_words, xr, ahead);
+        ws.request(ring + (2 * s + 1) * slot_words, dr, ahead);
+        m_next[kRing - 2] = mean_in[ahead];
+        r_next[kRing - 2] = rstd_in[ahead];
+      }
+      cp_commit();
+    }
+    cp_wait<kRing - 1>();
+    float xh[NV * N], t[NV * N], s[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (i0 + j * n < words) {
-        float d[VEC];
-        unpack<T, VEC>(xc[j], xh + j * VEC);
-        unpack<T, VEC>(dc[j], d);
+      if (live && ws.has(j)) {
+        float d[N];
+        ws.values(ring + 2 * at * slot_words, j, xh + j * N);
+        ws.values(ring + (2 * at + 1) * slot_words, j, d);
 #pragma unroll
-        for (int u = 0; u < VEC; ++u) {
-          const int k = j * VEC + u;
+        for (int u = 0; u < N; ++u) {
+          const int k = j * N + u;
           xh[k] = (xh[k] - mc) * rc;
           t[k] = d[u] * gv[k];
           s[0] += t[k];
           s[1] += t[k] * xh[k];
-          sg[k] += d[u] * xh[k];
-          sb[k] += d[u];
+          if (ws.in(j, u)) {  // (outside the row xh is not 0, and an infinite rstd would make it NaN)
+            sg[k] += d[u] * xh[k];
+            sb[k] += d[u];
+          }
         }
       }
-    row_sums<WARP>(s, slots, turn);
+    row_sums<TPR>(s, slots, turn);
     s[0] *= inv;
     s[1] *= inv;
-    W* p = reinterpret_cast<W*>(dx + r * lddx);
+    if (live)
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (i0 + j * n < words) {
-        float o[VEC];
+      for (int j = 0; j < NV; ++j)
+        if (ws.has(j)) {
+          float o[N];
 #pragma unroll
-        for (int u = 0; u < VEC; ++u) o[u] = rc * (t[j * VEC + u] - s[0] - xh[j * VEC + u] * s[1]);
-        p[i0 + j * n] = pack<T, VEC>(o);
-      }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      xc[j] = xn[j];
-      dc[j] = dn[j];
-    }
-    mc = mn;
-    rc = rn;
+          for (int u = 0; u < N; ++u) o[u] = rc * (t[j * N + u] - s[0] - xh[j * N + u] * s[1]);
+          ws.store(dx, lddx, r, j, o);
+        }
+    at = at + 1 == kRing ? 0 : at + 1;
   }
   float* out = part + static_cast<long long>(blockIdx.x) * 2 * C;
-  if constexpr (WARP) {
-    float* mine = sums + (threadIdx.x >> 5) * 2 * C;
+  if constexpr (TPR != 0) {
+    float* sums = reinterpret_cast<float*>(ring);
+    float* mine = sums + threadIdx.x / kPer * 2 * C;
+    cp_wait<0>();
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (i0 + j * n < words)
 #pragma unroll
-        for (int u = 0; u < VEC; ++u) {
-          mine[(i0 + j * n) * VEC + u] = sg[j * VEC + u];
-          mine[C + (i0 + j * n) * VEC + u] = sb[j * VEC + u];
+      for (int u = 0; u < N; ++u)
+        if (ws.in(j, u)) {
+          mine[ws.channel(j, u)] = sg[j * N + u];
+          mine[C + ws.channel(j, u)] = sb[j * N + u];
         }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * C; i += blockDim.x) {
       float a = 0.f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) a += sums[w * 2 * C + i];
+#pragma unroll 8
+      for (int w = 0; w < 256 / kPer; ++w) a += sums[w * 2 * C + i];
       out[i] = a;
     }
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (i0 + j * n < words)
 #pragma unroll
-        for (int u = 0; u < VEC; ++u) {
-          out[(i0 + j * n) * VEC + u] = sg[j * VEC + u];
-          out[C + (i0 + j * n) * VEC + u] = sb[j * VEC + u];
+      for (int u = 0; u < N; ++u)
+        if (ws.in(j, u)) {
+          out[ws.channel(j, u)] = sg[j * N + u];
+          out[C + ws.channel(j, u)] = sb[j * N + u];
         }
   }
 }
@@ -299,7 +416,7 @@ __global__ void __launch_bounds__(512)
       sums[i] += d * xh;
       sums[C + i] += d;
     }
-    row_sums<false>(s, slots, turn);
+    row_sums<0>(s, slots, turn);
     for (int i = threadIdx.x; i < C; i += blockDim.x) {
       const float xh = (to_f(px[i]) - m) * rs, t = to_f(pd[i]) * g[i];
       dx[r * lddx + i] = static_cast<T>(rs * (t - s[0] * inv - xh * (s[1] * inv)));
@@ -315,10 +432,12 @@ __global__ void __launch_bounds__(512)
 // groups of rows of the partials.
 __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* part, int P, int C, float* dg, float* db) {
   __shared__ float s[32][33];
+  pdl_wait();
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
   float a = 0.f;
   if (i < 2 * C)
+#pragma unroll 8
     for (int p = grp; p < P; p += 32) a += part[static_cast<long long>(p) * 2 * C + i];
   s[grp][lane] = a;
   __syncthreads();
@@ -349,18 +468,80 @@ struct ClipTable {
   int n;
 };
 
+// The squares of a word summed in float32, or in float64 where one is too
+// large or too small for that (2^-40 .. 2^60 keeps them and their sum exact to
+// float32's rounding); zeros are the common small values.
 template <typename T>
-__device__ double sum_squares(const T* p, unsigned long long n) {
+__device__ __forceinline__ double word_squares(const uint4& w) {
+  constexpr int N = 16 / sizeof(T);
+  float f[N], big = 0.f;
+  unpack<T, N>(w, f);
+  float s = 0.f;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    s = fmaf(f[u], f[u], s);
+    big = fmaxf(big, fabsf(f[u]));
+  }
+  if (big == 0.f || (big > 9.1e-13f && big < 1.1e18f)) return s;  // (a NaN beside numbers passes: s is NaN)
+  double d = 0.;
+#pragma unroll
+  for (int u = 0; u < N; ++u) d += static_cast<double>(f[u]) * f[u];
+  return d;
+}
+
+template <typename T>
+__device__ __forceinline__ double sum_squares(const T* p, unsigned n) {
+  constexpr unsigned N = 16 / sizeof(T);
   double s = 0.;
-  for (unsigned long long i = threadIdx.x; i < n; i += blockDim.x) {
+  unsigned done = 0;
+  if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    const uint4* w = reinterpret_cast<const uint4*>(p);
+    const unsigned words = n / N;
+    unsigned i = threadIdx.x;
+    for (; i + 3 * blockDim.x < words; i += 4 * blockDim.x) {  // four words in flight
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = w[i + k * blockDim.x];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s += word_squares<T>(v[k]);
+    }
+    for (; i < words; i += blockDim.x) s += word_squares<T>(w[i]);
+    done = words * N;
+  }
+  for (unsigned i = done + threadIdx.x; i < n; i += blockDim.x) {
     const double v = to_f(p[i]);
     s += v * v;
   }
   return s;
 }
+
 template <typename T>
-__device__ void scale_to(const T* p, T* o, unsigned long long n, float c) {
-  for (unsigned long long i = threadIdx.x; i < n; i += blockDim.x) o[i] = static_cast<T>(to_f(p[i]) * c);
+__device__ __forceinline__ void scale_to(const T* p, T* o, unsigned n, float c) {
+  constexpr unsigned N = 16 / sizeof(T);
+  unsigned done = 0;
+  if (((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(o)) & 15) == 0) {
+    const uint4* w = reinterpret_cast<const uint4*>(p);
+    uint4* q = reinterpret_cast<uint4*>(o);
+    const unsigned words = n / N;
+    auto scaled = [&](const uint4& v) {
+      float f[N];
+      unpack<T, N>(v, f);
+#pragma unroll
+      for (unsigned u = 0; u < N; ++u) f[u] *= c;
+      return pack<T, N>(f);
+    };
+    unsigned i = threadIdx.x;
+    for (; i + 3 * blockDim.x < words; i += 4 * blockDim.x) {
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = w[i + k * blockDim.x];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q[i + k * blockDim.x] = scaled(v[k]);
+    }
+    for (; i < words; i += blockDim.x) q[i] = scaled(w[i]);
+    done = words * N;
+  }
+  for (unsigned i = done + threadIdx.x; i < n; i += blockDim.x) o[i] = static_cast<T>(to_f(p[i]) * c);
 }
 
 __device__ __forceinline__ int tensor_of(const ClipTable& t, unsigned chunk) {
@@ -387,11 +568,12 @@ __device__ double block_sum(double v) {
 }
 
 __global__ void __launch_bounds__(512) clip_norm_kernel(const __grid_constant__ ClipTable t, double* part, int add) {
+  pdl_trigger();
   double s = 0.;
   for (unsigned c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
     const int i = tensor_of(t, c);
     const unsigned long long at = static_cast<unsigned long long>(c - t.first[i]) * kChunk;
-    const unsigned long long n = min(static_cast<unsigned long long>(kChunk), t.t[i].n - at);
+    const unsigned n = static_cast<unsigned>(min(static_cast<unsigned long long>(kChunk), t.t[i].n - at));
     if (t.t[i].dtype == SB_BF16) s += sum_squares(static_cast<const __nv_bfloat16*>(t.t[i].g) + at, n);
     else if (t.t[i].dtype == SB_FP16) s += sum_squares(static_cast<const __half*>(t.t[i].g) + at, n);
     else s += sum_squares(static_cast<const float*>(t.t[i].g) + at, n);
@@ -402,6 +584,7 @@ __global__ void __launch_bounds__(512) clip_norm_kernel(const __grid_constant__ 
 
 __global__ void __launch_bounds__(512)
     clip_scale_kernel(const __grid_constant__ ClipTable t, const double* part, double max_norm, float* norm) {
+  pdl_wait();
   double s = 0.;
   for (int i = threadIdx.x; i < kClipBlocks; i += blockDim.x) s += part[i];
   const double total = sqrt(block_sum(s));
@@ -410,10 +593,12 @@ __global__ void __launch_bounds__(512)
   double cd = max_norm / (total + 1e-6);
   if (cd > 1.) cd = 1.;
   const float c = static_cast<float>(cd);
-  for (unsigned k = blockIdx.x; k < t.first[t.n]; k += gridDim.x) {
+  // from the last chunk back: the norm's pass has left those in L2
+  for (unsigned b = blockIdx.x; b < t.first[t.n]; b += gridDim.x) {
+    const unsigned k = t.first[t.n] - 1 - b;
     const int i = tensor_of(t, k);
     const unsigned long long at = static_cast<unsigned long long>(k - t.first[i]) * kChunk;
-    const unsigned long long n = min(static_cast<unsigned long long>(kChunk), t.t[i].n - at);
+    const unsigned n = static_cast<unsigned>(min(static_cast<unsigned long long>(kChunk), t.t[i].n - at));
     if (t.t[i].g == t.t[i].out && c == 1.f) continue;
     if (t.t[i].dtype == SB_BF16)
       scale_to(static_cast<const __nv_bfloat16*>(t.t[i].g) + at, static_cast<__nv_bfloat16*>(t.t[i].out) + at, n, c);
@@ -426,11 +611,53 @@ __global__ void __launch_bounds__(512)
 // ------------------------------------------------------------------ host
 int launched() { return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA; }
 
-int sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 148;
+constexpr int kMaxDevices = 64;
+
+int device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices ? dev : -1;
+}
+
+// SMs of a device, asked once.
+int sms(int dev) {
+  static std::atomic<int> known[kMaxDevices];
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 148;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
   return n;
+}
+
+// Blocks of a kernel that an SM holds, asked once a device and block size (the
+// dynamic shared memory goes with the block size); also allows the memory.
+template <auto Kernel>
+int resident(int dev, int threads, size_t smem) {
+  static std::atomic<int> known[kMaxDevices][17];
+  std::atomic<int>& k = known[dev][threads / 32 <= 16 ? threads / 32 : 0];
+  int per = k.load(std::memory_order_relaxed);
+  if (per == 0) {
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, Kernel, threads, smem) != cudaSuccess || per < 1)
+      return 0;
+    k.store(per, std::memory_order_relaxed);
+  }
+  return per;
+}
+
+// A launch that may begin while the kernel before it in the stream drains.
+template <class... P, class... A>
+int launch_behind(void (*kernel)(P...), unsigned grid, unsigned block, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
 template <typename F>
@@ -444,15 +671,17 @@ int esize(int dtype) { return dtype == SB_FP32 ? 4 : 2; }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-bool rows16(const void* p, int64_t ld, int es) { return aligned(p, 16) && (ld * es) % 16 == 0; }
+// Whether the rows of two tensors lie at the same offsets from 16 bytes.
+bool alike(const void* a, int64_t lda, const void* b, int64_t ldb, int es) {
+  return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0 && ((lda - ldb) * es) % 16 == 0;
+}
 
 constexpr int kParts = 592;  // blocks of a backward launch, at most
 
-template <typename K>
-int resident(K kernel, int threads, size_t smem) {
-  int per = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem) != cudaSuccess || per < 1) return 1;
-  return per;
+// The words of a row, at most (it may begin anywhere in its first one).
+int words_of(const void* p, int64_t ld, int C, int es) {
+  const bool even = aligned(p, 16) && (ld * es) % 16 == 0;
+  return (C * es + 15) / 16 + (even ? 0 : 1);
 }
 
 }  // namespace sbt
@@ -472,34 +701,40 @@ int sparse_block_layer_norm_fwd(const void* x, int64_t ldx, const float* g, cons
   if (C > kMaxC) return SA_ERR_UNSUPPORTED;
   if (M == 0) return SA_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool vec = rows16(x, ldx, es) && rows16(y, ldy, es) && (C * es) % 16 == 0;
-  const int n_sm = sms();
+  const int dev = device();
+  if (dev < 0) return SA_ERR_CUDA;
+  const int n_sm = sms(dev), words = words_of(x, ldx, C, es);
+  const bool same = alike(x, ldx, y, ldy, es);
   return by_type(dtype, [&](auto t) -> int {
     using T = decltype(t);
-    const T* xp = static_cast<const T*>(x);
-    T* yp = static_cast<T*>(y);
-    auto go = [&](auto kernel, int threads, int rows_per_block) -> int {
-      const long long blocks = (M + rows_per_block - 1) / rows_per_block;
-      const int grid = static_cast<int>(std::min<long long>(blocks, static_cast<long long>(n_sm) * resident(kernel, threads, 0)));
-      kernel<<<grid, threads, 0, s>>>(xp, ldx, g, b, yp, ldy, mean, rstd, M, C, eps);
+    auto go = [&](auto nv, auto tpr) -> int {
+      constexpr int NV = nv.value, TPR = tpr.value;
+      constexpr auto K = norm_fwd_kernel<T, NV, TPR>;
+      const int threads = TPR ? 256 : (words + 32 * NV - 1) / (32 * NV) * 32;
+      const int rows = TPR ? 256 / (TPR ? TPR : 1) : 1;  // rows of a block at a time
+      const size_t smem = static_cast<size_t>(kDepth) * NV * threads * 16;
+      const int per = resident<K>(dev, threads, smem);
+      if (per == 0) return SA_ERR_CUDA;
+      long long grid = std::min<long long>((M + rows - 1) / rows, static_cast<long long>(n_sm) * per);
+      if (TPR == 0 && grid < M) grid = std::max<long long>(grid / 8 * 8, 8);  // rows of a thread: a multiple of 8 apart
+      K<<<static_cast<unsigned>(grid), threads, smem, s>>>(static_cast<const T*>(x), ldx, g, b, static_cast<T*>(y), ldy,
+                                                           mean, rstd, M, C, eps);
       return launched();
     };
-    auto pick = [&](auto v) -> int {
-      constexpr int V = v.value;
-      const int words = C / V;
-      if (words <= 32) return go(norm_fwd_kernel<T, V, 1, true>, 256, 8);
-      if (words <= 64) return go(norm_fwd_kernel<T, V, 2, true>, 256, 8);
-      if (words <= 128) return go(norm_fwd_kernel<T, V, 4, true>, 256, 8);
-      auto threads = [&](int nv) { return std::min(512, (words + 32 * nv - 1) / (32 * nv) * 32); };
-      if (words <= 1024) return go(norm_fwd_kernel<T, V, 2, false>, threads(2), 1);
-      if (words <= 2048) return go(norm_fwd_kernel<T, V, 4, false>, threads(4), 1);
-      if constexpr (V == 1) {
-        if (words <= 6144) return go(norm_fwd_kernel<T, V, 12, false>, threads(12), 1);
-      }
-      return go(norm_fwd_wide_kernel<T>, 512, 1);
-    };
-    if (vec) return pick(std::integral_constant<int, 16 / sizeof(T)>{});
-    return pick(std::integral_constant<int, 1>{});
+    using std::integral_constant;
+    if (same) {
+      if (words <= 8) return go(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+      if (words <= 16) return go(integral_constant<int, 1>{}, integral_constant<int, 16>{});
+      if (words <= 32) return go(integral_constant<int, 1>{}, integral_constant<int, 32>{});
+      if (words <= 64) return go(integral_constant<int, 2>{}, integral_constant<int, 32>{});
+      if (words <= 512) return go(integral_constant<int, 1>{}, integral_constant<int, 0>{});
+      if (words <= 1024) return go(integral_constant<int, 2>{}, integral_constant<int, 0>{});
+      if (words <= 2048) return go(integral_constant<int, 4>{}, integral_constant<int, 0>{});
+    }
+    const int grid = static_cast<int>(std::min<long long>(M, static_cast<long long>(n_sm) * 4));
+    norm_fwd_wide_kernel<T><<<grid, 512, 0, s>>>(static_cast<const T*>(x), ldx, g, b, static_cast<T*>(y), ldy, mean, rstd, M,
+                                                 C, eps);
+    return launched();
   });
 }
 
@@ -522,46 +757,56 @@ int sparse_block_layer_norm_bwd(const void* x, int64_t ldx, const float* g, cons
   if (!ws || !aligned(ws, 256) || ws_bytes < sparse_block_layer_norm_bwd_workspace_size(M, C)) return SA_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* part = static_cast<float*>(ws);
-  const int n_sm = sms();
+  const int dev = device();
+  if (dev < 0) return SA_ERR_CUDA;
+  const int n_sm = sms(dev);
   int P = 0;
-  const bool vec = rows16(x, ldx, es) && rows16(dy, lddy, es) && rows16(dx, lddx, es) && (C * es) % 16 == 0;
   if (M > 0) {
+    const int words = words_of(x, ldx, C, es);
+    const bool same = alike(x, ldx, dy, lddy, es) && alike(x, ldx, dx, lddx, es);
     const int st = by_type(dtype, [&](auto t) -> int {
       using T = decltype(t);
-      auto go = [&](auto kernel, int threads, int rows_per_block, size_t smem) -> int {
-        if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     static_cast<int>(smem)) != cudaSuccess)
-          return SA_ERR_CUDA;
-        const long long blocks = (M + rows_per_block - 1) / rows_per_block;
-        P = static_cast<int>(std::min<long long>(
-            std::min<long long>(blocks, kParts), static_cast<long long>(n_sm) * resident(kernel, threads, smem)));
-        kernel<<<P, threads, smem, s>>>(static_cast<const T*>(x), ldx, g, static_cast<const T*>(dy), lddy, mean, rstd,
-                                        static_cast<T*>(dx), lddx, part, M, C);
+      auto go = [&](auto nv, auto tpr) -> int {
+        constexpr int NV = nv.value, TPR = tpr.value;
+        constexpr auto K = norm_bwd_kernel<T, NV, TPR>;
+        const int threads = TPR ? 256 : (words + 32 * NV - 1) / (32 * NV) * 32;
+        const int rows = TPR ? 256 / (TPR ? TPR : 1) : 1;
+        // the ring, and in its place afterwards the row groups' sums of up to NV TPR words
+        const size_t ring = 2 * static_cast<size_t>(bwd_depth(NV)) * NV * threads * 16;
+        const size_t sums = TPR ? static_cast<size_t>(rows) * 2 * (NV * TPR * 16 / sizeof(T)) * sizeof(float) : 0;
+        const size_t smem = std::max(ring, sums);
+        const int per = resident<K>(dev, threads, smem);
+        if (per == 0) return SA_ERR_CUDA;
+        long long grid = std::min<long long>(std::min<long long>((M + rows - 1) / rows, kParts), static_cast<long long>(n_sm) * per);
+        if (TPR == 0 && grid < M) grid = std::max<long long>(grid / 8 * 8, 8);
+        P = static_cast<int>(grid);
+        K<<<P, threads, smem, s>>>(static_cast<const T*>(x), ldx, g, static_cast<const T*>(dy), lddy, mean, rstd,
+                                   static_cast<T*>(dx), lddx, part, M, C);
         return launched();
       };
-      auto pick = [&](auto v) -> int {
-        constexpr int V = v.value;
-        const int words = C / V;
-        const size_t sums = 8 * 2 * static_cast<size_t>(C) * sizeof(float);
-        if (words <= 32) return go(norm_bwd_kernel<T, V, 1, true>, 256, 8, sums);
-        if (words <= 64) return go(norm_bwd_kernel<T, V, 2, true>, 256, 8, sums);
-        auto threads = [&](int nv) { return std::min(512, (words + 32 * nv - 1) / (32 * nv) * 32); };
-        if (words <= 1024) return go(norm_bwd_kernel<T, V, 2, false>, threads(2), 1, 0);
-        if constexpr (V <= 4) {
-          if (words <= 2048) return go(norm_bwd_kernel<T, V, 4, false>, threads(4), 1, 0);
+      using std::integral_constant;
+      if (same) {
+        if (words <= 8) return go(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+        if (words <= 16) return go(integral_constant<int, 1>{}, integral_constant<int, 16>{});
+        if (words <= 32) return go(integral_constant<int, 1>{}, integral_constant<int, 32>{});
+        if (words <= 64) return go(integral_constant<int, 2>{}, integral_constant<int, 32>{});
+        if (words <= 512) return go(integral_constant<int, 1>{}, integral_constant<int, 0>{});
+        if (words <= 1024) return go(integral_constant<int, 2>{}, integral_constant<int, 0>{});
+        if constexpr (sizeof(T) == 4) {
+          if (words <= 2048) return go(integral_constant<int, 4>{}, integral_constant<int, 0>{});
         }
-        if constexpr (V == 1) {
-          if (words <= 6144) return go(norm_bwd_kernel<T, V, 12, false>, threads(12), 1, 0);
-        }
-        return go(norm_bwd_wide_kernel<T>, 512, 1, 2 * static_cast<size_t>(C) * sizeof(float));
-      };
-      if (vec) return pick(std::integral_constant<int, 16 / sizeof(T)>{});
-      return pick(std::integral_constant<int, 1>{});
+      }
+      constexpr auto K = norm_bwd_wide_kernel<T>;
+      const size_t smem = 2 * static_cast<size_t>(C) * sizeof(float);
+      if (resident<K>(dev, 512, smem) == 0) return SA_ERR_CUDA;
+      P = static_cast<int>(std::min<long long>(std::min<long long>(M, kParts), n_sm));
+      K<<<P, 512, smem, s>>>(static_cast<const T*>(x), ldx, g, static_cast<const T*>(dy), lddy, mean, rstd,
+                             static_cast<T*>(dx), lddx, part, M, C);
+      return launched();
     });
     if (st) return st;
   }
-  norm_bwd_sum_kernel<<<(2 * C + 31) / 32, 1024, 0, s>>>(part, P, C, dg, db);
-  return launched();
+  return launch_behind(norm_bwd_sum_kernel, (2 * C + 31) / 32, 1024, s, static_cast<const float*>(part), P, C, dg, db);
 }
 
 size_t sparse_block_clip_workspace_size(void) { return kClipBlocks * sizeof(double); }
@@ -622,9 +867,13 @@ int sparse_block_clip_grads(int n, const void* const* grads, void* const* outs, 
           t.first[t.n + 1] = t.first[t.n] + static_cast<unsigned>(chunks);
           ++t.n;
         }
-      if (pass == 0) clip_norm_kernel<<<kClipBlocks, 512, 0, s>>>(t, part, first ? 0 : 1);
-      else clip_scale_kernel<<<t.n ? kClipBlocks : 1, 512, 0, s>>>(t, part, max_norm, norm);
-      if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
+      if (pass == 0) {
+        clip_norm_kernel<<<kClipBlocks, 512, 0, s>>>(t, part, first ? 0 : 1);
+        if (launched()) return SA_ERR_CUDA;
+      } else if (launch_behind(clip_scale_kernel, t.n ? kClipBlocks : 1, 512, s, t, static_cast<const double*>(part), max_norm,
+                               norm)) {
+        return SA_ERR_CUDA;
+      }
       first = false;
     } while ((pass == 0 || outs) && at < ts.size());
   }

@@ -18,7 +18,6 @@ Use::
 """
 
 import ctypes
-import math
 import os
 
 import numpy as np
@@ -107,39 +106,39 @@ class Layout:
             pass
 
 
-def _dtype(t):
+def _check_tensors(q, k, v, layout, more=()):
+    """Shapes, types, strides and devices of a call; returns (T, Hq, Hkv, D, type code)."""
     import torch
 
-    if t.dtype == torch.bfloat16:
-        return 0
-    if t.dtype == torch.float16:
-        return 1
-    raise ValueError(f"expected bf16 or fp16 tensors, got {t.dtype}")
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3:
+        raise ValueError("expected q [T, Hq, D] and k, v [T, Hkv, D]")
+    T, Hq, D = qs
+    Hkv = ks[1]
+    if ks[0] != T or ks[2] != D or v.shape != ks:
+        raise ValueError(f"k and v must be [{T}, Hkv, {D}], got {tuple(ks)} and {tuple(v.shape)}")
+    if T < layout.rows:
+        raise ValueError(f"the layout has {layout.rows} rows, the tensors {T}")
+    dt, dev = q.dtype, q.device
+    if dt is torch.bfloat16:
+        code = 0
+    elif dt is torch.float16:
+        code = 1
+    else:
+        raise ValueError(f"expected bf16 or fp16 tensors, got {dt}")
+    for name, t, shape in (("q", q, qs), ("k", k, ks), ("v", v, ks), *more):
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        if t.dtype is not dt or not t.is_cuda or t.device != dev:
+            raise ValueError(f"{name} must be a {dt} tensor on the CUDA device of q")
+        if t.stride(2) != 1 and D > 1:
+            raise ValueError(f"the last dimension of {name} must be contiguous")
+    return T, Hq, Hkv, D, code
 
 
 def _desc(t):
     """The C view of a ``[T, H, D]`` tensor; the strides of extents of 1 carry no meaning and are not read."""
     return _Tensor(t.data_ptr(), t.stride(0), t.stride(1))
-
-
-def _check_tensors(q, k, v, layout, more=()):
-    """Shapes, types and devices of a call; returns (T, Hq, Hkv, D)."""
-    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
-        raise ValueError("expected q [T, Hq, D] and k, v [T, Hkv, D]")
-    T, Hq, D = (int(x) for x in q.shape)
-    Hkv = int(k.shape[1])
-    if tuple(k.shape) != (T, Hkv, D) or k.shape != v.shape:
-        raise ValueError(f"k and v must be [{T}, Hkv, {D}], got {tuple(k.shape)} and {tuple(v.shape)}")
-    if T < layout.rows:
-        raise ValueError(f"the layout has {layout.rows} rows, the tensors {T}")
-    for name, t, shape in (("q", q, q.shape), ("k", k, k.shape), ("v", v, k.shape), *more):
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-        if t.dtype != q.dtype or t.device != q.device or t.device.type != "cuda":
-            raise ValueError(f"{name} must be a {q.dtype} tensor on the CUDA device of q")
-        if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"the last dimension of {name} must be contiguous")
-    return T, Hq, Hkv, D
 
 
 def _check_lse(lse, Hq, T, q):
@@ -152,55 +151,49 @@ def _check_lse(lse, Hq, T, q):
     return lse.stride(0) if Hq > 1 else T
 
 
-def _stream_of(t, stream):
-    if stream is not None:
-        return sa._stream_ptr(stream)
+def _call(device, stream, what, fn, *args):
+    """``fn(*args, stream)`` with ``device`` as the current one, on the given stream or torch's current one of it."""
     import torch
 
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    if stream is None:
+        s = torch.cuda.current_stream(device).cuda_stream
+    else:
+        s = stream if isinstance(stream, int) else stream.cuda_stream
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, s)
+    if st:
+        raise sa.SparseAttnError(st, what)
 
 
-class _On:
-    """The device of a tensor as the current one for the length of a call (nothing to do when it is)."""
+def _fwd(q, k, v, o, lse, ls, dims, layout, stream, scale):
+    T, Hq, Hkv, D, code = dims
+    _call(q.device, stream, "packed_attn_fwd", lib.packed_attn_fwd, _desc(q), _desc(k), _desc(v), _desc(o), lse.data_ptr(),
+          ls, T, Hq, Hkv, D, code, D ** -0.5 if scale is None else float(scale), layout.handle)
 
-    def __init__(self, t):
-        import torch
 
-        self.guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
-
-    def __enter__(self):
-        if self.guard:
-            self.guard.__enter__()
-
-    def __exit__(self, *a):
-        if self.guard:
-            self.guard.__exit__(*a)
+def _bwd(q, k, v, o, lse, ls, dO, dq, dk, dv, dims, layout, ws, stream, scale):
+    T, Hq, Hkv, D, code = dims
+    if ws.device != q.device or not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the device of q")
+    _call(q.device, stream, "packed_attn_bwd", lib.packed_attn_bwd, _desc(q), _desc(k), _desc(v), _desc(o),
+          lse.data_ptr(), ls, _desc(dO), _desc(dq), _desc(dk), _desc(dv), T, Hq, Hkv, D, code,
+          D ** -0.5 if scale is None else float(scale), layout.handle, ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def packed_attn_fwd(q, k, v, o, lse, layout, stream=None, scale=None):
     """Writes ``o`` and ``lse`` in place (C ABI call); ``scale`` None is 1/sqrt(D)."""
-    T, Hq, Hkv, D = _check_tensors(q, k, v, layout, (("o", o, q.shape),))
-    ls = _check_lse(lse, Hq, T, q)
-    dt = _dtype(q)
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    with _On(q):
-        sa._check(lib.packed_attn_fwd(_desc(q), _desc(k), _desc(v), _desc(o), sa._ptr(lse), ls, T, Hq, Hkv, D, dt, scale,
-                                      layout.handle, _stream_of(q, stream)), "packed_attn_fwd")
+    dims = _check_tensors(q, k, v, layout, (("o", o, q.shape),))
+    _fwd(q, k, v, o, lse, _check_lse(lse, dims[1], dims[0], q), dims, layout, stream, scale)
 
 
 def packed_attn_bwd(q, k, v, o, lse, dO, dq, dk, dv, layout, ws, stream=None, scale=None):
     """Writes ``dq``, ``dk``, ``dv`` in place (C ABI call); ``scale`` None is 1/sqrt(D)."""
-    T, Hq, Hkv, D = _check_tensors(q, k, v, layout, (("o", o, q.shape), ("dO", dO, q.shape), ("dq", dq, q.shape),
-                                                     ("dk", dk, k.shape), ("dv", dv, k.shape)))
-    ls = _check_lse(lse, Hq, T, q)
-    dt = _dtype(q)
-    if ws.device != q.device or not ws.is_contiguous():
-        raise ValueError("the workspace must be contiguous and on the device of q")
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    with _On(q):
-        sa._check(lib.packed_attn_bwd(_desc(q), _desc(k), _desc(v), _desc(o), sa._ptr(lse), ls, _desc(dO), _desc(dq),
-                                      _desc(dk), _desc(dv), T, Hq, Hkv, D, dt, scale, layout.handle, sa._ptr(ws),
-                                      ws.numel() * ws.element_size(), _stream_of(q, stream)), "packed_attn_bwd")
+    dims = _check_tensors(q, k, v, layout, (("o", o, q.shape), ("dO", dO, q.shape), ("dq", dq, q.shape),
+                                            ("dk", dk, k.shape), ("dv", dv, k.shape)))
+    _bwd(q, k, v, o, lse, _check_lse(lse, dims[1], dims[0], q), dO, dq, dk, dv, dims, layout, ws, stream, scale)
 
 
 def packed_attn_status(stream=None):
@@ -208,26 +201,31 @@ def packed_attn_status(stream=None):
 
 
 # ------------------------------------------------------------ conveniences
-def _on_stream(stream, t):
+def _on_stream(stream, device):
     """torch work of a call (allocation, zeroing) on the stream that the call runs on."""
-    import contextlib
-
     import torch
 
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+
+
+def _outputs(q, layout, shapes):
+    """Tensors of ``(shape, dtype, dimension of the rows)``, zero in the rows behind the last sequence."""
+    import torch
+
+    outs = []
+    for shape, dtype, dim in shapes:
+        t = torch.empty(shape, dtype=dtype, device=q.device)
+        if layout.rows < shape[dim]:
+            t.narrow(dim, layout.rows, shape[dim] - layout.rows).zero_()
+        outs.append(t)
+    return outs
+
+
+def _allocate(q, layout, shapes, stream):
     if stream is None:
-        return contextlib.nullcontext()
-    s = torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int) else stream
-    return torch.cuda.stream(s)
-
-
-def _empty(t, heads, rows):
-    """An output like ``t`` with ``heads`` heads, zero in the rows behind the last sequence."""
-    import torch
-
-    out = torch.empty((t.shape[0], heads, t.shape[2]), dtype=t.dtype, device=t.device)
-    if rows < t.shape[0]:
-        out[rows:].zero_()
-    return out
+        return _outputs(q, layout, shapes)
+    with _on_stream(stream, q.device):
+        return _outputs(q, layout, shapes)
 
 
 def workspace(Hq, Hkv, D, layout, device):
@@ -243,21 +241,25 @@ def forward(q, k, v, layout, stream=None, scale=None):
     """Allocates ``o`` and ``lse`` (zero in rows behind the last sequence) and runs the forward pass."""
     import torch
 
-    T, Hq, _, _ = _check_tensors(q, k, v, layout)
-    with _on_stream(stream, q):
-        o = _empty(q, Hq, layout.rows)
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-        if layout.rows < T:
-            lse[:, layout.rows:].zero_()
-    packed_attn_fwd(q, k, v, o, lse, layout, stream, scale)
+    dims = _check_tensors(q, k, v, layout)
+    T, Hq, _, D, _ = dims
+    o, lse = _allocate(q, layout, (((T, Hq, D), q.dtype, 0), ((Hq, T), torch.float32, 1)), stream)
+    _fwd(q, k, v, o, lse, T, dims, layout, stream, scale)
     return o, lse
 
 
 def backward(q, k, v, o, lse, dO, layout, ws=None, stream=None, scale=None):
     """Allocates ``dq``, ``dk``, ``dv`` (zero in rows behind the last sequence), and a workspace if none is given."""
-    _, Hq, Hkv, D = _check_tensors(q, k, v, layout)
-    with _on_stream(stream, q):
-        ws = workspace(Hq, Hkv, D, layout, q.device) if ws is None else ws
-        dq, dk, dv = _empty(q, Hq, layout.rows), _empty(k, Hkv, layout.rows), _empty(k, Hkv, layout.rows)
-    packed_attn_bwd(q, k, v, o, lse, dO, dq, dk, dv, layout, ws, stream, scale)
+    dims = _check_tensors(q, k, v, layout, (("o", o, q.shape), ("dO", dO, q.shape)))
+    T, Hq, Hkv, D, _ = dims
+    ls = _check_lse(lse, Hq, T, q)
+    kv = ((T, Hkv, D), q.dtype, 0)
+    dq, dk, dv = _allocate(q, layout, (((T, Hq, D), q.dtype, 0), kv, kv), stream)
+    if ws is None:
+        if stream is None:
+            ws = workspace(Hq, Hkv, D, layout, q.device)
+        else:
+            with _on_stream(stream, q.device):
+                ws = workspace(Hq, Hkv, D, layout, q.device)
+    _bwd(q, k, v, o, lse, ls, dO, dq, dk, dv, dims, layout, ws, stream, scale)
     return dq, dk, dv

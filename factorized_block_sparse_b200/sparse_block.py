@@ -141,32 +141,36 @@ def gelu(u, grad=False, stream=None):
 def _dtype(t):
     import torch
 
-    try:
-        return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}[t.dtype]
-    except KeyError:
-        raise ValueError(f"expected a bf16, fp16 or float32 tensor, got {t.dtype}") from None
+    dt = t.dtype
+    if dt is torch.bfloat16:
+        return 0
+    if dt is torch.float16:
+        return 1
+    if dt is torch.float32:
+        return 2
+    raise ValueError(f"expected a bf16, fp16 or float32 tensor, got {dt}")
 
 
-def _rows(name, t, like=None):
-    """``t`` as ``(pointer tensor, rows, C, row stride)``: the leading dimensions must be one run of rows."""
-    if t.device.type != "cuda":
+def _rows(name, t):
+    """``(rows, C, row stride)`` of a tensor whose leading dimensions are one run of rows."""
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() < 1 or t.shape[-1] < 1:
         raise ValueError(f"{name} must have at least one channel")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must be a {like.dtype} tensor of shape {tuple(like.shape)} on {like.device}")
-    C = int(t.shape[-1])
+    C = t.shape[-1]
+    if t.is_contiguous():
+        return t.numel() // C, C, C
     if C > 1 and t.stride(-1) != 1:
         raise ValueError(f"the channels of {name} must be contiguous")
     rows, ld = 1, C
     for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if n == 1:
             continue
-        if rows > 1 and n > 0 and st != rows * ld:
+        if rows > 1 and st != rows * ld:
             raise ValueError(f"the leading dimensions of {name} must be rows at one stride")
         if rows == 1:
-            ld = int(st)
-        rows *= int(n)
+            ld = st
+        rows *= n
     if rows > 1 and ld < C:
         raise ValueError(f"the rows of {name} overlap")
     return rows, C, (ld if rows > 1 else C)
@@ -175,37 +179,31 @@ def _rows(name, t, like=None):
 def _vector(name, t, C, device):
     import torch
 
-    if t.dtype != torch.float32 or t.device != device or tuple(t.shape) != (C,) or not t.is_contiguous():
+    if t.dtype is not torch.float32 or t.device != device or t.shape != (C,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 [{C}] tensor on {device}")
-    return sa._ptr(t)
+    return t.data_ptr()
 
 
-def _on(t):
-    """The device of ``t`` as the current one for the length of a call."""
+def _on(device, stream):
+    """A context of the device and the stream that a call runs on, for its allocations and its launch."""
     import contextlib
 
     import torch
 
-    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    cm = contextlib.ExitStack()
+    if device.index != torch.cuda.current_device():
+        cm.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        cm.enter_context(torch.cuda.stream(
+            torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream))
+    return cm
 
 
-def _stream(t, stream):
+def _here(device, stream):
+    """Whether a call runs on the current device and its current stream, so that it needs no context."""
     import torch
 
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
-    return sa._stream_ptr(stream)
-
-
-def _alloc_on(stream, t):
-    """torch allocations of a call belong to the stream that the call runs on."""
-    import contextlib
-
-    import torch
-
-    if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int) else stream)
+    return stream is None and device.index == torch.cuda.current_device()
 
 
 def layer_norm(x, g, b=None, eps=1e-5, stream=None):
@@ -214,19 +212,22 @@ def layer_norm(x, g, b=None, eps=1e-5, stream=None):
     float32 ``[C]``; without ``b`` there is no bias."""
     import torch
 
+    dev = x.device
     M, C, ld = _rows("x", x)
     dt = _dtype(x)
-    gp = _vector("g", g, C, x.device)
-    bp = _vector("b", b, C, x.device) if b is not None else None
-    with _on(x), _alloc_on(stream, x):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device)
-        mean, rstd = stats[0], stats[1]
-        if M:
-            sa._check(lib.sparse_block_layer_norm_fwd(sa._ptr(x), ld, gp, bp, sa._ptr(y), C, sa._ptr(mean),
-                                                      sa._ptr(rstd), M, C, eps, dt, _stream(x, stream)),
-                      "sparse_block_layer_norm_fwd")
-    return y, mean, rstd
+    gp = _vector("g", g, C, dev)
+    bp = None if b is None else _vector("b", b, C, dev)
+    if not _here(dev, stream):
+        with _on(dev, stream):
+            return layer_norm(x, g, b, eps)
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev)
+    mp = stats.data_ptr()
+    if M:
+        sa._check(lib.sparse_block_layer_norm_fwd(x.data_ptr(), ld, gp, bp, y.data_ptr(), C, mp, mp + 4 * M, M, C, eps,
+                                                  dt, torch.cuda.current_stream(dev).cuda_stream),
+                  "sparse_block_layer_norm_fwd")
+    return y, stats[0], stats[1]
 
 
 def layer_norm_backward(x, g, dy, mean, rstd, bias=True, stream=None):
@@ -234,28 +235,32 @@ def layer_norm_backward(x, g, dy, mean, rstd, bias=True, stream=None):
     type and shape, contiguous; dg and db float32 ``[C]`` (db None without ``bias``)."""
     import torch
 
+    dev = x.device
     M, C, ld = _rows("x", x)
     dt = _dtype(x)
-    _, _, ldd = _rows("dy", dy, x)
-    gp = _vector("g", g, C, x.device)
+    if dy.shape != x.shape or dy.dtype is not x.dtype or dy.device != dev:
+        raise ValueError(f"dy must be a {x.dtype} tensor of shape {tuple(x.shape)} on {dev}")
+    ldd = _rows("dy", dy)[2]
+    gp = _vector("g", g, C, dev)
     for name, t in (("mean", mean), ("rstd", rstd)):
-        if t.dtype != torch.float32 or t.shape != x.shape[:-1] or t.device != x.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(x.shape[:-1])} on {x.device}")
-    with _on(x), _alloc_on(stream, x):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dg = torch.empty(C, dtype=torch.float32, device=x.device)
-        db = torch.empty(C, dtype=torch.float32, device=x.device) if bias else None
-        n = int(lib.sparse_block_layer_norm_bwd_workspace_size(M, C))
-        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=x.device)
-        if M == 0:
-            dg.zero_()
-            if bias:
-                db.zero_()
-        else:
-            sa._check(lib.sparse_block_layer_norm_bwd(sa._ptr(x), ld, gp, sa._ptr(dy), ldd, sa._ptr(mean), sa._ptr(rstd),
-                                                      sa._ptr(dx), C, sa._ptr(dg), sa._ptr(db) if bias else None, M, C,
-                                                      dt, sa._ptr(ws), ws.numel(), _stream(x, stream)),
-                      "sparse_block_layer_norm_bwd")
+        if t.dtype is not torch.float32 or t.shape != x.shape[:-1] or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(x.shape[:-1])} on {dev}")
+    if not _here(dev, stream):
+        with _on(dev, stream):
+            return layer_norm_backward(x, g, dy, mean, rstd, bias)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    grads = torch.empty((2, C) if bias else (1, C), dtype=torch.float32, device=dev)
+    dg, db = grads[0], (grads[1] if bias else None)
+    if M == 0:
+        grads.zero_()
+        return dx, dg, db
+    n = lib.sparse_block_layer_norm_bwd_workspace_size(M, C)
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    gptr = grads.data_ptr()
+    sa._check(lib.sparse_block_layer_norm_bwd(x.data_ptr(), ld, gp, dy.data_ptr(), ldd, mean.data_ptr(), rstd.data_ptr(),
+                                              dx.data_ptr(), C, gptr, gptr + 4 * C if bias else None, M, C, dt,
+                                              ws.data_ptr(), max(n, 256), torch.cuda.current_stream(dev).cuda_stream),
+              "sparse_block_layer_norm_bwd")
     return dx, dg, db
 
 
@@ -277,20 +282,26 @@ def _clip(grads, max_norm, out, stream):
             raise ValueError(f"gradients must be contiguous tensors on {dev}")
     n = len(grads)
     dts = [_dtype(t) for t in grads]
-    if outs is not None:
+    if out is not grads and outs is not None:
         for t, o in zip(grads, outs):
-            if o.shape != t.shape or o.dtype != t.dtype or o.device != dev or not o.is_contiguous():
+            if o.shape != t.shape or o.dtype is not t.dtype or o.device != dev or not o.is_contiguous():
                 raise ValueError("an output must be a contiguous tensor of its gradient's shape, type and device")
-    VPn, SZn, In = ctypes.c_void_p * n, ctypes.c_size_t * n, ctypes.c_int * n
+    if not _here(dev, stream):
+        with _on(dev, stream):
+            return _clip(grads, max_norm, outs, None)
+    VPn = ctypes.c_void_p * n
     gp = VPn(*[t.data_ptr() for t in grads])
     op = None if outs is None else VPn(*[t.data_ptr() for t in outs])
-    with _on(grads[0]), _alloc_on(stream, grads[0]):
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        ws = torch.empty(int(lib.sparse_block_clip_workspace_size()), dtype=torch.uint8, device=dev)
-        sa._check(lib.sparse_block_clip_grads(n, gp, op, SZn(*[t.numel() for t in grads]), In(*dts), float(max_norm),
-                                              sa._ptr(norm), sa._ptr(ws), ws.numel(), _stream(grads[0], stream)),
-                  "sparse_block_clip_grads")
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    ws = torch.empty(CLIP_WORKSPACE, dtype=torch.uint8, device=dev)
+    sa._check(lib.sparse_block_clip_grads(n, gp, op, (ctypes.c_size_t * n)(*[t.numel() for t in grads]),
+                                          (ctypes.c_int * n)(*dts), float(max_norm), norm.data_ptr(), ws.data_ptr(),
+                                          CLIP_WORKSPACE, torch.cuda.current_stream(dev).cuda_stream),
+              "sparse_block_clip_grads")
     return norm
+
+
+CLIP_WORKSPACE = int(lib.sparse_block_clip_workspace_size())
 
 
 def grad_norm(grads, stream=None):
