@@ -62,9 +62,22 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* slots, int& turn)
     if (lane == 0)
 #pragma unroll
       for (int k = 0; k < N; ++k) s[k * 32 + w] = v[k];
+    if (w == 0 && lane >= nw)  // every sum takes whole groups of four
+#pragma unroll
+      for (int k = 0; k < N; ++k) s[k * 32 + lane] = 0.f;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = warp_sum(lane < nw ? s[k * 32 + lane] : 0.f);
+    for (int k = 0; k < N; ++k) {
+      float4 a = reinterpret_cast<const float4*>(s + k * 32)[0];
+      for (int i = 4; i < nw; i += 4) {
+        const float4 b = *reinterpret_cast<const float4*>(s + k * 32 + i);
+        a.x += b.x;
+        a.y += b.y;
+        a.z += b.z;
+        a.w += b.w;
+      }
+      v[k] = (a.x + a.y) + (a.z + a.w);
+    }
   }
 }
 
@@ -106,19 +119,22 @@ struct Rows {
         ld(ldx * static_cast<long long>(sizeof(T))) {}
 };
 
-// The thread's words of a row: w = i0 + j n for j < NV.
-template <typename T, int NV>
+// The thread's words of a row: w = i0 + j n for j < NV.  EDGE: words may hold
+// other rows' elements (else rows begin and end on 16 bytes).
+template <typename T, int NV, bool EDGE>
 struct Words {
   static constexpr int N = 16 / sizeof(T);
   int i0, n, words, shift, C;
   __device__ __forceinline__ Words(const Rows<T>& x, long long r0, int C_, int i0_, int n_) : i0(i0_), n(n_), C(C_) {
-    shift = static_cast<int>((reinterpret_cast<uintptr_t>(x.base) + static_cast<uintptr_t>(r0 * x.ld)) & 15) / static_cast<int>(sizeof(T));
+    shift = !EDGE ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(x.base) + static_cast<uintptr_t>(r0 * x.ld)) & 15) / static_cast<int>(sizeof(T));
     words = (shift + C + N - 1) / N;
   }
   __device__ __forceinline__ bool has(int j) const { return i0 + j * n < words; }
   __device__ __forceinline__ int channel(int j, int u) const { return (i0 + j * n) * N - shift + u; }
-  __device__ __forceinline__ bool in(int j, int u) const { return static_cast<unsigned>(channel(j, u)) < static_cast<unsigned>(C); }
-  __device__ __forceinline__ bool whole(int j) const { return channel(j, 0) >= 0 && channel(j, N - 1) < C; }
+  __device__ __forceinline__ bool in(int j, int u) const {
+    return EDGE ? static_cast<unsigned>(channel(j, u)) < static_cast<unsigned>(C) : has(j);
+  }
+  __device__ __forceinline__ bool whole(int j) const { return !EDGE || (channel(j, 0) >= 0 && channel(j, N - 1) < C); }
   __device__ __forceinline__ const char* at(const Rows<T>& x, long long r, int j) const {
     return x.base + r * x.ld + static_cast<long long>(channel(j, 0)) * static_cast<long long>(sizeof(T));
   }
@@ -129,7 +145,7 @@ struct Words {
       if (!has(j)) continue;
       const char* p = at(x, r, j);
       uint4* d = slot + j * blockDim.x + threadIdx.x;
-      if (p >= x.base && p + 16 <= x.end) {
+      if (!EDGE || (p >= x.base && p + 16 <= x.end)) {
         cp_async16(d, p);
       } else {  // at the tensor's very ends
         T* e = reinterpret_cast<T*>(d);
@@ -158,21 +174,21 @@ struct Words {
   }
 };
 
-// y = (x - mean) rstd g + b, and the row's mean and rstd.  TPR threads a row (0: the block).
-template <typename T, int NV, int TPR>
-__global__ void __launch_bounds__(TPR ? 256 : 512)
+// y = (x - mean) rstd g + b, and the row's mean and rstd.  TPR threads a row (0: the block, of at most MAXT).
+template <typename T, int NV, int TPR, bool EDGE, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT <= 384 ? 2 : 1)
     norm_fwd_kernel(const T* x, long long ldx, const float* __restrict__ g, const float* __restrict__ b, T* y,
                     long long ldy, float* mean_out, float* rstd_out, long long M, int C, float eps) {
   constexpr int N = 16 / sizeof(T);
   extern __shared__ uint4 ring[];  // [kDepth][NV][threads]
-  __shared__ float slots[64];
+  __shared__ __align__(16) float slots[64];
   int turn = 0;
   constexpr int kPer = TPR ? TPR : 1;
   const long long gid = TPR ? (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / kPer : blockIdx.x;
   const long long step = TPR ? static_cast<long long>(gridDim.x) * blockDim.x / kPer : gridDim.x;
   const long long warp0 = TPR ? gid - (threadIdx.x & 31) / kPer : gid;  // the warp's first row
   const Rows<T> xr(x, ldx, M, C);
-  const Words<T, NV> ws(xr, gid, C, TPR ? threadIdx.x % kPer : threadIdx.x, TPR ? kPer : blockDim.x);
+  const Words<T, NV, EDGE> ws(xr, gid, C, TPR ? threadIdx.x % kPer : threadIdx.x, TPR ? kPer : blockDim.x);
   const int slot_words = NV * blockDim.x;
 #pragma unroll
   for (int d = 0; d < kDepth - 1; ++d) {
@@ -245,7 +261,7 @@ template <typename T>
 __global__ void __launch_bounds__(512)
     norm_fwd_wide_kernel(const T* x, long long ldx, const float* g, const float* b, T* y, long long ldy,
                          float* mean_out, float* rstd_out, long long M, int C, float eps) {
-  __shared__ float slots[64];
+  __shared__ __align__(16) float slots[64];
   int turn = 0;
   const float inv = 1.f / C;
   for (long long r = blockIdx.x; r < M; r += gridDim.x) {
@@ -271,15 +287,17 @@ __host__ __device__ constexpr int bwd_depth(int nv) { return nv >= 4 ? 2 : kDept
 
 // dx per row, and this block's sums of dy xh and dy per channel into
 // part[blockIdx.x][2][C].
-template <typename T, int NV, int TPR>
-__global__ void __launch_bounds__(TPR ? 256 : 512)
+// x and dy are read from the ring twice, before and after the row's two sums,
+// so that only the gains and the column sums stay in registers.
+template <typename T, int NV, int TPR, bool EDGE, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT <= 384 ? 2 : 1)
     norm_bwd_kernel(const T* x, long long ldx, const float* __restrict__ g, const T* dy, long long lddy,
                     const float* __restrict__ mean_in, const float* __restrict__ rstd_in, T* dx, long long lddx,
                     float* part, long long M, int C) {
   constexpr int N = 16 / sizeof(T);
   constexpr int kRing = bwd_depth(NV);
   extern __shared__ uint4 ring[];  // [kRing][x, dy][NV][threads]; then the row groups' sums [groups][2][C]
-  __shared__ float slots[128];
+  __shared__ __align__(16) float slots[128];
   pdl_trigger();
   int turn = 0;
   constexpr int kPer = TPR ? TPR : 1;
@@ -287,7 +305,7 @@ __global__ void __launch_bounds__(TPR ? 256 : 512)
   const long long step = TPR ? static_cast<long long>(gridDim.x) * blockDim.x / kPer : gridDim.x;
   const long long warp0 = TPR ? gid - (threadIdx.x & 31) / kPer : gid;
   const Rows<T> xr(x, ldx, M, C), dr(dy, lddy, M, C);
-  const Words<T, NV> ws(xr, gid, C, TPR ? threadIdx.x % kPer : threadIdx.x, TPR ? kPer : blockDim.x);
+  const Words<T, NV, EDGE> ws(xr, gid, C, TPR ? threadIdx.x % kPer : threadIdx.x, TPR ? kPer : blockDim.x);
   const int slot_words = NV * blockDim.x;
   float m_next[kRing - 1], r_next[kRing - 1];  // statistics of the rows in flight
 #pragma unroll
@@ -329,37 +347,40 @@ __global__ void __launch_bounds__(TPR ? 256 : 512)
       cp_commit();
     }
     cp_wait<kRing - 1>();
-    float xh[NV * N], t[NV * N], s[2] = {0.f, 0.f};
+    const uint4* xs = ring + 2 * at * slot_words;
+    const uint4* ds = xs + slot_words;
+    float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (live && ws.has(j)) {
-        float d[N];
-        ws.values(ring + 2 * at * slot_words, j, xh + j * N);
-        ws.values(ring + (2 * at + 1) * slot_words, j, d);
+        float xh[N], d[N];
+        ws.values(xs, j, xh);
+        ws.values(ds, j, d);
 #pragma unroll
         for (int u = 0; u < N; ++u) {
           const int k = j * N + u;
-          xh[k] = (xh[k] - mc) * rc;
-          t[k] = d[u] * gv[k];
-          s[0] += t[k];
-          s[1] += t[k] * xh[k];
-          if (ws.in(j, u)) {  // (outside the row xh is not 0, and an infinite rstd would make it NaN)
-            sg[k] += d[u] * xh[k];
-            sb[k] += d[u];
-          }
+          xh[u] = (xh[u] - mc) * rc;  // (not x rc - m rc, which cancels where the mean is large)
+          sg[k] = fmaf(d[u], xh[u], sg[k]);
+          sb[k] += d[u];
+          const float t = d[u] * gv[k];
+          s[0] += t;
+          s[1] = fmaf(t, xh[u], s[1]);
         }
       }
     row_sums<TPR>(s, slots, turn);
-    s[0] *= inv;
-    s[1] *= inv;
+    // dx = rc t - rc mean(t) - xh rc mean(t xh)
+    const float c0 = -rc * (s[0] * inv), c1 = -rc * (s[1] * inv);
     if (live)
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (ws.has(j)) {
-          float o[N];
+          float xh[N], d[N];
+          ws.values(xs, j, xh);
+          ws.values(ds, j, d);
 #pragma unroll
-          for (int u = 0; u < N; ++u) o[u] = rc * (t[j * N + u] - s[0] - xh[j * N + u] * s[1]);
-          ws.store(dx, lddx, r, j, o);
+          for (int u = 0; u < N; ++u)
+            d[u] = fmaf(rc, d[u] * gv[j * N + u], fmaf((xh[u] - mc) * rc, c1, c0));
+          ws.store(dx, lddx, r, j, d);
         }
     at = at + 1 == kRing ? 0 : at + 1;
   }
@@ -401,7 +422,7 @@ __global__ void __launch_bounds__(512)
     norm_bwd_wide_kernel(const T* x, long long ldx, const float* g, const T* dy, long long lddy, const float* mean_in,
                          const float* rstd_in, T* dx, long long lddx, float* part, long long M, int C) {
   extern __shared__ float sums[];  // [2][C]; a channel belongs to one thread
-  __shared__ float slots[128];
+  __shared__ __align__(16) float slots[128];
   int turn = 0;
   for (int i = threadIdx.x; i < C; i += blockDim.x) sums[i] = sums[C + i] = 0.f;
   const float inv = 1.f / C;
@@ -452,7 +473,6 @@ __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* part, i
 
 // --------------------------------------------------------------- clipping
 constexpr int kTensors = 120;   // tensors a launch (their table is a kernel argument)
-constexpr int kChunk = 16384;   // elements a block takes at a time
 constexpr int kClipBlocks = 592;
 
 struct ClipTensor {
@@ -466,6 +486,7 @@ struct ClipTable {
   ClipTensor t[kTensors];
   unsigned first[kTensors + 1];  // first chunk of each tensor
   int n;
+  unsigned chunk;  // elements a block takes at a time, a multiple of 8
 };
 
 // The squares of a word summed in float32, or in float64 where one is too
@@ -572,8 +593,8 @@ __global__ void __launch_bounds__(512) clip_norm_kernel(const __grid_constant__ 
   double s = 0.;
   for (unsigned c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
     const int i = tensor_of(t, c);
-    const unsigned long long at = static_cast<unsigned long long>(c - t.first[i]) * kChunk;
-    const unsigned n = static_cast<unsigned>(min(static_cast<unsigned long long>(kChunk), t.t[i].n - at));
+    const unsigned long long at = static_cast<unsigned long long>(c - t.first[i]) * t.chunk;
+    const unsigned n = static_cast<unsigned>(min(static_cast<unsigned long long>(t.chunk), t.t[i].n - at));
     if (t.t[i].dtype == SB_BF16) s += sum_squares(static_cast<const __nv_bfloat16*>(t.t[i].g) + at, n);
     else if (t.t[i].dtype == SB_FP16) s += sum_squares(static_cast<const __half*>(t.t[i].g) + at, n);
     else s += sum_squares(static_cast<const float*>(t.t[i].g) + at, n);
@@ -597,8 +618,8 @@ __global__ void __launch_bounds__(512)
   for (unsigned b = blockIdx.x; b < t.first[t.n]; b += gridDim.x) {
     const unsigned k = t.first[t.n] - 1 - b;
     const int i = tensor_of(t, k);
-    const unsigned long long at = static_cast<unsigned long long>(k - t.first[i]) * kChunk;
-    const unsigned n = static_cast<unsigned>(min(static_cast<unsigned long long>(kChunk), t.t[i].n - at));
+    const unsigned long long at = static_cast<unsigned long long>(k - t.first[i]) * t.chunk;
+    const unsigned n = static_cast<unsigned>(min(static_cast<unsigned long long>(t.chunk), t.t[i].n - at));
     if (t.t[i].g == t.t[i].out && c == 1.f) continue;
     if (t.t[i].dtype == SB_BF16)
       scale_to(static_cast<const __nv_bfloat16*>(t.t[i].g) + at, static_cast<__nv_bfloat16*>(t.t[i].out) + at, n, c);
@@ -671,6 +692,30 @@ int esize(int dtype) { return dtype == SB_FP32 ? 4 : 2; }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// go(words a thread, threads a row, EDGE, block's threads at most) for a row of `words` words; -1 above the widest.
+// Narrow rows share a warp; up to 64 words a warp takes a row, above that a block: with 384 threads two blocks of it
+// fit an SM, which hides the row's barriers (16384 x 6144 bf16 backward: one block of 512 threads 273 us).
+template <typename T, typename F, typename E>
+int by_width(int words, F&& go, E edge) {
+  using std::integral_constant;
+  using I1 = integral_constant<int, 1>;
+  using I2 = integral_constant<int, 2>;
+  using Warp = integral_constant<int, 32>;
+  using Block = integral_constant<int, 0>;
+  using T256 = integral_constant<int, 256>;
+  using T384 = integral_constant<int, 384>;
+  using T512 = integral_constant<int, 512>;
+  if (words <= 8) return go(I1{}, integral_constant<int, 8>{}, edge, T256{});
+  if (words <= 16) return go(I1{}, integral_constant<int, 16>{}, edge, T256{});
+  if (words <= 32) return go(I1{}, Warp{}, edge, T256{});
+  if (words <= 64) return go(I2{}, Warp{}, edge, T256{});
+  if (words <= 384) return go(I1{}, Block{}, edge, T384{});
+  if (words <= 768) return go(I2{}, Block{}, edge, T384{});
+  if (words <= 1024) return go(I2{}, Block{}, edge, T512{});
+  if (words <= 2048) return go(integral_constant<int, 4>{}, Block{}, edge, T512{});
+  return -1;
+}
+
 // Whether the rows of two tensors lie at the same offsets from 16 bytes.
 bool alike(const void* a, int64_t lda, const void* b, int64_t ldb, int es) {
   return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0 && ((lda - ldb) * es) % 16 == 0;
@@ -705,11 +750,12 @@ int sparse_block_layer_norm_fwd(const void* x, int64_t ldx, const float* g, cons
   if (dev < 0) return SA_ERR_CUDA;
   const int n_sm = sms(dev), words = words_of(x, ldx, C, es);
   const bool same = alike(x, ldx, y, ldy, es);
+  const bool edge = !aligned(x, 16) || (ldx * es) % 16 != 0 || (C * es) % 16 != 0;
   return by_type(dtype, [&](auto t) -> int {
     using T = decltype(t);
-    auto go = [&](auto nv, auto tpr) -> int {
+    auto go = [&](auto nv, auto tpr, auto edge, auto maxt) -> int {
       constexpr int NV = nv.value, TPR = tpr.value;
-      constexpr auto K = norm_fwd_kernel<T, NV, TPR>;
+      constexpr auto K = norm_fwd_kernel<T, NV, TPR, edge.value, maxt.value>;
       const int threads = TPR ? 256 : (words + 32 * NV - 1) / (32 * NV) * 32;
       const int rows = TPR ? 256 / (TPR ? TPR : 1) : 1;  // rows of a block at a time
       const size_t smem = static_cast<size_t>(kDepth) * NV * threads * 16;
@@ -721,15 +767,9 @@ int sparse_block_layer_norm_fwd(const void* x, int64_t ldx, const float* g, cons
                                                            mean, rstd, M, C, eps);
       return launched();
     };
-    using std::integral_constant;
     if (same) {
-      if (words <= 8) return go(integral_constant<int, 1>{}, integral_constant<int, 8>{});
-      if (words <= 16) return go(integral_constant<int, 1>{}, integral_constant<int, 16>{});
-      if (words <= 32) return go(integral_constant<int, 1>{}, integral_constant<int, 32>{});
-      if (words <= 64) return go(integral_constant<int, 2>{}, integral_constant<int, 32>{});
-      if (words <= 512) return go(integral_constant<int, 1>{}, integral_constant<int, 0>{});
-      if (words <= 1024) return go(integral_constant<int, 2>{}, integral_constant<int, 0>{});
-      if (words <= 2048) return go(integral_constant<int, 4>{}, integral_constant<int, 0>{});
+      const int st = edge ? by_width<T>(words, go, std::true_type{}) : by_width<T>(words, go, std::false_type{});
+      if (st >= 0) return st;
     }
     const int grid = static_cast<int>(std::min<long long>(M, static_cast<long long>(n_sm) * 4));
     norm_fwd_wide_kernel<T><<<grid, 512, 0, s>>>(static_cast<const T*>(x), ldx, g, b, static_cast<T*>(y), ldy, mean, rstd, M,
@@ -764,11 +804,12 @@ int sparse_block_layer_norm_bwd(const void* x, int64_t ldx, const float* g, cons
   if (M > 0) {
     const int words = words_of(x, ldx, C, es);
     const bool same = alike(x, ldx, dy, lddy, es) && alike(x, ldx, dx, lddx, es);
+    const bool edge = !aligned(x, 16) || (ldx * es) % 16 != 0 || (C * es) % 16 != 0;
     const int st = by_type(dtype, [&](auto t) -> int {
       using T = decltype(t);
-      auto go = [&](auto nv, auto tpr) -> int {
+      auto go = [&](auto nv, auto tpr, auto edge, auto maxt) -> int {
         constexpr int NV = nv.value, TPR = tpr.value;
-        constexpr auto K = norm_bwd_kernel<T, NV, TPR>;
+        constexpr auto K = norm_bwd_kernel<T, NV, TPR, edge.value, maxt.value>;
         const int threads = TPR ? 256 : (words + 32 * NV - 1) / (32 * NV) * 32;
         const int rows = TPR ? 256 / (TPR ? TPR : 1) : 1;
         // the ring, and in its place afterwards the row groups' sums of up to NV TPR words
@@ -784,17 +825,9 @@ int sparse_block_layer_norm_bwd(const void* x, int64_t ldx, const float* g, cons
                                    static_cast<T*>(dx), lddx, part, M, C);
         return launched();
       };
-      using std::integral_constant;
-      if (same) {
-        if (words <= 8) return go(integral_constant<int, 1>{}, integral_constant<int, 8>{});
-        if (words <= 16) return go(integral_constant<int, 1>{}, integral_constant<int, 16>{});
-        if (words <= 32) return go(integral_constant<int, 1>{}, integral_constant<int, 32>{});
-        if (words <= 64) return go(integral_constant<int, 2>{}, integral_constant<int, 32>{});
-        if (words <= 512) return go(integral_constant<int, 1>{}, integral_constant<int, 0>{});
-        if (words <= 1024) return go(integral_constant<int, 2>{}, integral_constant<int, 0>{});
-        if constexpr (sizeof(T) == 4) {
-          if (words <= 2048) return go(integral_constant<int, 4>{}, integral_constant<int, 0>{});
-        }
+      if (same && (sizeof(T) == 4 || words <= 1024)) {
+        const int r = edge ? by_width<T>(words, go, std::true_type{}) : by_width<T>(words, go, std::false_type{});
+        if (r >= 0) return r;
       }
       constexpr auto K = norm_bwd_wide_kernel<T>;
       const size_t smem = 2 * static_cast<size_t>(C) * sizeof(float);
@@ -852,6 +885,11 @@ int sparse_block_clip_grads(int n, const void* const* grads, void* const* outs, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   double* part = static_cast<double*>(ws);
   ClipTable t;
+  // A chunk is 2048 elements (one word a thread and more) to 65536: small enough that every block has one, large
+  // enough that finding its tensor costs nothing.
+  size_t total = 0;
+  for (const ClipTensor& x : ts) total += x.n;
+  t.chunk = static_cast<unsigned>(std::min<size_t>(std::max<size_t>((total / (2 * kClipBlocks) + 2047) / 2048 * 2048, 2048), 65536));
   // `norm` pass over the tensors, then the scaling pass; kTensors of them a launch
   for (int pass = 0; pass < 2; ++pass) {
     size_t at = 0;
@@ -861,7 +899,7 @@ int sparse_block_clip_grads(int n, const void* const* grads, void* const* outs, 
       t.first[0] = 0;
       if (pass == 0 || outs)
         while (at < ts.size() && t.n < kTensors) {
-          const size_t chunks = (ts[at].n + kChunk - 1) / kChunk;
+          const size_t chunks = (ts[at].n + t.chunk - 1) / t.chunk;
           if (t.first[t.n] + chunks > 0x7fffffffu) break;
           t.t[t.n] = ts[at++];
           t.first[t.n + 1] = t.first[t.n] + static_cast<unsigned>(chunks);

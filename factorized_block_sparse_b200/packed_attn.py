@@ -21,6 +21,7 @@ import ctypes
 import os
 
 import numpy as np
+import torch
 
 from . import sparse_attn as sa
 
@@ -89,8 +90,6 @@ class Layout:
 
     def upload(self, device=None, stream=None):
         """Tables to ``device`` (default: the current one); needed before a call is captured into a graph."""
-        import torch
-
         with torch.cuda.device(device):
             sa._check(lib.packed_attn_layout_upload(self.handle, sa._stream_ptr(stream)), "packed_attn_layout_upload")
 
@@ -108,8 +107,6 @@ class Layout:
 
 def _check_tensors(q, k, v, layout, more=()):
     """Shapes, types, strides and devices of a call; returns (T, Hq, Hkv, D, type code)."""
-    import torch
-
     qs, ks = q.shape, k.shape
     if len(qs) != 3 or len(ks) != 3:
         raise ValueError("expected q [T, Hq, D] and k, v [T, Hkv, D]")
@@ -142,8 +139,6 @@ def _desc(t):
 
 
 def _check_lse(lse, Hq, T, q):
-    import torch
-
     if tuple(lse.shape) != (Hq, T) or lse.dtype != torch.float32 or lse.device != q.device:
         raise ValueError(f"lse must be float32 [{Hq}, {T}] on the device of q")
     if T > 1 and lse.stride(1) != 1:
@@ -151,12 +146,15 @@ def _check_lse(lse, Hq, T, q):
     return lse.stride(0) if Hq > 1 else T
 
 
+# torch's current stream of a device as an integer, without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(device, stream, what, fn, *args):
     """``fn(*args, stream)`` with ``device`` as the current one, on the given stream or torch's current one of it."""
-    import torch
-
     if stream is None:
-        s = torch.cuda.current_stream(device).cuda_stream
+        s = _raw_stream(device.index)
     else:
         s = stream if isinstance(stream, int) else stream.cuda_stream
     if device.index == torch.cuda.current_device():
@@ -203,21 +201,16 @@ def packed_attn_status(stream=None):
 # ------------------------------------------------------------ conveniences
 def _on_stream(stream, device):
     """torch work of a call (allocation, zeroing) on the stream that the call runs on."""
-    import torch
-
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
 
 
 def _outputs(q, layout, shapes):
     """Tensors of ``(shape, dtype, dimension of the rows)``, zero in the rows behind the last sequence."""
-    import torch
-
-    outs = []
-    for shape, dtype, dim in shapes:
-        t = torch.empty(shape, dtype=dtype, device=q.device)
-        if layout.rows < shape[dim]:
-            t.narrow(dim, layout.rows, shape[dim] - layout.rows).zero_()
-        outs.append(t)
+    dev, rows = q.device, layout.rows
+    outs = [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype, _ in shapes]
+    for t, (shape, _, dim) in zip(outs, shapes):
+        if rows < shape[dim]:
+            t.narrow(dim, rows, shape[dim] - rows).zero_()
     return outs
 
 
@@ -229,8 +222,6 @@ def _allocate(q, layout, shapes, stream):
 
 
 def workspace(Hq, Hkv, D, layout, device):
-    import torch
-
     n = int(lib.packed_attn_bwd_workspace_size(Hq, Hkv, D, layout.handle))
     if n == 0:
         raise sa.SparseAttnError(sa.SA_ERR_INVALID_ARG, "packed_attn_bwd_workspace_size")
@@ -239,8 +230,6 @@ def workspace(Hq, Hkv, D, layout, device):
 
 def forward(q, k, v, layout, stream=None, scale=None):
     """Allocates ``o`` and ``lse`` (zero in rows behind the last sequence) and runs the forward pass."""
-    import torch
-
     dims = _check_tensors(q, k, v, layout)
     T, Hq, _, D, _ = dims
     o, lse = _allocate(q, layout, (((T, Hq, D), q.dtype, 0), ((Hq, T), torch.float32, 1)), stream)

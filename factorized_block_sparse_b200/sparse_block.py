@@ -12,6 +12,8 @@ parameters and parameter gradients float32.  There is no CPU fallback.
 import ctypes
 import os
 
+import torch
+
 from . import sparse_attn as sa
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -139,8 +141,6 @@ def gelu(u, grad=False, stream=None):
 
 # ------------------------------------------------------------ layer norm
 def _dtype(t):
-    import torch
-
     dt = t.dtype
     if dt is torch.bfloat16:
         return 0
@@ -177,8 +177,6 @@ def _rows(name, t):
 
 
 def _vector(name, t, C, device):
-    import torch
-
     if t.dtype is not torch.float32 or t.device != device or t.shape != (C,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 [{C}] tensor on {device}")
     return t.data_ptr()
@@ -187,8 +185,6 @@ def _vector(name, t, C, device):
 def _on(device, stream):
     """A context of the device and the stream that a call runs on, for its allocations and its launch."""
     import contextlib
-
-    import torch
 
     cm = contextlib.ExitStack()
     if device.index != torch.cuda.current_device():
@@ -199,10 +195,13 @@ def _on(device, stream):
     return cm
 
 
+# torch's current stream of a device as an integer, without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _here(device, stream):
     """Whether a call runs on the current device and its current stream, so that it needs no context."""
-    import torch
-
     return stream is None and device.index == torch.cuda.current_device()
 
 
@@ -210,8 +209,6 @@ def layer_norm(x, g, b=None, eps=1e-5, stream=None):
     """``(y, mean, rstd)`` of rows ``x [..., C]`` (bf16, fp16 or float32; rows at any one stride): y of x's type and
     shape, contiguous; mean and rstd float32 of the leading shape, for ``layer_norm_backward``.  ``g`` and ``b`` are
     float32 ``[C]``; without ``b`` there is no bias."""
-    import torch
-
     dev = x.device
     M, C, ld = _rows("x", x)
     dt = _dtype(x)
@@ -225,16 +222,15 @@ def layer_norm(x, g, b=None, eps=1e-5, stream=None):
     mp = stats.data_ptr()
     if M:
         sa._check(lib.sparse_block_layer_norm_fwd(x.data_ptr(), ld, gp, bp, y.data_ptr(), C, mp, mp + 4 * M, M, C, eps,
-                                                  dt, torch.cuda.current_stream(dev).cuda_stream),
+                                                  dt, _raw_stream(dev.index)),
                   "sparse_block_layer_norm_fwd")
-    return y, stats[0], stats[1]
+    mean, rstd = stats.unbind(0)
+    return y, mean, rstd
 
 
 def layer_norm_backward(x, g, dy, mean, rstd, bias=True, stream=None):
     """``(dx, dg, db)`` from ``layer_norm``'s input, gain and statistics and the upstream gradient ``dy``: dx of x's
     type and shape, contiguous; dg and db float32 ``[C]`` (db None without ``bias``)."""
-    import torch
-
     dev = x.device
     M, C, ld = _rows("x", x)
     dt = _dtype(x)
@@ -259,15 +255,13 @@ def layer_norm_backward(x, g, dy, mean, rstd, bias=True, stream=None):
     gptr = grads.data_ptr()
     sa._check(lib.sparse_block_layer_norm_bwd(x.data_ptr(), ld, gp, dy.data_ptr(), ldd, mean.data_ptr(), rstd.data_ptr(),
                                               dx.data_ptr(), C, gptr, gptr + 4 * C if bias else None, M, C, dt,
-                                              ws.data_ptr(), max(n, 256), torch.cuda.current_stream(dev).cuda_stream),
+                                              ws.data_ptr(), max(n, 256), _raw_stream(dev.index)),
               "sparse_block_layer_norm_bwd")
     return dx, dg, db
 
 
 # ------------------------------------------------- norm and clipping of gradients
 def _clip(grads, max_norm, out, stream):
-    import torch
-
     grads = list(grads.values()) if isinstance(grads, dict) else list(grads)
     outs = None if out is None else (list(out.values()) if isinstance(out, dict) else list(out))
     if not grads:
@@ -296,7 +290,7 @@ def _clip(grads, max_norm, out, stream):
     ws = torch.empty(CLIP_WORKSPACE, dtype=torch.uint8, device=dev)
     sa._check(lib.sparse_block_clip_grads(n, gp, op, (ctypes.c_size_t * n)(*[t.numel() for t in grads]),
                                           (ctypes.c_int * n)(*dts), float(max_norm), norm.data_ptr(), ws.data_ptr(),
-                                          CLIP_WORKSPACE, torch.cuda.current_stream(dev).cuda_stream),
+                                          CLIP_WORKSPACE, _raw_stream(dev.index)),
               "sparse_block_clip_grads")
     return norm
 
