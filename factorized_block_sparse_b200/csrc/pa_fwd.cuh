@@ -35,9 +35,6 @@
 
 namespace pa {
 
-template <int D>
-constexpr int kFwdPoly = D <= 64 ? 1 : 0;
-
 enum Pairing : int { kSingle = 0, kHeads = 1, kTiles = 2 };
 
 struct FwdArgs {
@@ -416,10 +413,10 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 e =
-                ex2_pair<T, kFwdPoly<D>>(f2_fma(f2_pack(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc2, ng2), i);
-            rs[i & 3] = f2_add(rs[i & 3], f2_pack(e.x, e.y));
-            pk[i] = Elem<T>::pack(e.x, e.y);
+            const float2 e = f2_unpack(f2_fma(f2_pack(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc2, ng2));
+            const float p0 = ex2(e.x), p1 = ex2(e.y);
+            rs[i & 3] = f2_add(rs[i & 3], f2_pack(p0, p1));
+            pk[i] = Elem<T>::pack(p0, p1);
           }
           tmem_st8(t_p + c * 16, pk);
           tmem_st8(t_p + c * 16 + 8, pk + 8);
@@ -474,7 +471,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       }
       if (half == 0 && lane < rows)
         a.lse[static_cast<long long>(it.h[u]) * a.ls + row0 + lane] =
-            (m_used + lg2(l_sum) - Elem<T>::kBias) * 0.6931471805599453f;
+            (m_used + log2f(l_sum) - Elem<T>::kBias) * 0.6931471805599453f;
     }
   }
   tc_fence_before();
