@@ -27,9 +27,9 @@
 // order, so a product behind another that reads its destination columns needs
 // no wait.
 //
-// Roles of both (704 threads): warps 0..15 four compute groups (thread = row
-// of the tile, 32 columns of the step each), warps 16..19 the read-out of an
-// item's result, warp 20 lane 0 the TMA producer, warp 21 TMEM and the MMAs.
+// Roles of both: compute groups of four warps (thread = row of the tile,
+// kCols columns of the step each), four warps for the read-out of an item's
+// result, one whose lane 0 is the TMA producer, one for TMEM and the MMAs.
 #pragma once
 
 #include <type_traits>
@@ -42,7 +42,39 @@ template <int D>
 constexpr int kDkvPoly = D <= 64 ? 1 : 3;
 template <int D>
 constexpr int kDqPoly = D <= 64 ? 1 : 0;
-constexpr int kBwdThreads = 704, kBwdComputeWarps = 16;
+// Columns of the step that a compute thread takes.
+constexpr int kCols = 32;
+constexpr int kBwdComputeWarps = 4 * 128 / kCols, kBwdThreads = 32 * (kBwdComputeWarps + 6);
+
+// TMEM column, inside its 128, of k-step kk of a weight tile: each group's
+// packed pairs begin at the first of its kCols score columns.
+__device__ constexpr uint32_t weight_col(int kk) { return (kk / (kCols / 16)) * kCols + (kk % (kCols / 16)) * 8; }
+
+// Position in a ring of N stages: the stage and its phase's parity.
+template <int N>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == N) st = 0, ph ^= 1;
+  }
+};
+
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float* v) {
+#pragma unroll
+  for (int c = 0; c < kCols / 32; ++c) tmem_ld32(taddr + c * 32, v + c * 32);
+  tmem_wait_ld();
+}
+__device__ __forceinline__ void tmem_st_weights(uint32_t taddr, const uint32_t* pk) {
+#pragma unroll
+  for (int c = 0; c < kCols / 16; ++c) tmem_st8(taddr + c * 8, pk + c * 8);
+  tmem_wait_st();
+}
+// Zeroes the pairs' values whose bit is not set (a bit a column, kCols / 32 words).
+__device__ __forceinline__ void keep_bits(float* v, const uint32_t* m) {
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) v[i] = ((m[i / 32] >> (i % 32)) & 1u) ? v[i] : 0.f;
+}
 
 // TPR threads a row, 8 columns each.
 template <typename T, int D>
@@ -71,7 +103,7 @@ __global__ void __launch_bounds__(256)
     for (int w = TPR / 2; w >= 1; w >>= 1) d += __shfl_xor_sync(0xffffffffu, d, w);
     if (tid % TPR == 0) {
       out[r] = in ? -1.4426950408889634f * lse[static_cast<long long>(h) * ls + s.start + i] : -INFINITY;
-      out[kTile + r] = d;
+      out[kTile + r] = -d;
     }
   }
 }
@@ -98,7 +130,7 @@ struct DkvArgs {
   const Slot* slots;
   int n_items, Hkv, G;
   int n_tiles;      // 128-row tiles of all sequences
-  const float* ld;  // [Hq][n_tiles][2][128]: -lse log2 e (padding -inf), delta (padding 0)
+  const float* ld;  // [Hq][n_tiles][2][128]: -lse log2 e (padding -inf), -delta (padding 0)
   View dk, dv;
   float scale, scale_log2;
 };
@@ -183,14 +215,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 21) tmem_alloc<512>(tmem_slot);
+  if (warp == kBwdComputeWarps + 5) tmem_alloc<512>(tmem_slot);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const SlotWalk walk(a.slots, a.n_items, a.Hkv);
 
-  if (warp == 20) {
+  if (warp == kBwdComputeWarps + 4) {
     // -------------------------------------------------------------- producer
     if (lane == 0) {
       bool ok = true;
@@ -234,7 +266,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           mbar_wait_drain(bar_do_full + i % C::OST, (i / C::OST) & 1);
       }
     }
-  } else if (warp == 21) {
+  } else if (warp == kBwdComputeWarps + 5) {
     // ------------------------------------------------------------------ MMAs
     constexpr uint32_t id_s = make_idesc<T>(128, 128, false, false);
     constexpr uint32_t id_o = make_idesc<T>(128, D, false, true);
@@ -305,7 +337,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)  // 16 queries = 8 TMEM columns of P^T, each group's from its first column on
-            mma_bf16_ts(tmem + C::COL_DV, tmem + (g % C::NS) * 128 + (kk / 2) * 32 + (kk % 2) * 8, do_mn.at(G::mnstep(kk)),
+            mma_bf16_ts(tmem + C::COL_DV, tmem + (g % C::NS) * 128 + weight_col(kk), do_mn.at(G::mnstep(kk)),
                         id_o, j > 0 || kk > 0);
           mma_commit(bar_do_free + so);
         }
@@ -315,11 +347,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (C::DS_IN_S && j + 1 < it.n && !(ok = issue_dp(g + 1))) break;
         tc_fence_after();
         const Desc q_mn = G::mnmajor(smem_u32(smem + C::OFF_Q) + sq * G::BYTES);
-        const uint32_t t_ds = tmem + (C::DS_IN_S ? (g % C::NS) * 128 + 16 : C::COL_DP);
+        const uint32_t t_ds = tmem + (C::DS_IN_S ? (g % C::NS) * 128 + kCols / 2 : C::COL_DP);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_bf16_ts(tmem + C::COL_DK, t_ds + (kk / 2) * 32 + (kk % 2) * 8, q_mn.at(G::mnstep(kk)), id_o,
+            mma_bf16_ts(tmem + C::COL_DK, t_ds + weight_col(kk), q_mn.at(G::mnstep(kk)), id_o,
                         j > 0 || kk > 0);
           mma_commit(bar_q_free + sq);
         }
@@ -340,7 +372,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_wait_drain(bar_drain, 0);
     }
     __syncwarp();
-  } else if (warp >= 16) {
+  } else if (warp >= kBwdComputeWarps) {
     // --------------------------------------------------- read-out of dK, dV
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
@@ -363,31 +395,36 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else {
     // ------------------------------------------------------ P^T and dS^T
-    const int w = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;  // w: which 32 queries
-    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_dp = tmem + lane_base + C::COL_DP + w * 32;
+    const int w = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;  // w: which kCols queries
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + w * kCols;
     const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
-    const int first = row - w * 32;  // on the diagonal: the first query at or behind the key
-    const uint32_t behind = first <= 0 ? 0xffffffffu : (first >= 32 ? 0u : 0xffffffffu << first);
+    uint32_t behind[kCols / 32];  // on the diagonal: the queries at or behind the key
+#pragma unroll
+    for (int c = 0; c < kCols / 32; ++c) {
+      const int first = row - w * kCols - c * 32;
+      behind[c] = first <= 0 ? 0xffffffffu : (first >= 32 ? 0u : 0xffffffffu << first);
+    }
+    const float* lse0 = reinterpret_cast<const float*>(smem + C::OFF_LSE) + w * kCols;
+    const float* delta0 = reinterpret_cast<const float*>(smem + C::OFF_DELTA) + w * kCols;
     bool ok = true;
-    int g = 0;
+    Ring<C::QST> rq;
+    Ring<C::OST> ro;
+    Ring<C::NS> rs;
+    uint32_t ph = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
       const DkvItem it = dkv_item(a, walk.take(item, k), item);
-      for (int j = 0, in_head = 0; ok && j < it.n; ++j, ++g) {
-        const int sq = g % C::QST, so = g % C::OST, sb = g % C::NS;
+      for (int j = 0, in_head = 0; ok && j < it.n; ++j) {
         const bool diag = in_head == 0;
         if (++in_head == it.per) in_head = 0;
-        const uint32_t t_s = tmem + lane_base + sb * 128 + w * 32;
-        const float* lse = reinterpret_cast<const float*>(smem + C::OFF_LSE + so * C::VEC) + w * 32;
-        const float* delta = reinterpret_cast<const float*>(smem + C::OFF_DELTA + sq * C::VEC) + w * 32;
-        ok = mbar_wait(bar_do_full + so, (g / C::OST) & 1, abort_flag) &&
-             mbar_wait(bar_s_full + sb, (g / C::NS) & 1, abort_flag);
+        const uint32_t t_s = t_row + rs.st * 128, t_dp = t_row + C::COL_DP;
+        const float* lse = lse0 + ro.st * kTile;
+        const float* delta = delta0 + rq.st * kTile;
+        ok = mbar_wait(bar_do_full + ro.st, ro.ph, abort_flag) && mbar_wait(bar_s_full + rs.st, rs.ph, abort_flag);
         tc_fence_after();
-        float p[32];
-        tmem_ld32(t_s, p);
-        tmem_wait_ld();
+        float p[kCols];
+        tmem_ld_cols(t_s, p);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < kCols / 4; ++c) {
           const float4 l = *reinterpret_cast<const float4*>(lse + 4 * c);
           const float2 e0 = ex2_pair<T, kDkvPoly<D>>(f2_fma(f2_pack(p[4 * c], p[4 * c + 1]), sc2, f2_pack(l.x, l.y)), 2 * c);
           const float2 e1 =
@@ -397,51 +434,46 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           p[4 * c + 2] = e1.x;
           p[4 * c + 3] = e1.y;
         }
-        if (diag) {
+        if (diag) keep_bits(p, behind);
+        uint32_t pk[kCols / 2];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) p[i] = ((behind >> i) & 1u) ? p[i] : 0.f;
-        }
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) pk[i] = Elem<T>::pack(p[2 * i] * kP, p[2 * i + 1] * kP);
-        tmem_st8(t_s, pk);
-        tmem_st8(t_s + 8, pk + 8);
-        tmem_wait_st();
+        for (int i = 0; i < kCols / 2; ++i) pk[i] = Elem<T>::pack(p[2 * i] * kP, p[2 * i + 1] * kP);
+        tmem_st_weights(t_s, pk);
         tc_fence_before();
         warp_arrive(bar_p_full, lane);
 
-        ok = ok && mbar_wait(bar_q_full + sq, (g / C::QST) & 1, abort_flag) && mbar_wait(bar_dp_full, g & 1, abort_flag);
+        ok = ok && mbar_wait(bar_q_full + rq.st, rq.ph, abort_flag) && mbar_wait(bar_dp_full, ph, abort_flag);
         tc_fence_after();
-        float dp[32];
-        tmem_ld32(t_dp, dp);
-        tmem_wait_ld();
+        float dp[kCols];
+        tmem_ld_cols(t_dp, dp);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < kCols / 4; ++c) {
           const float4 dl = *reinterpret_cast<const float4*>(delta + 4 * c);
-          float s0 = p[4 * c] * (dp[4 * c] - dl.x), s1 = p[4 * c + 1] * (dp[4 * c + 1] - dl.y);
-          float s2 = p[4 * c + 2] * (dp[4 * c + 2] - dl.z), s3 = p[4 * c + 3] * (dp[4 * c + 3] - dl.w);
-          if (diag) {  // a masked place stays 0 whatever dP holds there
-            const uint32_t m = behind >> (4 * c);
-            s0 = (m & 1u) ? s0 : 0.f;
-            s1 = (m & 2u) ? s1 : 0.f;
-            s2 = (m & 4u) ? s2 : 0.f;
-            s3 = (m & 8u) ? s3 : 0.f;
-          }
-          pk[2 * c] = Elem<T>::pack(s0, s1);
-          pk[2 * c + 1] = Elem<T>::pack(s2, s3);
+          const float2 d0 = f2_unpack(f2_mul(f2_pack(p[4 * c], p[4 * c + 1]),
+                                             f2_add(f2_pack(dp[4 * c], dp[4 * c + 1]), f2_pack(dl.x, dl.y))));
+          const float2 d1 = f2_unpack(f2_mul(f2_pack(p[4 * c + 2], p[4 * c + 3]),
+                                             f2_add(f2_pack(dp[4 * c + 2], dp[4 * c + 3]), f2_pack(dl.z, dl.w))));
+          dp[4 * c] = d0.x;
+          dp[4 * c + 1] = d0.y;
+          dp[4 * c + 2] = d1.x;
+          dp[4 * c + 3] = d1.y;
         }
-        const uint32_t t_ds = C::DS_IN_S ? t_s + 16 : t_dp;
-        tmem_st8(t_ds, pk);
-        tmem_st8(t_ds + 8, pk + 8);
-        tmem_wait_st();
+        if (diag) keep_bits(dp, behind);  // a masked place stays 0 whatever dP holds there
+#pragma unroll
+        for (int i = 0; i < kCols / 2; ++i) pk[i] = Elem<T>::pack(dp[2 * i], dp[2 * i + 1]);
+        tmem_st_weights(C::DS_IN_S ? t_s + kCols / 2 : t_dp, pk);
         tc_fence_before();
         warp_arrive(bar_ds_full, lane);
+        rq.next();
+        ro.next();
+        rs.next();
+        ph ^= 1;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 21) {
+  if (warp == kBwdComputeWarps + 5) {
     tc_fence_after();
     tmem_dealloc<512>(tmem);
   }
@@ -512,14 +544,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 21) tmem_alloc<512>(tmem_slot);
+  if (warp == kBwdComputeWarps + 5) tmem_alloc<512>(tmem_slot);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const SlotWalk walk(a.slots, a.n_items, a.Hq);
 
-  if (warp == 20) {
+  if (warp == kBwdComputeWarps + 4) {
     // -------------------------------------------------------------- producer
     if (lane == 0) {
       bool ok = true;
@@ -558,7 +590,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int i = nv > C::VST ? nv - C::VST : 0; i < nv; ++i) mbar_wait_drain(bar_v_full + i % C::VST, (i / C::VST) & 1);
       }
     }
-  } else if (warp == 21) {
+  } else if (warp == kBwdComputeWarps + 5) {
     // ------------------------------------------------------------------ MMAs
     constexpr uint32_t id_s = make_idesc<T>(128, 128, false, false);
     constexpr uint32_t id_o = make_idesc<T>(128, D, false, true);
@@ -614,7 +646,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_bf16_ts(tmem + C::COL_DQ + ob * D, tmem + (g & 1) * 128 + (kk / 2) * 32 + (kk % 2) * 8, k_mn.at(G::mnstep(kk)),
+            mma_bf16_ts(tmem + C::COL_DQ + ob * D, tmem + (g & 1) * 128 + weight_col(kk), k_mn.at(G::mnstep(kk)),
                         id_o, j > 0 || kk > 0);
           mma_commit(bar_k_free + sk);
         }
@@ -631,7 +663,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_wait_drain(bar_drain, 0);
     }
     __syncwarp();
-  } else if (warp >= 16) {
+  } else if (warp >= kBwdComputeWarps) {
     // ------------------------------------------------------ read-out of dQ
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
@@ -651,59 +683,62 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else {
     // ---------------------------------------------------------- P and dS
-    const int w = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;  // w: which 32 keys
-    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_dp = tmem + lane_base + C::COL_DP + w * 32;
+    const int w = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;  // w: which kCols keys
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + w * kCols;
     const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
-    const int last = row - w * 32;  // on the diagonal: the last key that the query sees
-    const uint32_t before = last < 0 ? 0u : (last >= 31 ? 0xffffffffu : (2u << last) - 1u);
+    uint32_t before[kCols / 32];  // on the diagonal: the keys that the query sees
+#pragma unroll
+    for (int c = 0; c < kCols / 32; ++c) {
+      const int last = row - w * kCols - c * 32;
+      before[c] = last < 0 ? 0u : (last >= 31 ? 0xffffffffu : (2u << last) - 1u);
+    }
     bool ok = true;
-    int g = 0;
+    Ring<2> rs;
+    uint32_t ph = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
       const int h = item % a.Hq;
       const Slot s = walk.take(item, k);
       const float* ld = a.ld + (static_cast<long long>(h) * a.n_tiles + s.base + s.tile) * 2 * kTile;
-      const float neg_lse = ld[row], delta = ld[kTile + row];
-      const uint64_t l2 = f2_pack(neg_lse, neg_lse);
-      for (int j = 0; ok && j <= s.tile; ++j, ++g) {
+      const float neg_lse = ld[row], neg_delta = ld[kTile + row];
+      const uint64_t l2 = f2_pack(neg_lse, neg_lse), d2 = f2_pack(neg_delta, neg_delta);
+      for (int j = 0; ok && j <= s.tile; ++j) {
         const bool diag = j == s.tile;
-        ok = mbar_wait(bar_s_full + (g & 1), (g >> 1) & 1, abort_flag);
+        const uint32_t t_s = t_row + rs.st * 128;
+        ok = mbar_wait(bar_s_full + rs.st, rs.ph, abort_flag);
         tc_fence_after();
-        float p[32];
-        const uint32_t t_s = tmem + lane_base + (g & 1) * 128 + w * 32;
-        tmem_ld32(t_s, p);
-        tmem_wait_ld();
+        float p[kCols];
+        tmem_ld_cols(t_s, p);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < kCols / 2; ++i) {
           const float2 e = ex2_pair<T, kDqPoly<D>>(f2_fma(f2_pack(p[2 * i], p[2 * i + 1]), sc2, l2), i);
           p[2 * i] = e.x;
           p[2 * i + 1] = e.y;
         }
-        ok = ok && mbar_wait(bar_dp_full, g & 1, abort_flag);
+        ok = ok && mbar_wait(bar_dp_full, ph, abort_flag);
         tc_fence_after();
-        float dp[32];
-        tmem_ld32(t_dp, dp);
-        tmem_wait_ld();
+        float dp[kCols];
+        tmem_ld_cols(t_row + C::COL_DP, dp);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) dp[i] = p[i] * (dp[i] - delta);
-        if (diag) {  // a masked place is 0 whatever S and dP hold there
-#pragma unroll
-          for (int i = 0; i < 32; ++i) dp[i] = ((before >> i) & 1u) ? dp[i] : 0.f;
+        for (int i = 0; i < kCols / 2; ++i) {
+          const float2 v = f2_unpack(f2_mul(f2_pack(p[2 * i], p[2 * i + 1]), f2_add(f2_pack(dp[2 * i], dp[2 * i + 1]), d2)));
+          dp[2 * i] = v.x;
+          dp[2 * i + 1] = v.y;
         }
-        uint32_t pk[16];
+        if (diag) keep_bits(dp, before);  // a masked place is 0 whatever S and dP hold there
+        uint32_t pk[kCols / 2];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) pk[i] = Elem<T>::pack(dp[2 * i], dp[2 * i + 1]);
-        tmem_st8(t_s, pk);
-        tmem_st8(t_s + 8, pk + 8);
-        tmem_wait_st();
+        for (int i = 0; i < kCols / 2; ++i) pk[i] = Elem<T>::pack(dp[2 * i], dp[2 * i + 1]);
+        tmem_st_weights(t_s, pk);
         tc_fence_before();
         warp_arrive(bar_ds_full, lane);
+        rs.next();
+        ph ^= 1;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 21) {
+  if (warp == kBwdComputeWarps + 5) {
     tc_fence_after();
     tmem_dealloc<512>(tmem);
   }
