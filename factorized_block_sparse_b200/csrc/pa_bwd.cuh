@@ -50,16 +50,6 @@ constexpr int kBwdComputeWarps = 4 * 128 / kCols, kBwdThreads = 32 * (kBwdComput
 // packed pairs begin at the first of its kCols score columns.
 __device__ constexpr uint32_t weight_col(int kk) { return (kk / (kCols / 16)) * kCols + (kk % (kCols / 16)) * 8; }
 
-// Position in a ring of N stages: the stage and its phase's parity.
-template <int N>
-struct Ring {
-  int st = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void next() {
-    if (++st == N) st = 0, ph ^= 1;
-  }
-};
-
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float* v) {
 #pragma unroll
   for (int c = 0; c < kCols / 32; ++c) tmem_ld32(taddr + c * 32, v + c * 32);
@@ -271,17 +261,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     constexpr uint32_t id_s = make_idesc<T>(128, 128, false, false);
     constexpr uint32_t id_o = make_idesc<T>(128, D, false, true);
     bool ok = true;
-    int g = 0, ni = 0;
+    int ni = 0;
+    // next S^T and dP^T to issue; the step whose weights are awaited
+    Ring<C::QST> iq, rq;
+    Ring<C::OST> io, ro;
+    Ring<C::NS> is, rs;
+    Ring<C::KVB> rk;
+    uint32_t ph = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
       DkvItem it = dkv_item(a, walk.take(item, k), item);
       it.s = uniform(it.s);
       it.per = uniform(it.per);
       it.n = uniform(it.n);
-      const int kb = ni % C::KVB;
+      const int kb = rk.st;
       uint8_t* sK = smem + C::OFF_K + kb * G::BYTES;
       uint8_t* sV = smem + C::OFF_V + kb * G::BYTES;
       const Desc k_k = G::kmajor(smem_u32(sK)), v_k = G::kmajor(smem_u32(sV));
-      ok = mbar_wait_warp(bar_kv_full + kb, (ni / C::KVB) & 1, abort_flag);
+      ok = mbar_wait_warp(bar_kv_full + kb, rk.ph, abort_flag);
+      rk.next();
       if (!ok) break;
       const int keys = it.s.len - it.s.tile * kTile;
       if (keys < kTile) {
@@ -289,11 +286,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         zero_rows<D>(sV, keys, lane);
       }
       int rows_s = it.s.len - it.s.tile * kTile, left_s = it.per, rows_p = rows_s, left_p = it.per;  // of the next query tile
-      // S^T (dP^T) of the item's next step, global step gg; a last, partial query tile is zeroed behind its rows first
-      auto issue_s = [&](int gg) -> bool {
-        const int st = gg % C::QST, sb = gg % C::NS;
-        if (!mbar_wait_warp(bar_q_full + st, (gg / C::QST) & 1, abort_flag)) return false;
-        uint8_t* sQ = smem + C::OFF_Q + st * G::BYTES;
+      // S^T (dP^T) of the item's next step; a last, partial query tile is zeroed behind its rows first
+      auto issue_s = [&]() -> bool {
+        if (!mbar_wait_warp(bar_q_full + iq.st, iq.ph, abort_flag)) return false;
+        uint8_t* sQ = smem + C::OFF_Q + iq.st * G::BYTES;
         if (rows_s < kTile) zero_rows<D>(sQ, rows_s, lane);
         rows_s -= kTile;
         if (--left_s == 0) rows_s = keys, left_s = it.per;
@@ -302,16 +298,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16_ss(tmem + sb * 128, k_k.at(G::kstep(kk)), q_k.at(G::kstep(kk)), id_s, kk > 0);
-          mma_commit(bar_s_full + sb);
+            mma_bf16_ss(tmem + is.st * 128, k_k.at(G::kstep(kk)), q_k.at(G::kstep(kk)), id_s, kk > 0);
+          mma_commit(bar_s_full + is.st);
         }
         __syncwarp();
+        iq.next();
+        is.next();
         return true;
       };
-      auto issue_dp = [&](int gg) -> bool {
-        const int st = gg % C::OST;
-        if (!mbar_wait_warp(bar_do_full + st, (gg / C::OST) & 1, abort_flag)) return false;
-        uint8_t* sDO = smem + C::OFF_DO + st * G::BYTES;
+      auto issue_dp = [&]() -> bool {
+        if (!mbar_wait_warp(bar_do_full + io.st, io.ph, abort_flag)) return false;
+        uint8_t* sDO = smem + C::OFF_DO + io.st * G::BYTES;
         if (rows_p < kTile) zero_rows<D>(sDO, rows_p, lane);
         rows_p -= kTile;
         if (--left_p == 0) rows_p = keys, left_p = it.per;
@@ -324,42 +321,46 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           mma_commit(bar_dp_full);
         }
         __syncwarp();
+        io.next();
         return true;
       };
-      ok = issue_s(g) && issue_dp(g) && (C::NS == 1 || it.n == 1 || issue_s(g + 1));
-      for (int j = 0; ok && j < it.n; ++j, ++g) {
-        const int sq = g % C::QST, so = g % C::OST;
-        ok = mbar_wait_warp(bar_p_full, g & 1, abort_flag);
+      ok = issue_s() && issue_dp() && (C::NS == 1 || it.n == 1 || issue_s());
+      for (int j = 0; ok && j < it.n; ++j) {
+        ok = mbar_wait_warp(bar_p_full, ph, abort_flag);
         if (ok && j == 0 && ni > 0) ok = mbar_wait_warp(bar_out_free, (ni - 1) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        const Desc do_mn = G::mnmajor(smem_u32(smem + C::OFF_DO) + so * G::BYTES);
+        const Desc do_mn = G::mnmajor(smem_u32(smem + C::OFF_DO) + ro.st * G::BYTES);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)  // 16 queries = 8 TMEM columns of P^T, each group's from its first column on
-            mma_bf16_ts(tmem + C::COL_DV, tmem + (g % C::NS) * 128 + weight_col(kk), do_mn.at(G::mnstep(kk)),
+            mma_bf16_ts(tmem + C::COL_DV, tmem + rs.st * 128 + weight_col(kk), do_mn.at(G::mnstep(kk)),
                         id_o, j > 0 || kk > 0);
-          mma_commit(bar_do_free + so);
+          mma_commit(bar_do_free + ro.st);
         }
         __syncwarp();
-        if (!C::DS_IN_S && j + 1 < it.n && !(ok = issue_s(g + 1))) break;  // over P^T, behind its product
-        if (!(ok = mbar_wait_warp(bar_ds_full, g & 1, abort_flag))) break;
-        if (C::DS_IN_S && j + 1 < it.n && !(ok = issue_dp(g + 1))) break;
+        if (!C::DS_IN_S && j + 1 < it.n && !(ok = issue_s())) break;  // over P^T, behind its product
+        if (!(ok = mbar_wait_warp(bar_ds_full, ph, abort_flag))) break;
+        if (C::DS_IN_S && j + 1 < it.n && !(ok = issue_dp())) break;
         tc_fence_after();
-        const Desc q_mn = G::mnmajor(smem_u32(smem + C::OFF_Q) + sq * G::BYTES);
-        const uint32_t t_ds = tmem + (C::DS_IN_S ? (g % C::NS) * 128 + kCols / 2 : C::COL_DP);
+        const Desc q_mn = G::mnmajor(smem_u32(smem + C::OFF_Q) + rq.st * G::BYTES);
+        const uint32_t t_ds = tmem + (C::DS_IN_S ? rs.st * 128 + kCols / 2 : C::COL_DP);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
             mma_bf16_ts(tmem + C::COL_DK, t_ds + weight_col(kk), q_mn.at(G::mnstep(kk)), id_o,
                         j > 0 || kk > 0);
-          mma_commit(bar_q_free + sq);
+          mma_commit(bar_q_free + rq.st);
         }
         __syncwarp();
+        rq.next();
+        ro.next();
+        rs.next();
+        ph ^= 1;
         if (C::DS_IN_S) {
-          if (j + 2 < it.n) ok = issue_s(g + 2);  // over P^T and dS^T, behind their products
+          if (j + 2 < it.n) ok = issue_s();  // over P^T and dS^T, behind their products
         } else if (j + 1 < it.n) {
-          ok = issue_dp(g + 1);  // over dS^T, behind its product
+          ok = issue_dp();  // over dS^T, behind its product
         }
       }
       if (ok && elect_one()) {
@@ -595,17 +596,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     constexpr uint32_t id_s = make_idesc<T>(128, 128, false, false);
     constexpr uint32_t id_o = make_idesc<T>(128, D, false, true);
     bool ok = true;
-    int g = 0, ni = 0;
+    int ni = 0;
+    Ring<C::KST> ik, rk;  // next S to issue; the step whose weights are awaited
+    Ring<C::VST> iv;
+    Ring<2> is, rs;
+    Ring<C::QB> rq;
+    Ring<C::OB> rb;
+    uint32_t ph = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
       const Slot s = uniform(walk.take(item, k));
-      const int n = s.tile + 1, qb = ni % C::QB, ob = ni % C::OB;
-      ok = mbar_wait_warp(bar_q_full + qb, (ni / C::QB) & 1, abort_flag);
+      const int n = s.tile + 1, qb = rq.st, ob = rb.st;
+      ok = mbar_wait_warp(bar_q_full + qb, rq.ph, abort_flag);
       if (!ok) break;
       const Desc q_k = G::kmajor(smem_u32(smem + C::OFF_Q) + qb * G::BYTES);
       const Desc do_k = G::kmajor(smem_u32(smem + C::OFF_DO) + qb * G::BYTES);
-      auto issue_s = [&](int j, int gg) -> bool {
-        const int st = gg % C::KST;
-        if (!mbar_wait_warp(bar_k_full + st, (gg / C::KST) & 1, abort_flag)) return false;
+      auto issue_s = [&](int j) -> bool {
+        const int st = ik.st;
+        if (!mbar_wait_warp(bar_k_full + st, ik.ph, abort_flag)) return false;
         // keys behind the sequence's last: masked in S, but dS = 0 must not meet a NaN in dS K
         if (s.len - j * kTile < kTile) zero_rows<D>(smem + C::OFF_K + st * G::BYTES, s.len - j * kTile, lane);
         tc_fence_after();
@@ -613,15 +620,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16_ss(tmem + (gg & 1) * 128, q_k.at(G::kstep(kk)), k_k.at(G::kstep(kk)), id_s, kk > 0);
-          mma_commit(bar_s_full + (gg & 1));
+            mma_bf16_ss(tmem + is.st * 128, q_k.at(G::kstep(kk)), k_k.at(G::kstep(kk)), id_s, kk > 0);
+          mma_commit(bar_s_full + is.st);
         }
         __syncwarp();
+        ik.next();
+        is.next();
         return true;
       };
-      auto issue_dp = [&](int gg) -> bool {
-        const int st = gg % C::VST;
-        if (!mbar_wait_warp(bar_v_full + st, (gg / C::VST) & 1, abort_flag)) return false;
+      auto issue_dp = [&]() -> bool {
+        const int st = iv.st;
+        if (!mbar_wait_warp(bar_v_full + st, iv.ph, abort_flag)) return false;
         tc_fence_after();
         const Desc v_k = G::kmajor(smem_u32(smem + C::OFF_V) + st * G::BYTES);
         if (elect_one()) {
@@ -632,31 +641,36 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           mma_commit(bar_v_free + st);
         }
         __syncwarp();
+        iv.next();
         return true;
       };
-      ok = issue_s(0, g) && issue_dp(g) && (n == 1 || issue_s(1, g + 1));
-      for (int j = 0; ok && j < n; ++j, ++g) {
-        ok = mbar_wait_warp(bar_ds_full, g & 1, abort_flag);
-        if (ok && j == 0 && ni >= C::OB) ok = mbar_wait_warp(bar_out_free + ob, (ni / C::OB - 1) & 1, abort_flag);
+      ok = issue_s(0) && issue_dp() && (n == 1 || issue_s(1));
+      for (int j = 0; ok && j < n; ++j) {
+        ok = mbar_wait_warp(bar_ds_full, ph, abort_flag);
+        if (ok && j == 0 && ni >= C::OB) ok = mbar_wait_warp(bar_out_free + ob, rb.ph ^ 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        if (j + 1 < n && !(ok = issue_dp(g + 1))) break;
-        const int sk = g % C::KST;
-        const Desc k_mn = G::mnmajor(smem_u32(smem + C::OFF_K) + sk * G::BYTES);
+        if (j + 1 < n && !(ok = issue_dp())) break;
+        const Desc k_mn = G::mnmajor(smem_u32(smem + C::OFF_K) + rk.st * G::BYTES);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_bf16_ts(tmem + C::COL_DQ + ob * D, tmem + (g & 1) * 128 + weight_col(kk), k_mn.at(G::mnstep(kk)),
+            mma_bf16_ts(tmem + C::COL_DQ + ob * D, tmem + rs.st * 128 + weight_col(kk), k_mn.at(G::mnstep(kk)),
                         id_o, j > 0 || kk > 0);
-          mma_commit(bar_k_free + sk);
+          mma_commit(bar_k_free + rk.st);
         }
         __syncwarp();
-        if (j + 2 < n && !(ok = issue_s(j + 2, g + 2))) break;  // over dS, behind its product
+        rk.next();
+        rs.next();
+        ph ^= 1;
+        if (j + 2 < n && !(ok = issue_s(j + 2))) break;  // over dS, behind its product
       }
       if (ok && elect_one()) {
         mma_commit(bar_q_free + qb);
         mma_commit(bar_out_full + ob);
       }
+      rq.next();
+      rb.next();
     }
     if (elect_one()) {  // every MMA has completed before TMEM is released
       mma_commit(bar_drain);

@@ -243,6 +243,16 @@ __device__ __forceinline__ int zigzag(int k, int cta, int n_ctas) {
   return k * n_ctas + ((k & 1) ? (n_ctas - 1 - cta) : cta);
 }
 
+// Position in a ring of N stages: the stage and its phase's parity.
+template <int N>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == N) st = 0, ph ^= 1;
+  }
+};
+
 // The slots of a CTA's items in order, the next one requested into L1 while
 // this one is worked on: a slot comes from global memory, and every role would
 // wait for it at every item.  (Held in registers one item ahead it cost the
