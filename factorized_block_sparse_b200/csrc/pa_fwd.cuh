@@ -51,7 +51,7 @@ struct FwdArgs {
 template <int D>
 struct FwdCfg {
   using G = TileGeo<D>;
-  static constexpr int STAGES = D >= 128 ? 4 : 6;  // K and V tiles in turn
+  static constexpr int STAGES = D >= 128 ? 4 : 8;  // K and V tiles in turn
   static constexpr int NH = D <= 64 ? 2 : 1;       // threads a query row
   static constexpr int SOFT_WARPS = 8 * NH;
   static constexpr int STG_COLS = D >= 64 ? 32 : 16;  // staging: 32 rows of so many columns per warp
