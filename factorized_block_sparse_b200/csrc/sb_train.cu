@@ -87,11 +87,23 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* slots, int& turn)
 // visits rows a multiple of 8 apart, so its shift, and with it the channels of
 // its words, are the same in every row whatever the stride (8 rows of 2-byte
 // elements are a multiple of 16 bytes): gains and sums stay in registers.
-// Words come through a ring in shared memory of the thread's own (cp.async, kDepth rows
-// in flight, no barrier); a word is read whole where it lies inside the
+// Words come through a ring in shared memory of the thread's own (cp.async, kDepth
+// groups of rows, no barrier); a word is read whole where it lies inside the
 // tensor's first and last byte, and written element by element where it
 // holds another row's elements.
-constexpr int kDepth = 4;
+constexpr int kDepth = 3;
+
+// Rows a thread takes at a time: their sums share a barrier, their words the
+// gains in registers.
+__host__ __device__ constexpr int rows_at_once(int nv) { return nv >= 4 ? 1 : 2; }
+
+// 1 / sqrt(v) to float32's last bit or so: the hardware's approximation and
+// one step of Newton's method (0 and infinity pass through).
+__device__ __forceinline__ float rsqrt_newton(float v) {
+  const float r = rsqrtf(v);
+  const float e = fmaf(-v * r, r, 1.f);
+  return fabsf(e) < 1.f ? fmaf(0.5f * r, e, r) : r;
+}
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
@@ -108,25 +120,14 @@ __device__ __forceinline__ void cp_wait() {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-template <typename T>
-struct Rows {
-  const char* base;  // the tensor's first element
-  const char* end;   // behind its last
-  long long ld;      // bytes from a row to the next
-  __device__ __forceinline__ Rows(const T* p, long long ldx, long long M, int C)
-      : base(reinterpret_cast<const char*>(p)),
-        end(reinterpret_cast<const char*>(p + (M - 1) * ldx + C)),
-        ld(ldx * static_cast<long long>(sizeof(T))) {}
-};
-
-// The thread's words of a row: w = i0 + j n for j < NV.  EDGE: words may hold
+// The words of a thread: w = i0 + j n of a row, j < NV.  EDGE: words may hold
 // other rows' elements (else rows begin and end on 16 bytes).
 template <typename T, int NV, bool EDGE>
 struct Words {
   static constexpr int N = 16 / sizeof(T);
   int i0, n, words, shift, C;
-  __device__ __forceinline__ Words(const Rows<T>& x, long long r0, int C_, int i0_, int n_) : i0(i0_), n(n_), C(C_) {
-    shift = !EDGE ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(x.base) + static_cast<uintptr_t>(r0 * x.ld)) & 15) / static_cast<int>(sizeof(T));
+  __device__ __forceinline__ Words(const T* row, int C_, int i0_, int n_) : i0(i0_), n(n_), C(C_) {
+    shift = EDGE ? static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15) / static_cast<int>(sizeof(T)) : 0;
     words = (shift + C + N - 1) / N;
   }
   __device__ __forceinline__ bool has(int j) const { return i0 + j * n < words; }
@@ -135,66 +136,106 @@ struct Words {
     return EDGE ? static_cast<unsigned>(channel(j, u)) < static_cast<unsigned>(C) : has(j);
   }
   __device__ __forceinline__ bool whole(int j) const { return !EDGE || (channel(j, 0) >= 0 && channel(j, N - 1) < C); }
-  __device__ __forceinline__ const char* at(const Rows<T>& x, long long r, int j) const {
-    return x.base + r * x.ld + static_cast<long long>(channel(j, 0)) * static_cast<long long>(sizeof(T));
-  }
-  // row r's words on their way into the ring slot (NV words, blockDim.x threads)
-  __device__ __forceinline__ void request(uint4* slot, const Rows<T>& x, long long r) const {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (!has(j)) continue;
-      const char* p = at(x, r, j);
-      uint4* d = slot + j * blockDim.x + threadIdx.x;
-      if (!EDGE || (p >= x.base && p + 16 <= x.end)) {
-        cp_async16(d, p);
-      } else {  // at the tensor's very ends
-        T* e = reinterpret_cast<T*>(d);
-        for (int u = 0; u < N; ++u)
-          if (in(j, u)) e[u] = reinterpret_cast<const T*>(p)[u];
-      }
-    }
-  }
   // values of word j, zero outside the row
   __device__ __forceinline__ void values(const uint4* slot, int j, float* f) const {
-    const uint4 w = slot[j * blockDim.x + threadIdx.x];
+    const uint4 w = slot[j * blockDim.x];
     unpack<T, N>(w, f);
     if (!whole(j))
 #pragma unroll
       for (int u = 0; u < N; ++u) f[u] = in(j, u) ? f[u] : 0.f;
   }
-  __device__ __forceinline__ void store(T* y, long long ldy, long long r, int j, const float* f) const {
-    T* p = y + r * ldy + channel(j, 0);
-    if (whole(j)) {
-      *reinterpret_cast<uint4*>(p) = pack<T, N>(f);
-    } else {
+};
+
+// A tensor's rows as a thread visits them: its first word of the next row, and the tensor's bytes.
+template <typename T, int NV, bool EDGE>
+struct Feed {
+  const char *p, *base, *end;
+  long long step;
+  __device__ __forceinline__ Feed(const T* t, long long ld, long long M, long long row, long long rows,
+                                  const Words<T, NV, EDGE>& w)
+      : p(reinterpret_cast<const char*>(t + row * ld + w.channel(0, 0))),
+        base(reinterpret_cast<const char*>(t)),
+        end(reinterpret_cast<const char*>(t + (M - 1) * ld + w.C)),
+        step(rows * ld * static_cast<long long>(sizeof(T))) {}
+  // the next row's words on their way into the thread's words of a ring slot
+  __device__ __forceinline__ void request(uint4* slot, const Words<T, NV, EDGE>& w) {
 #pragma unroll
-      for (int u = 0; u < N; ++u)
-        if (in(j, u)) p[u] = static_cast<T>(f[u]);
+    for (int j = 0; j < NV; ++j) {
+      if (!w.has(j)) continue;
+      const char* q = p + j * w.n * 16;
+      uint4* d = slot + j * blockDim.x;
+      if (!EDGE || (q >= base && q + 16 <= end)) {
+        cp_async16(d, q);
+      } else {  // at the tensor's very ends
+        T* e = reinterpret_cast<T*>(d);
+        for (int u = 0; u < Words<T, NV, EDGE>::N; ++u)
+          if (w.in(j, u)) e[u] = reinterpret_cast<const T*>(q)[u];
+      }
     }
+    p += step;
   }
 };
 
+template <typename T, int NV, bool EDGE>
+__device__ __forceinline__ void store_word(char* row, const Words<T, NV, EDGE>& w, int j, const float* f) {
+  constexpr int N = 16 / sizeof(T);
+  T* p = reinterpret_cast<T*>(row + j * w.n * 16);
+  if (w.whole(j)) {
+    *reinterpret_cast<uint4*>(p) = pack<T, N>(f);
+  } else {
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      if (w.in(j, u)) p[u] = static_cast<T>(f[u]);
+  }
+}
+
+// Rows of a thread: the first, the distance, how many, and how many its warp (block) goes round.
+template <int TPR>
+struct Share {
+  static constexpr int kPer = TPR ? TPR : 1;
+  long long first, step;
+  int mine, all, i0, n;
+  __device__ __forceinline__ explicit Share(long long M) {
+    first = TPR ? (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / kPer : blockIdx.x;
+    step = TPR ? static_cast<long long>(gridDim.x) * blockDim.x / kPer : gridDim.x;
+    const long long warp0 = TPR ? first - (threadIdx.x & 31) / kPer : first;
+    mine = first < M ? static_cast<int>((M - first - 1) / step) + 1 : 0;
+    all = warp0 < M ? static_cast<int>((M - warp0 - 1) / step) + 1 : 0;
+    i0 = TPR ? threadIdx.x % kPer : threadIdx.x;
+    n = TPR ? kPer : blockDim.x;
+  }
+};
+
+// Blocks an SM that a kernel's registers are to allow: gains, biases and the row (column sums) of NV words.
+__host__ __device__ constexpr int min_blocks(int nv, int maxt, bool bwd) {
+  return maxt <= 256 ? (nv == 1 ? (bwd ? 3 : 4) : 2) : (maxt <= 384 ? 2 : 1);
+}
+
 // y = (x - mean) rstd g + b, and the row's mean and rstd.  TPR threads a row (0: the block, of at most MAXT).
 template <typename T, int NV, int TPR, bool EDGE, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= 384 ? 2 : 1)
+__global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, false))
     norm_fwd_kernel(const T* x, long long ldx, const float* __restrict__ g, const float* __restrict__ b, T* y,
                     long long ldy, float* mean_out, float* rstd_out, long long M, int C, float eps) {
   constexpr int N = 16 / sizeof(T);
-  extern __shared__ uint4 ring[];  // [kDepth][NV][threads]
-  __shared__ __align__(16) float slots[64];
+  extern __shared__ uint4 ring_[];  // [kDepth][rows at once][NV][threads]
+  __shared__ __align__(16) float slots[128];
   int turn = 0;
-  constexpr int kPer = TPR ? TPR : 1;
-  const long long gid = TPR ? (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / kPer : blockIdx.x;
-  const long long step = TPR ? static_cast<long long>(gridDim.x) * blockDim.x / kPer : gridDim.x;
-  const long long warp0 = TPR ? gid - (threadIdx.x & 31) / kPer : gid;  // the warp's first row
-  const Rows<T> xr(x, ldx, M, C);
-  const Words<T, NV, EDGE> ws(xr, gid, C, TPR ? threadIdx.x % kPer : threadIdx.x, TPR ? kPer : blockDim.x);
-  const int slot_words = NV * blockDim.x;
+  const Share<TPR> sh(M);
+  const Words<T, NV, EDGE> ws(x + sh.first * ldx, C, sh.i0, sh.n);
+  Feed<T, NV, EDGE> xs(x, ldx, M, sh.first, sh.step, ws);
+  uint4* ring = ring_ + threadIdx.x;
+  constexpr int R = rows_at_once(NV);
+  const int row_words = NV * blockDim.x, slot_words = R * row_words;
+  int asked = 0;
+  auto request = [&](uint4* slot) {
 #pragma unroll
-  for (int d = 0; d < kDepth - 1; ++d) {
-    if (gid + d * step < M) ws.request(ring + d * slot_words, xr, gid + d * step);
+    for (int k = 0; k < R; ++k)
+      if (asked + k < sh.mine) xs.request(slot + k * row_words, ws);
+    asked += R;
     cp_commit();
-  }
+  };
+#pragma unroll
+  for (int d = 0; d < kDepth - 1; ++d) request(ring + d * slot_words);
   float gv[NV * N], bv[NV * N];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -205,51 +246,59 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 384 ? 2 : 1)
       bv[j * N + u] = (b && in) ? b[ws.channel(j, u)] : 0.f;
     }
   const float inv = 1.f / C;
+  char* out = reinterpret_cast<char*>(y + sh.first * ldy + ws.channel(0, 0));
+  const long long out_step = sh.step * ldy * static_cast<long long>(sizeof(T));
   int at = 0;
-  for (long long r = gid, w0 = warp0; w0 < M; r += step, w0 += step) {
-    const bool live = r < M;
-    {
-      const long long ahead = r + (kDepth - 1) * step;
-      const int s = at == 0 ? kDepth - 1 : at - 1;
-      if (ahead < M) ws.request(ring + s * slot_words, xr, ahead);
-      cp_commit();
-    }
+  for (int i = 0; i < sh.all; i += R) {
+    request(ring + (at == 0 ? kDepth - 1 : at - 1) * slot_words);
     cp_wait<kDepth - 1>();
-    float f[NV * N], s[1] = {0.f};
+    float f[R][NV * N], s[R], q[R];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (live && ws.has(j)) ws.values(ring + at * slot_words, j, f + j * N);
-      else
+    for (int k = 0; k < R; ++k) {
+      s[k] = 0.f;
 #pragma unroll
-        for (int u = 0; u < N; ++u) f[j * N + u] = 0.f;
+      for (int j = 0; j < NV; ++j) {
+        if (i + k < sh.mine && ws.has(j)) ws.values(ring + at * slot_words + k * row_words, j, f[k] + j * N);
+        else
 #pragma unroll
-      for (int u = 0; u < N; ++u) s[0] += f[j * N + u];
+          for (int u = 0; u < N; ++u) f[k][j * N + u] = 0.f;
+#pragma unroll
+        for (int u = 0; u < N; ++u) s[k] += f[k][j * N + u];
+      }
     }
     row_sums<TPR>(s, slots, turn);
-    const float mean = s[0] * inv;
-    float q[1] = {0.f};
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int u = 0; u < N; ++u) {
-        f[j * N + u] -= mean;
-        if (ws.in(j, u)) q[0] += f[j * N + u] * f[j * N + u];
-      }
-    row_sums<TPR>(q, slots, turn);
-    const float rstd = 1.f / sqrtf(q[0] * inv + eps);
-    if (live) {
-      if (ws.i0 == 0) {
-        if (mean_out) mean_out[r] = mean;
-        if (rstd_out) rstd_out[r] = rstd;
-      }
+    for (int k = 0; k < R; ++k) {
+      s[k] *= inv;  // the mean
+      q[k] = 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (ws.has(j)) {
-          float o[N];
 #pragma unroll
-          for (int u = 0; u < N; ++u) o[u] = f[j * N + u] * rstd * gv[j * N + u] + bv[j * N + u];
-          ws.store(y, ldy, r, j, o);
+        for (int u = 0; u < N; ++u) {
+          f[k][j * N + u] -= s[k];
+          if (ws.in(j, u)) q[k] += f[k][j * N + u] * f[k][j * N + u];
         }
+    }
+    row_sums<TPR>(q, slots, turn);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const float rstd = rsqrt_newton(q[k] * inv + eps);
+      if (i + k < sh.mine) {
+        if (sh.i0 == 0) {
+          const long long r = sh.first + (i + k) * sh.step;
+          if (mean_out) mean_out[r] = s[k];
+          if (rstd_out) rstd_out[r] = rstd;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (ws.has(j)) {
+            float o[N];
+#pragma unroll
+            for (int u = 0; u < N; ++u) o[u] = f[k][j * N + u] * rstd * gv[j * N + u] + bv[j * N + u];
+            store_word(out, ws, j, o);
+          }
+      }
+      out += out_step;
     }
     at = at + 1 == kDepth ? 0 : at + 1;
   }
@@ -272,7 +321,7 @@ __global__ void __launch_bounds__(512)
     const float mean = s[0] * inv;
     for (int i = threadIdx.x; i < C; i += blockDim.x) q[0] += (to_f(p[i]) - mean) * (to_f(p[i]) - mean);
     row_sums<0>(q, slots, turn);
-    const float rstd = 1.f / sqrtf(q[0] * inv + eps);
+    const float rstd = rsqrt_newton(q[0] * inv + eps);
     if (threadIdx.x == 0) {
       if (mean_out) mean_out[r] = mean;
       if (rstd_out) rstd_out[r] = rstd;
@@ -283,110 +332,121 @@ __global__ void __launch_bounds__(512)
 }
 
 // Rows in flight of the backward kernel (x and dy; four words a thread fill shared memory with two).
-__host__ __device__ constexpr int bwd_depth(int nv) { return nv >= 4 ? 2 : kDepth; }
+__host__ __device__ constexpr int bwd_depth(int nv) { return nv >= 4 ? 2 : 4; }
 
 // dx per row, and this block's sums of dy xh and dy per channel into
 // part[blockIdx.x][2][C].
 // x and dy are read from the ring twice, before and after the row's two sums,
 // so that only the gains and the column sums stay in registers.
 template <typename T, int NV, int TPR, bool EDGE, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= 384 ? 2 : 1)
+__global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, true))
     norm_bwd_kernel(const T* x, long long ldx, const float* __restrict__ g, const T* dy, long long lddy,
                     const float* __restrict__ mean_in, const float* __restrict__ rstd_in, T* dx, long long lddx,
                     float* part, long long M, int C) {
   constexpr int N = 16 / sizeof(T);
   constexpr int kRing = bwd_depth(NV);
-  extern __shared__ uint4 ring[];  // [kRing][x, dy][NV][threads]; then the row groups' sums [groups][2][C]
-  __shared__ __align__(16) float slots[128];
+  extern __shared__ uint4 ring_[];  // [kRing][rows at once][x, dy][NV][threads]; then the row groups' sums [groups][2][C]
+  __shared__ __align__(16) float slots[256];
   pdl_trigger();
   int turn = 0;
-  constexpr int kPer = TPR ? TPR : 1;
-  const long long gid = TPR ? (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / kPer : blockIdx.x;
-  const long long step = TPR ? static_cast<long long>(gridDim.x) * blockDim.x / kPer : gridDim.x;
-  const long long warp0 = TPR ? gid - (threadIdx.x & 31) / kPer : gid;
-  const Rows<T> xr(x, ldx, M, C), dr(dy, lddy, M, C);
-  const Words<T, NV, EDGE> ws(xr, gid, C, TPR ? threadIdx.x % kPer : threadIdx.x, TPR ? kPer : blockDim.x);
-  const int slot_words = NV * blockDim.x;
-  float m_next[kRing - 1], r_next[kRing - 1];  // statistics of the rows in flight
+  const Share<TPR> sh(M);
+  const Words<T, NV, EDGE> ws(x + sh.first * ldx, C, sh.i0, sh.n);
+  Feed<T, NV, EDGE> xs(x, ldx, M, sh.first, sh.step, ws), ds(dy, lddy, M, sh.first, sh.step, ws);
+  uint4* ring = ring_ + threadIdx.x;
+  constexpr int R = 1;  // (two at a time: the ring leaves room for one block an SM, 16384 x 6144 bf16 192 us for 158)
+  const int row_words = NV * blockDim.x, slot_words = 2 * R * row_words;
+  float m_next[kRing - 1][R], r_next[kRing - 1][R];  // statistics of the rows in flight
+  const float *pm = mean_in + sh.first, *pr = rstd_in + sh.first;
+  int asked = 0;
+  auto request = [&](uint4* slot, float (&m)[R], float (&rs)[R]) {
 #pragma unroll
-  for (int d = 0; d < kRing - 1; ++d) {
-    const long long r = gid + d * step;
-    m_next[d] = r_next[d] = 0.f;
-    if (r < M) {
-      ws.request(ring + 2 * d * slot_words, xr, r);
-      ws.request(ring + (2 * d + 1) * slot_words, dr, r);
-      m_next[d] = mean_in[r];
-      r_next[d] = rstd_in[r];
+    for (int k = 0; k < R; ++k) {
+      m[k] = rs[k] = 0.f;
+      if (asked + k < sh.mine) {
+        xs.request(slot + 2 * k * row_words, ws);
+        ds.request(slot + (2 * k + 1) * row_words, ws);
+        m[k] = *pm;
+        rs[k] = *pr;
+        pm += sh.step;
+        pr += sh.step;
+      }
     }
+    asked += R;
     cp_commit();
-  }
+  };
+#pragma unroll
+  for (int d = 0; d < kRing - 1; ++d) request(ring + d * slot_words, m_next[d], r_next[d]);
   float gv[NV * N], sg[NV * N] = {}, sb[NV * N] = {};
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int u = 0; u < N; ++u) gv[j * N + u] = ws.in(j, u) ? g[ws.channel(j, u)] : 0.f;
   const float inv = 1.f / C;
+  char* out = reinterpret_cast<char*>(dx + sh.first * lddx + ws.channel(0, 0));
+  const long long out_step = sh.step * lddx * static_cast<long long>(sizeof(T));
   int at = 0;
-  for (long long r = gid, w0 = warp0; w0 < M; r += step, w0 += step) {
-    const bool live = r < M;
-    const float mc = m_next[0], rc = r_next[0];
+  for (int i = 0; i < sh.all; i += R) {
+    float mc[R], rc[R];
 #pragma unroll
-    for (int d = 0; d + 1 < kRing - 1; ++d) {
-      m_next[d] = m_next[d + 1];
-      r_next[d] = r_next[d + 1];
-    }
-    {
-      const long long ahead = r + (kRing - 1) * step;
-      const int s = at == 0 ? kRing - 1 : at - 1;
-      if (ahead < M) {
-        ws.request(ring + 2 * s * slot_words, xr, ahead);
-        ws.request(ring + (2 * s + 1) * slot_words, dr, ahead);
-        m_next[kRing - 2] = mean_in[ahead];
-        r_next[kRing - 2] = rstd_in[ahead];
+    for (int k = 0; k < R; ++k) {
+      mc[k] = m_next[0][k];
+      rc[k] = r_next[0][k];
+#pragma unroll
+      for (int d = 0; d + 1 < kRing - 1; ++d) {
+        m_next[d][k] = m_next[d + 1][k];
+        r_next[d][k] = r_next[d + 1][k];
       }
-      cp_commit();
     }
+    request(ring + (at == 0 ? kRing - 1 : at - 1) * slot_words, m_next[kRing - 2], r_next[kRing - 2]);
     cp_wait<kRing - 1>();
-    const uint4* xs = ring + 2 * at * slot_words;
-    const uint4* ds = xs + slot_words;
-    float s[2] = {0.f, 0.f};
+    const uint4* xw = ring + at * slot_words;
+    float s[2 * R];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (live && ws.has(j)) {
-        float xh[N], d[N];
-        ws.values(xs, j, xh);
-        ws.values(ds, j, d);
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-          const int k = j * N + u;
-          xh[u] = (xh[u] - mc) * rc;  // (not x rc - m rc, which cancels where the mean is large)
-          sg[k] = fmaf(d[u], xh[u], sg[k]);
-          sb[k] += d[u];
-          const float t = d[u] * gv[k];
-          s[0] += t;
-          s[1] = fmaf(t, xh[u], s[1]);
-        }
-      }
-    row_sums<TPR>(s, slots, turn);
-    // dx = rc t - rc mean(t) - xh rc mean(t xh)
-    const float c0 = -rc * (s[0] * inv), c1 = -rc * (s[1] * inv);
-    if (live)
+    for (int k = 0; k < R; ++k) {
+      s[2 * k] = s[2 * k + 1] = 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (ws.has(j)) {
+        if (i + k < sh.mine && ws.has(j)) {
           float xh[N], d[N];
-          ws.values(xs, j, xh);
-          ws.values(ds, j, d);
+          ws.values(xw + 2 * k * row_words, j, xh);
+          ws.values(xw + (2 * k + 1) * row_words, j, d);
 #pragma unroll
-          for (int u = 0; u < N; ++u)
-            d[u] = fmaf(rc, d[u] * gv[j * N + u], fmaf((xh[u] - mc) * rc, c1, c0));
-          ws.store(dx, lddx, r, j, d);
+          for (int u = 0; u < N; ++u) {
+            const int c = j * N + u;
+            xh[u] = (xh[u] - mc[k]) * rc[k];  // (not x rc - m rc, which cancels where the mean is large)
+            sg[c] = fmaf(d[u], xh[u], sg[c]);
+            sb[c] += d[u];
+            const float t = d[u] * gv[c];
+            s[2 * k] += t;
+            s[2 * k + 1] = fmaf(t, xh[u], s[2 * k + 1]);
+          }
         }
+    }
+    row_sums<TPR>(s, slots, turn);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      // dx = rc t - rc mean(t) - xh rc mean(t xh)
+      const float c0 = -rc[k] * (s[2 * k] * inv), c1 = -rc[k] * (s[2 * k + 1] * inv);
+      if (i + k < sh.mine)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (ws.has(j)) {
+            float xh[N], d[N];
+            ws.values(xw + 2 * k * row_words, j, xh);
+            ws.values(xw + (2 * k + 1) * row_words, j, d);
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+              d[u] = fmaf(rc[k], d[u] * gv[j * N + u], fmaf((xh[u] - mc[k]) * rc[k], c1, c0));
+            store_word(out, ws, j, d);
+          }
+      out += out_step;
+    }
     at = at + 1 == kRing ? 0 : at + 1;
   }
-  float* out = part + static_cast<long long>(blockIdx.x) * 2 * C;
+  float* dst = part + static_cast<long long>(blockIdx.x) * 2 * C;
   if constexpr (TPR != 0) {
-    float* sums = reinterpret_cast<float*>(ring);
+    constexpr int kPer = TPR ? TPR : 1;
+    float* sums = reinterpret_cast<float*>(ring_);
     float* mine = sums + threadIdx.x / kPer * 2 * C;
     cp_wait<0>();
     __syncthreads();
@@ -403,7 +463,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 384 ? 2 : 1)
       float a = 0.f;
 #pragma unroll 8
       for (int w = 0; w < 256 / kPer; ++w) a += sums[w * 2 * C + i];
-      out[i] = a;
+      dst[i] = a;
     }
   } else {
 #pragma unroll
@@ -411,8 +471,8 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 384 ? 2 : 1)
 #pragma unroll
       for (int u = 0; u < N; ++u)
         if (ws.in(j, u)) {
-          out[ws.channel(j, u)] = sg[j * N + u];
-          out[C + ws.channel(j, u)] = sb[j * N + u];
+          dst[ws.channel(j, u)] = sg[j * N + u];
+          dst[C + ws.channel(j, u)] = sb[j * N + u];
         }
   }
 }
@@ -709,7 +769,7 @@ int by_width(int words, F&& go, E edge) {
   if (words <= 16) return go(I1{}, integral_constant<int, 16>{}, edge, T256{});
   if (words <= 32) return go(I1{}, Warp{}, edge, T256{});
   if (words <= 64) return go(I2{}, Warp{}, edge, T256{});
-  if (words <= 384) return go(I1{}, Block{}, edge, T384{});
+  if (words <= 256) return go(I1{}, Block{}, edge, T256{});
   if (words <= 768) return go(I2{}, Block{}, edge, T384{});
   if (words <= 1024) return go(I2{}, Block{}, edge, T512{});
   if (words <= 2048) return go(integral_constant<int, 4>{}, Block{}, edge, T512{});
@@ -758,7 +818,7 @@ int sparse_block_layer_norm_fwd(const void* x, int64_t ldx, const float* g, cons
       constexpr auto K = norm_fwd_kernel<T, NV, TPR, edge.value, maxt.value>;
       const int threads = TPR ? 256 : (words + 32 * NV - 1) / (32 * NV) * 32;
       const int rows = TPR ? 256 / (TPR ? TPR : 1) : 1;  // rows of a block at a time
-      const size_t smem = static_cast<size_t>(kDepth) * NV * threads * 16;
+      const size_t smem = static_cast<size_t>(kDepth) * rows_at_once(NV) * NV * threads * 16;
       const int per = resident<K>(dev, threads, smem);
       if (per == 0) return SA_ERR_CUDA;
       long long grid = std::min<long long>((M + rows - 1) / rows, static_cast<long long>(n_sm) * per);
