@@ -25,6 +25,37 @@ __device__ __forceinline__ float to_f(T v) {
   return static_cast<float>(v);
 }
 
+// Pairs of float32 in a 64-bit register: one instruction for two elements.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f2_get(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+  const float2 t = f2_get(v);
+  return t.x + t.y;
+}
+
 // The N elements of a 16-byte word.
 template <typename T, int N>
 __device__ __forceinline__ void unpack(const uint4& w, float* f) {
@@ -136,13 +167,16 @@ struct Words {
     return EDGE ? static_cast<unsigned>(channel(j, u)) < static_cast<unsigned>(C) : has(j);
   }
   __device__ __forceinline__ bool whole(int j) const { return !EDGE || (channel(j, 0) >= 0 && channel(j, N - 1) < C); }
-  // values of word j, zero outside the row
-  __device__ __forceinline__ void values(const uint4* slot, int j, float* f) const {
+  // values of word j in pairs, zero outside the row
+  __device__ __forceinline__ void values(const uint4* slot, int j, uint64_t* v) const {
     const uint4 w = slot[j * blockDim.x];
+    float f[N];
     unpack<T, N>(w, f);
     if (!whole(j))
 #pragma unroll
       for (int u = 0; u < N; ++u) f[u] = in(j, u) ? f[u] : 0.f;
+#pragma unroll
+    for (int u = 0; u < N / 2; ++u) v[u] = f2(f[2 * u], f[2 * u + 1]);
   }
 };
 
@@ -177,8 +211,15 @@ struct Feed {
 };
 
 template <typename T, int NV, bool EDGE>
-__device__ __forceinline__ void store_word(char* row, const Words<T, NV, EDGE>& w, int j, const float* f) {
+__device__ __forceinline__ void store_word(char* row, const Words<T, NV, EDGE>& w, int j, const uint64_t* v) {
   constexpr int N = 16 / sizeof(T);
+  float f[N];
+#pragma unroll
+  for (int u = 0; u < N / 2; ++u) {
+    const float2 t = f2_get(v[u]);
+    f[2 * u] = t.x;
+    f[2 * u + 1] = t.y;
+  }
   T* p = reinterpret_cast<T*>(row + j * w.n * 16);
   if (w.whole(j)) {
     *reinterpret_cast<uint4*>(p) = pack<T, N>(f);
@@ -236,14 +277,15 @@ __global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, false))
   };
 #pragma unroll
   for (int d = 0; d < kDepth - 1; ++d) request(ring + d * slot_words);
-  float gv[NV * N], bv[NV * N];
+  constexpr int H = N / 2;  // pairs of a word
+  uint64_t gv[NV * H], bv[NV * H];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-      const bool in = ws.in(j, u);
-      gv[j * N + u] = in ? g[ws.channel(j, u)] : 0.f;
-      bv[j * N + u] = (b && in) ? b[ws.channel(j, u)] : 0.f;
+    for (int u = 0; u < H; ++u) {
+      auto at_channel = [&](const float* p, int e) { return p && ws.in(j, e) ? p[ws.channel(j, e)] : 0.f; };
+      gv[j * H + u] = f2(at_channel(g, 2 * u), at_channel(g, 2 * u + 1));
+      bv[j * H + u] = f2(at_channel(b, 2 * u), at_channel(b, 2 * u + 1));
     }
   const float inv = 1.f / C;
   char* out = reinterpret_cast<char*>(y + sh.first * ldy + ws.channel(0, 0));
@@ -252,37 +294,47 @@ __global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, false))
   for (int i = 0; i < sh.all; i += R) {
     request(ring + (at == 0 ? kDepth - 1 : at - 1) * slot_words);
     cp_wait<kDepth - 1>();
-    float f[R][NV * N], s[R], q[R];
+    uint64_t f[R][NV * H];
+    float s[R], q[R];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      s[k] = 0.f;
+      uint64_t sum = 0;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (i + k < sh.mine && ws.has(j)) ws.values(ring + at * slot_words + k * row_words, j, f[k] + j * N);
+        if (i + k < sh.mine && ws.has(j)) ws.values(ring + at * slot_words + k * row_words, j, f[k] + j * H);
         else
 #pragma unroll
-          for (int u = 0; u < N; ++u) f[k][j * N + u] = 0.f;
+          for (int u = 0; u < H; ++u) f[k][j * H + u] = 0;
 #pragma unroll
-        for (int u = 0; u < N; ++u) s[k] += f[k][j * N + u];
+        for (int u = 0; u < H; ++u) sum = f2_add(sum, f[k][j * H + u]);
       }
+      s[k] = f2_sum(sum);
     }
     row_sums<TPR>(s, slots, turn);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       s[k] *= inv;  // the mean
-      q[k] = 0.f;
+      const uint64_t neg = f2(-s[k], -s[k]);
+      uint64_t sum = 0;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-          f[k][j * N + u] -= s[k];
-          if (ws.in(j, u)) q[k] += f[k][j * N + u] * f[k][j * N + u];
+        for (int u = 0; u < H; ++u) {
+          uint64_t& v = f[k][j * H + u];
+          v = f2_add(v, neg);
+          if (EDGE || !ws.has(j)) {  // outside the row there is no deviation
+            const float2 t = f2_get(v);
+            v = f2(ws.in(j, 2 * u) ? t.x : 0.f, ws.in(j, 2 * u + 1) ? t.y : 0.f);
+          }
+          sum = f2_fma(v, v, sum);
         }
+      q[k] = f2_sum(sum);
     }
     row_sums<TPR>(q, slots, turn);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       const float rstd = rsqrt_newton(q[k] * inv + eps);
+      const uint64_t r2 = f2(rstd, rstd);
       if (i + k < sh.mine) {
         if (sh.i0 == 0) {
           const long long r = sh.first + (i + k) * sh.step;
@@ -292,9 +344,9 @@ __global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, false))
 #pragma unroll
         for (int j = 0; j < NV; ++j)
           if (ws.has(j)) {
-            float o[N];
+            uint64_t o[H];
 #pragma unroll
-            for (int u = 0; u < N; ++u) o[u] = f[k][j * N + u] * rstd * gv[j * N + u] + bv[j * N + u];
+            for (int u = 0; u < H; ++u) o[u] = f2_fma(f2_mul(f[k][j * H + u], r2), gv[j * H + u], bv[j * H + u]);
             store_word(out, ws, j, o);
           }
       }
@@ -376,11 +428,15 @@ __global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, true))
   };
 #pragma unroll
   for (int d = 0; d < kRing - 1; ++d) request(ring + d * slot_words, m_next[d], r_next[d]);
-  float gv[NV * N], sg[NV * N] = {}, sb[NV * N] = {};
+  constexpr int H = N / 2;  // pairs of a word
+  uint64_t gv[NV * H], sg[NV * H] = {}, sb[NV * H] = {};
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int u = 0; u < N; ++u) gv[j * N + u] = ws.in(j, u) ? g[ws.channel(j, u)] : 0.f;
+    for (int u = 0; u < H; ++u) {
+      auto gain = [&](int e) { return ws.in(j, e) ? g[ws.channel(j, e)] : 0.f; };
+      gv[j * H + u] = f2(gain(2 * u), gain(2 * u + 1));
+    }
   const float inv = 1.f / C;
   char* out = reinterpret_cast<char*>(dx + sh.first * lddx + ws.channel(0, 0));
   const long long out_step = sh.step * lddx * static_cast<long long>(sizeof(T));
@@ -403,61 +459,69 @@ __global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, true))
     float s[2 * R];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      s[2 * k] = s[2 * k + 1] = 0.f;
+      const uint64_t neg = f2(-mc[k], -mc[k]), r2 = f2(rc[k], rc[k]);
+      uint64_t s0 = 0, s1 = 0;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (i + k < sh.mine && ws.has(j)) {
-          float xh[N], d[N];
-          ws.values(xw + 2 * k * row_words, j, xh);
-          ws.values(xw + (2 * k + 1) * row_words, j, d);
+          uint64_t x2[H], d2[H];
+          ws.values(xw + 2 * k * row_words, j, x2);
+          ws.values(xw + (2 * k + 1) * row_words, j, d2);
 #pragma unroll
-          for (int u = 0; u < N; ++u) {
-            const int c = j * N + u;
-            xh[u] = (xh[u] - mc[k]) * rc[k];  // (not x rc - m rc, which cancels where the mean is large)
-            sg[c] = fmaf(d[u], xh[u], sg[c]);
-            sb[c] += d[u];
-            const float t = d[u] * gv[c];
-            s[2 * k] += t;
-            s[2 * k + 1] = fmaf(t, xh[u], s[2 * k + 1]);
+          for (int u = 0; u < H; ++u) {
+            const int c = j * H + u;
+            const uint64_t xh = f2_mul(f2_add(x2[u], neg), r2);  // (not x r - m r, which cancels where the mean is large)
+            sg[c] = f2_fma(d2[u], xh, sg[c]);
+            sb[c] = f2_add(sb[c], d2[u]);
+            const uint64_t t = f2_mul(d2[u], gv[c]);
+            s0 = f2_add(s0, t);
+            s1 = f2_fma(t, xh, s1);
           }
         }
+      s[2 * k] = f2_sum(s0);
+      s[2 * k + 1] = f2_sum(s1);
     }
     row_sums<TPR>(s, slots, turn);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      // dx = rc t - rc mean(t) - xh rc mean(t xh)
-      const float c0 = -rc[k] * (s[2 * k] * inv), c1 = -rc[k] * (s[2 * k + 1] * inv);
+      // dx = r t - r mean(t) - xh r mean(t xh)
+      const float a0 = -rc[k] * (s[2 * k] * inv), a1 = -rc[k] * (s[2 * k + 1] * inv);
+      const uint64_t c0 = f2(a0, a0), c1 = f2(a1, a1), neg = f2(-mc[k], -mc[k]), r2 = f2(rc[k], rc[k]);
       if (i + k < sh.mine)
 #pragma unroll
         for (int j = 0; j < NV; ++j)
           if (ws.has(j)) {
-            float xh[N], d[N];
-            ws.values(xw + 2 * k * row_words, j, xh);
-            ws.values(xw + (2 * k + 1) * row_words, j, d);
+            uint64_t x2[H], d2[H];
+            ws.values(xw + 2 * k * row_words, j, x2);
+            ws.values(xw + (2 * k + 1) * row_words, j, d2);
 #pragma unroll
-            for (int u = 0; u < N; ++u)
-              d[u] = fmaf(rc[k], d[u] * gv[j * N + u], fmaf((xh[u] - mc[k]) * rc[k], c1, c0));
-            store_word(out, ws, j, d);
+            for (int u = 0; u < H; ++u)
+              d2[u] = f2_fma(r2, f2_mul(d2[u], gv[j * H + u]), f2_fma(f2_mul(f2_add(x2[u], neg), r2), c1, c0));
+            store_word(out, ws, j, d2);
           }
       out += out_step;
     }
     at = at + 1 == kRing ? 0 : at + 1;
   }
   float* dst = part + static_cast<long long>(blockIdx.x) * 2 * C;
+  auto put = [&](float* to) {  // the thread's column sums
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int u = 0; u < N; ++u)
+        if (ws.in(j, u)) {
+          const float2 a = f2_get(sg[j * H + u / 2]), b = f2_get(sb[j * H + u / 2]);
+          to[ws.channel(j, u)] = u & 1 ? a.y : a.x;
+          to[C + ws.channel(j, u)] = u & 1 ? b.y : b.x;
+        }
+  };
   if constexpr (TPR != 0) {
     constexpr int kPer = TPR ? TPR : 1;
     float* sums = reinterpret_cast<float*>(ring_);
     float* mine = sums + threadIdx.x / kPer * 2 * C;
     cp_wait<0>();
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int u = 0; u < N; ++u)
-        if (ws.in(j, u)) {
-          mine[ws.channel(j, u)] = sg[j * N + u];
-          mine[C + ws.channel(j, u)] = sb[j * N + u];
-        }
+    put(mine);
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * C; i += blockDim.x) {
       float a = 0.f;
@@ -466,14 +530,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, true))
       dst[i] = a;
     }
   } else {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int u = 0; u < N; ++u)
-        if (ws.in(j, u)) {
-          dst[ws.channel(j, u)] = sg[j * N + u];
-          dst[C + ws.channel(j, u)] = sb[j * N + u];
-        }
+    put(dst);
   }
 }
 
