@@ -225,8 +225,7 @@ int run_bwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tens
   int st, sms;
   if ((st = map_rows(&mq, q, c, c.Hq, L->rows, kTile)) || (st = map_rows(&mk, k, c, c.Hkv, L->rows, kTile)) ||
       (st = map_rows(&mv, v, c, c.Hkv, L->rows, kTile)) || (st = map_rows(&mdo, dO, c, c.Hq, L->rows, kTile)) ||
-      (st = sm_count(&sms)) || (st = allow_smem<pa_bwd_dkv_kernel<T, D>, DkvCfg<D>::SMEM>()) ||
-      (st = allow_smem<pa_bwd_dq_kernel<T, D>, DqCfg<D>::SMEM>()))
+      (st = sm_count(&sms)) || (st = allow_smem<pa_bwd_kernel<T, D>, BwdCfg<D>::SMEM>()))
     return st;
   const unsigned tiles = static_cast<unsigned>(L->fwd.size());
   if (static_cast<long long>(tiles) * c.Hq > (1ll << 30)) return SA_ERR_UNSUPPORTED;  // item numbers stay in 31 bits
@@ -254,9 +253,19 @@ int run_bwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tens
   b.scale = c.scale;
   b.scale_log2 = scale_log2;
   pa_bwd_pre_kernel<T, D><<<dim3(tiles, c.Hq), 256, 0, c.s>>>(dc.fwd, view(o), view(dO), lse, ls, ld, a.n_tiles);
-  pa_bwd_dkv_kernel<T, D><<<std::min(a.n_items, sms), kBwdThreads, DkvCfg<D>::SMEM, c.s>>>(mq, mk, mv, mdo, a);
-  pa_bwd_dq_kernel<T, D><<<std::min(b.n_items, sms), kBwdThreads, DqCfg<D>::SMEM, c.s>>>(mq, mk, mv, mdo, b);
-  return launched();
+  if ((st = launched())) return st;
+  // The main kernel sets itself up while the one before it drains (programmatic stream serialisation).
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(static_cast<long long>(a.n_items) + b.n_items, sms)));
+  cfg.blockDim = dim3(kBwdThreads);
+  cfg.dynamicSmemBytes = BwdCfg<D>::SMEM;
+  cfg.stream = c.s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pa_bwd_kernel<T, D>, mq, mk, mv, mdo, a, b) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
 template <typename F>

@@ -2,14 +2,16 @@
 //
 // pa_bwd_pre_kernel   per (query tile, head): delta_i = <dO_i, o_i> and
 //                     -lse_i log2 e, padded to whole tiles.
-// pa_bwd_dkv_kernel   an item is a tile of 128 keys of one K/V head and all
+// pa_bwd_kernel, dkv_part
+//                     an item is a tile of 128 keys of one K/V head and all
 //                     query tiles of all query heads that see it (head by
 //                     head, diagonal first).  Per step of 128 queries, keys on
 //                     TMEM lanes:
 //                       S^T = K Q^T,    P^T = 2^(S^T c - lse log2 e)
 //                       dP^T = V dO^T,  dS^T = P^T (dP^T - delta)
 //                       dV += P^T dO,   dK += dS^T Q
-// pa_bwd_dq_kernel    an item is a tile of 128 queries of one head and the key
+// pa_bwd_kernel, dq_part
+//                     an item is a tile of 128 queries of one head and the key
 //                     tiles before it; per step S, dP and dS with queries on
 //                     TMEM lanes, and dQ += dS K.
 //
@@ -71,6 +73,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256)
     pa_bwd_pre_kernel(const Slot* slots, View o, View dO, const float* lse, long long ls, float* ld, int n_tiles) {
   constexpr int TPR = D / 8, RPI = 256 / TPR;
+  pdl_trigger();
   const Slot s = slots[blockIdx.x];
   const int h = blockIdx.y, tid = threadIdx.x;
   float* out = ld + (static_cast<long long>(h) * n_tiles + s.base + s.tile) * 2 * kTile;
@@ -115,6 +118,17 @@ __device__ __forceinline__ void row_out(T* out, uint32_t taddr, bool in, float f
   }
 }
 
+// Shared memory of the two parts: their tiles from 0 on, then the barriers of each.
+template <int D>
+struct BwdSmem {
+  static constexpr int BARS = D >= 128 ? 19 : 32;
+  static constexpr int OFF_BARS = 227 * 1024 - 16 - 16 * BARS;
+};
+template <int D>
+struct BwdCfg {
+  static constexpr int OFF_MISC = 227 * 1024 - 16, SMEM = 227 * 1024;
+};
+
 // ------------------------------------------------------------------ dK, dV
 struct DkvArgs {
   const Slot* slots;
@@ -139,17 +153,16 @@ struct DkvCfg {
   static constexpr int OFF_DO = OFF_Q + QST * G::BYTES;
   static constexpr int OFF_DELTA = OFF_DO + OST * G::BYTES;
   static constexpr int OFF_LSE = OFF_DELTA + QST * VEC;
-  static constexpr int OFF_BAR = OFF_LSE + OST * VEC;
+  static constexpr int END = OFF_LSE + OST * VEC;  // of the tiles
   static constexpr int N_BARS = 2 * KVB + 2 * QST + 2 * OST + NS + 3 + 2 + 1;
-  static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
-  static constexpr int SMEM = OFF_MISC + 16;
+  static constexpr int OFF_BAR = BwdSmem<D>::OFF_BARS;
   static constexpr int COL_DP = NS * 128, COL_DV = COL_DP + 128, COL_DK = COL_DV + D;
   // P^T takes the first 16 of each group's 32 columns of its S^T buffer.  With
   // two buffers dS^T takes the other 16, so dP^T is free once it has been read
   // and the next one is under way before dK; with one buffer dS^T goes over
   // dP^T, so that the next S^T only waits for dV.
   static constexpr bool DS_IN_S = NS == 2;
-  static_assert(SMEM <= 227 * 1024 && COL_DK + D <= 512, "shared memory and TMEM");
+  static_assert(END <= OFF_BAR && N_BARS <= BwdSmem<D>::BARS && COL_DK + D <= 512, "shared memory and TMEM");
 };
 
 struct DkvItem {
@@ -166,50 +179,49 @@ __device__ __forceinline__ DkvItem dkv_item(const DkvArgs& a, const Slot& s, int
   return it;
 }
 
+// One part of the kernel: its barriers (their place in shared memory), initialised by one thread.
+template <int D>
+struct DkvBars {
+  using C = DkvCfg<D>;
+  uint64_t *kv_full, *kv_free, *q_full, *q_free, *do_full, *do_free, *s_full, *p_full, *dp_full, *ds_full, *out_full,
+      *out_free, *drain;
+  __device__ __forceinline__ explicit DkvBars(uint8_t* smem) {
+    kv_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [KVB]
+    kv_free = kv_full + C::KVB;                                // [KVB]
+    q_full = kv_free + C::KVB;                                 // [QST]
+    q_free = q_full + C::QST;                                  // [QST]
+    do_full = q_free + C::QST;                                 // [OST]
+    do_free = do_full + C::OST;                                // [OST]
+    s_full = do_free + C::OST;                                 // [NS] S^T of a step
+    p_full = s_full + C::NS;                                   // P^T of a step written
+    dp_full = p_full + 1;                                      // dP^T of a step
+    ds_full = dp_full + 1;                                     // dS^T of a step written
+    out_full = ds_full + 1;                                    // the item's dK, dV
+    out_free = out_full + 1;
+    drain = out_free + 1;
+  }
+  __device__ __forceinline__ void init() const {
+    for (uint64_t* b = kv_full; b < p_full; ++b) mbar_init(b, 1);
+    mbar_init(p_full, kBwdComputeWarps);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, kBwdComputeWarps);
+    mbar_init(out_full, 1);
+    mbar_init(out_free, 4);
+    mbar_init(drain, 1);
+  }
+};
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    pa_bwd_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const DkvArgs a) {
+__device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int* abort_flag, const CUtensorMap& mq,
+                                         const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
+                                         const DkvArgs& a) {
   using C = DkvCfg<D>;
   using G = TileGeo<D>;
   // fp16's P (at most 1) is scaled up for its product, away from the type's subnormals; dV is scaled back
   constexpr float kP = std::is_same<T, __half>::value ? 4096.f : 1.f;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* bar_kv_full = bars;                      // [KVB]
-  uint64_t* bar_kv_free = bar_kv_full + C::KVB;      // [KVB]
-  uint64_t* bar_q_full = bar_kv_free + C::KVB;       // [QST]
-  uint64_t* bar_q_free = bar_q_full + C::QST;        // [QST]
-  uint64_t* bar_do_full = bar_q_free + C::QST;       // [OST]
-  uint64_t* bar_do_free = bar_do_full + C::OST;      // [OST]
-  uint64_t* bar_s_full = bar_do_free + C::OST;       // [NS] S^T of a step
-  uint64_t* bar_p_full = bar_s_full + C::NS;         // P^T of a step written
-  uint64_t* bar_dp_full = bar_p_full + 1;            // dP^T of a step
-  uint64_t* bar_ds_full = bar_dp_full + 1;           // dS^T of a step written
-  uint64_t* bar_out_full = bar_ds_full + 1;          // the item's dK, dV
-  uint64_t* bar_out_free = bar_out_full + 1;
-  uint64_t* bar_drain = bar_out_free + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
-  int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
-
+  const DkvBars<D> bar(smem);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int cta = blockIdx.x, n_ctas = gridDim.x;
-  if (threadIdx.x == 0) {
-    for (int b = 0; b < 2 * C::KVB + 2 * C::QST + 2 * C::OST + C::NS; ++b) mbar_init(bars + b, 1);
-    mbar_init(bar_p_full, kBwdComputeWarps);
-    mbar_init(bar_dp_full, 1);
-    mbar_init(bar_ds_full, kBwdComputeWarps);
-    mbar_init(bar_out_full, 1);
-    mbar_init(bar_out_free, 4);
-    mbar_init(bar_drain, 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == kBwdComputeWarps + 5) tmem_alloc<512>(tmem_slot);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   const SlotWalk walk(a.slots, a.n_items, a.Hkv);
 
   if (warp == kBwdComputeWarps + 4) {
@@ -220,40 +232,40 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
         const DkvItem it = dkv_item(a, walk.take(item, k), item);
         const int kb = ni % C::KVB;
-        if (ni >= C::KVB && !mbar_wait(bar_kv_free + kb, (ni / C::KVB - 1) & 1, abort_flag)) break;
+        if (ni >= C::KVB && !mbar_wait(bar.kv_free + kb, (ni / C::KVB - 1) & 1, abort_flag)) break;
         const int key0 = it.s.start + it.s.tile * kTile;
-        mbar_arrive_expect_tx(bar_kv_full + kb, 2 * G::BYTES);
-        load_tile<D>(smem + C::OFF_K + kb * G::BYTES, &mk, bar_kv_full + kb, it.hk, key0);
-        load_tile<D>(smem + C::OFF_V + kb * G::BYTES, &mv, bar_kv_full + kb, it.hk, key0);
+        mbar_arrive_expect_tx(bar.kv_full + kb, 2 * G::BYTES);
+        load_tile<D>(smem + C::OFF_K + kb * G::BYTES, &mk, bar.kv_full + kb, it.hk, key0);
+        load_tile<D>(smem + C::OFF_V + kb * G::BYTES, &mv, bar.kv_full + kb, it.hk, key0);
         ++ni;
         for (int j = 0; ok && j < it.n; ++j) {
           const int h = it.hk * a.G + j / it.per, qt = it.s.tile + j % it.per, row = it.s.start + qt * kTile;
           const float* ld = a.ld + (static_cast<long long>(h) * a.n_tiles + it.s.base + qt) * 2 * kTile;
           const int sq = g % C::QST;
-          if (g >= C::QST && !mbar_wait(bar_q_free + sq, (g / C::QST - 1) & 1, abort_flag)) {
+          if (g >= C::QST && !mbar_wait(bar.q_free + sq, (g / C::QST - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(bar_q_full + sq, G::BYTES + C::VEC);
-          load_tile<D>(smem + C::OFF_Q + sq * G::BYTES, &mq, bar_q_full + sq, h, row);
-          bulk_load(smem + C::OFF_DELTA + sq * C::VEC, ld + kTile, C::VEC, bar_q_full + sq);
+          mbar_arrive_expect_tx(bar.q_full + sq, G::BYTES + C::VEC);
+          load_tile<D>(smem + C::OFF_Q + sq * G::BYTES, &mq, bar.q_full + sq, h, row);
+          bulk_load(smem + C::OFF_DELTA + sq * C::VEC, ld + kTile, C::VEC, bar.q_full + sq);
           ++g;
           const int so = n_do % C::OST;
-          if (n_do >= C::OST && !mbar_wait(bar_do_free + so, (n_do / C::OST - 1) & 1, abort_flag)) {
+          if (n_do >= C::OST && !mbar_wait(bar.do_free + so, (n_do / C::OST - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(bar_do_full + so, G::BYTES + C::VEC);
-          load_tile<D>(smem + C::OFF_DO + so * G::BYTES, &mdo, bar_do_full + so, h, row);
-          bulk_load(smem + C::OFF_LSE + so * C::VEC, ld, C::VEC, bar_do_full + so);
+          mbar_arrive_expect_tx(bar.do_full + so, G::BYTES + C::VEC);
+          load_tile<D>(smem + C::OFF_DO + so * G::BYTES, &mdo, bar.do_full + so, h, row);
+          bulk_load(smem + C::OFF_LSE + so * C::VEC, ld, C::VEC, bar.do_full + so);
           ++n_do;
         }
       }
       if (*(volatile int*)abort_flag) {  // no copy may land after the CTA has gone
-        for (int i = ni > C::KVB ? ni - C::KVB : 0; i < ni; ++i) mbar_wait_drain(bar_kv_full + i % C::KVB, (i / C::KVB) & 1);
-        for (int i = g > C::QST ? g - C::QST : 0; i < g; ++i) mbar_wait_drain(bar_q_full + i % C::QST, (i / C::QST) & 1);
+        for (int i = ni > C::KVB ? ni - C::KVB : 0; i < ni; ++i) mbar_wait_drain(bar.kv_full + i % C::KVB, (i / C::KVB) & 1);
+        for (int i = g > C::QST ? g - C::QST : 0; i < g; ++i) mbar_wait_drain(bar.q_full + i % C::QST, (i / C::QST) & 1);
         for (int i = n_do > C::OST ? n_do - C::OST : 0; i < n_do; ++i)
-          mbar_wait_drain(bar_do_full + i % C::OST, (i / C::OST) & 1);
+          mbar_wait_drain(bar.do_full + i % C::OST, (i / C::OST) & 1);
       }
     }
   } else if (warp == kBwdComputeWarps + 5) {
@@ -277,7 +289,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       uint8_t* sK = smem + C::OFF_K + kb * G::BYTES;
       uint8_t* sV = smem + C::OFF_V + kb * G::BYTES;
       const Desc k_k = G::kmajor(smem_u32(sK)), v_k = G::kmajor(smem_u32(sV));
-      ok = mbar_wait_warp(bar_kv_full + kb, rk.ph, abort_flag);
+      ok = mbar_wait_warp(bar.kv_full + kb, rk.ph, abort_flag);
       rk.next();
       if (!ok) break;
       const int keys = it.s.len - it.s.tile * kTile;
@@ -288,7 +300,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       int rows_s = it.s.len - it.s.tile * kTile, left_s = it.per, rows_p = rows_s, left_p = it.per;  // of the next query tile
       // S^T (dP^T) of the item's next step; a last, partial query tile is zeroed behind its rows first
       auto issue_s = [&]() -> bool {
-        if (!mbar_wait_warp(bar_q_full + iq.st, iq.ph, abort_flag)) return false;
+        if (!mbar_wait_warp(bar.q_full + iq.st, iq.ph, abort_flag)) return false;
         uint8_t* sQ = smem + C::OFF_Q + iq.st * G::BYTES;
         if (rows_s < kTile) zero_rows<D>(sQ, rows_s, lane);
         rows_s -= kTile;
@@ -299,7 +311,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             mma_bf16_ss(tmem + is.st * 128, k_k.at(G::kstep(kk)), q_k.at(G::kstep(kk)), id_s, kk > 0);
-          mma_commit(bar_s_full + is.st);
+          mma_commit(bar.s_full + is.st);
         }
         __syncwarp();
         iq.next();
@@ -307,7 +319,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         return true;
       };
       auto issue_dp = [&]() -> bool {
-        if (!mbar_wait_warp(bar_do_full + io.st, io.ph, abort_flag)) return false;
+        if (!mbar_wait_warp(bar.do_full + io.st, io.ph, abort_flag)) return false;
         uint8_t* sDO = smem + C::OFF_DO + io.st * G::BYTES;
         if (rows_p < kTile) zero_rows<D>(sDO, rows_p, lane);
         rows_p -= kTile;
@@ -318,7 +330,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             mma_bf16_ss(tmem + C::COL_DP, v_k.at(G::kstep(kk)), do_k.at(G::kstep(kk)), id_s, kk > 0);
-          mma_commit(bar_dp_full);
+          mma_commit(bar.dp_full);
         }
         __syncwarp();
         io.next();
@@ -326,8 +338,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       };
       ok = issue_s() && issue_dp() && (C::NS == 1 || it.n == 1 || issue_s());
       for (int j = 0; ok && j < it.n; ++j) {
-        ok = mbar_wait_warp(bar_p_full, ph, abort_flag);
-        if (ok && j == 0 && ni > 0) ok = mbar_wait_warp(bar_out_free, (ni - 1) & 1, abort_flag);
+        ok = mbar_wait_warp(bar.p_full, ph, abort_flag);
+        if (ok && j == 0 && ni > 0) ok = mbar_wait_warp(bar.out_free, (ni - 1) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         const Desc do_mn = G::mnmajor(smem_u32(smem + C::OFF_DO) + ro.st * G::BYTES);
@@ -336,11 +348,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int kk = 0; kk < kTile / 16; ++kk)  // 16 queries = 8 TMEM columns of P^T, each group's from its first column on
             mma_bf16_ts(tmem + C::COL_DV, tmem + rs.st * 128 + weight_col(kk), do_mn.at(G::mnstep(kk)),
                         id_o, j > 0 || kk > 0);
-          mma_commit(bar_do_free + ro.st);
+          mma_commit(bar.do_free + ro.st);
         }
         __syncwarp();
         if (!C::DS_IN_S && j + 1 < it.n && !(ok = issue_s())) break;  // over P^T, behind its product
-        if (!(ok = mbar_wait_warp(bar_ds_full, ph, abort_flag))) break;
+        if (!(ok = mbar_wait_warp(bar.ds_full, ph, abort_flag))) break;
         if (C::DS_IN_S && j + 1 < it.n && !(ok = issue_dp())) break;
         tc_fence_after();
         const Desc q_mn = G::mnmajor(smem_u32(smem + C::OFF_Q) + rq.st * G::BYTES);
@@ -350,7 +362,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int kk = 0; kk < kTile / 16; ++kk)
             mma_bf16_ts(tmem + C::COL_DK, t_ds + weight_col(kk), q_mn.at(G::mnstep(kk)), id_o,
                         j > 0 || kk > 0);
-          mma_commit(bar_q_free + rq.st);
+          mma_commit(bar.q_free + rq.st);
         }
         __syncwarp();
         rq.next();
@@ -364,13 +376,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
       }
       if (ok && elect_one()) {
-        mma_commit(bar_kv_free + kb);
-        mma_commit(bar_out_full);
+        mma_commit(bar.kv_free + kb);
+        mma_commit(bar.out_full);
       }
     }
     if (elect_one()) {  // every MMA has completed before TMEM is released
-      mma_commit(bar_drain);
-      mbar_wait_drain(bar_drain, 0);
+      mma_commit(bar.drain);
+      mbar_wait_drain(bar.drain, 0);
     }
     __syncwarp();
   } else if (warp >= kBwdComputeWarps) {
@@ -381,7 +393,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int ni = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
       const DkvItem it = dkv_item(a, walk.take(item, k), item);
-      ok = mbar_wait(bar_out_full, ni & 1, abort_flag);
+      ok = mbar_wait(bar.out_full, ni & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
       const int key = it.s.tile * kTile + row;
@@ -392,7 +404,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       row_out<T, D>(static_cast<T*>(const_cast<void*>(a.dk.p)) + krow * a.dk.rs + it.hk * a.dk.hs,
                     tmem + lane_base + C::COL_DK, in, a.scale);
       tc_fence_before();
-      warp_arrive(bar_out_free, lane);
+      warp_arrive(bar.out_free, lane);
     }
   } else {
     // ------------------------------------------------------ P^T and dS^T
@@ -420,7 +432,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const uint32_t t_s = t_row + rs.st * 128, t_dp = t_row + C::COL_DP;
         const float* lse = lse0 + ro.st * kTile;
         const float* delta = delta0 + rq.st * kTile;
-        ok = mbar_wait(bar_do_full + ro.st, ro.ph, abort_flag) && mbar_wait(bar_s_full + rs.st, rs.ph, abort_flag);
+        ok = mbar_wait(bar.do_full + ro.st, ro.ph, abort_flag) && mbar_wait(bar.s_full + rs.st, rs.ph, abort_flag);
         tc_fence_after();
         float p[kCols];
         tmem_ld_cols(t_s, p);
@@ -441,9 +453,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int i = 0; i < kCols / 2; ++i) pk[i] = Elem<T>::pack(p[2 * i] * kP, p[2 * i + 1] * kP);
         tmem_st_weights(t_s, pk);
         tc_fence_before();
-        warp_arrive(bar_p_full, lane);
+        warp_arrive(bar.p_full, lane);
 
-        ok = ok && mbar_wait(bar_q_full + rq.st, rq.ph, abort_flag) && mbar_wait(bar_dp_full, ph, abort_flag);
+        ok = ok && mbar_wait(bar.q_full + rq.st, rq.ph, abort_flag) && mbar_wait(bar.dp_full, ph, abort_flag);
         tc_fence_after();
         float dp[kCols];
         tmem_ld_cols(t_dp, dp);
@@ -464,19 +476,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int i = 0; i < kCols / 2; ++i) pk[i] = Elem<T>::pack(dp[2 * i], dp[2 * i + 1]);
         tmem_st_weights(C::DS_IN_S ? t_s + kCols / 2 : t_dp, pk);
         tc_fence_before();
-        warp_arrive(bar_ds_full, lane);
+        warp_arrive(bar.ds_full, lane);
         rq.next();
         ro.next();
         rs.next();
         ph ^= 1;
       }
     }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == kBwdComputeWarps + 5) {
-    tc_fence_after();
-    tmem_dealloc<512>(tmem);
   }
 }
 
@@ -501,56 +507,54 @@ struct DqCfg {
   static constexpr int OFF_DO = OFF_Q + QB * G::BYTES;
   static constexpr int OFF_K = OFF_DO + QB * G::BYTES;
   static constexpr int OFF_V = OFF_K + KST * G::BYTES;
-  static constexpr int OFF_BAR = OFF_V + VST * G::BYTES;
+  static constexpr int END = OFF_V + VST * G::BYTES;  // of the tiles
   static constexpr int N_BARS = 2 * QB + 2 * KST + 2 * VST + 2 + 2 + 2 * OB + 1;
-  static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
-  static constexpr int SMEM = OFF_MISC + 16;
+  static constexpr int OFF_BAR = BwdSmem<D>::OFF_BARS + 8 * BwdSmem<D>::BARS;
   static constexpr int COL_DP = 256, COL_DQ = 384;  // S: two buffers from 0; dQ + b * D
-  static_assert(SMEM <= 227 * 1024 && COL_DQ + OB * D <= 512, "shared memory and TMEM");
+  static_assert(END <= BwdSmem<D>::OFF_BARS && N_BARS <= BwdSmem<D>::BARS && COL_DQ + OB * D <= 512,
+                "shared memory and TMEM");
+};
+
+template <int D>
+struct DqBars {
+  using C = DqCfg<D>;
+  uint64_t *q_full, *q_free, *k_full, *k_free, *v_full, *v_free, *s_full, *dp_full, *ds_full, *out_full, *out_free, *drain;
+  __device__ __forceinline__ explicit DqBars(uint8_t* smem) {
+    q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [QB] Q and dO of an item
+    q_free = q_full + C::QB;                                  // [QB]
+    k_full = q_free + C::QB;                                  // [KST]
+    k_free = k_full + C::KST;                                 // [KST]
+    v_full = k_free + C::KST;                                 // [VST]
+    v_free = v_full + C::VST;                                 // [VST]
+    s_full = v_free + C::VST;                                 // [2]
+    dp_full = s_full + 2;
+    ds_full = dp_full + 1;
+    out_full = ds_full + 1;                                   // [OB]
+    out_free = out_full + C::OB;                              // [OB]
+    drain = out_free + C::OB;
+  }
+  __device__ __forceinline__ void init() const {
+    for (uint64_t* b = q_full; b < ds_full; ++b) mbar_init(b, 1);
+    mbar_init(ds_full, kBwdComputeWarps);
+    for (int b = 0; b < C::OB; ++b) {
+      mbar_init(out_full + b, 1);
+      mbar_init(out_free + b, 4);
+    }
+    mbar_init(drain, 1);
+  }
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    pa_bwd_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const DqArgs a) {
+__device__ __forceinline__ void dq_part(uint8_t* smem, const uint32_t tmem, int* abort_flag, const CUtensorMap& mq,
+                                        const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
+                                        const DqArgs& a) {
   using C = DqCfg<D>;
   using G = TileGeo<D>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* bar_q_full = bars;                     // [QB] Q and dO of an item
-  uint64_t* bar_q_free = bar_q_full + C::QB;       // [QB]
-  uint64_t* bar_k_full = bar_q_free + C::QB;       // [KST]
-  uint64_t* bar_k_free = bar_k_full + C::KST;      // [KST]
-  uint64_t* bar_v_full = bar_k_free + C::KST;      // [VST]
-  uint64_t* bar_v_free = bar_v_full + C::VST;      // [VST]
-  uint64_t* bar_s_full = bar_v_free + C::VST;      // [2]
-  uint64_t* bar_dp_full = bar_s_full + 2;
-  uint64_t* bar_ds_full = bar_dp_full + 1;
-  uint64_t* bar_out_full = bar_ds_full + 1;        // [OB]
-  uint64_t* bar_out_free = bar_out_full + C::OB;   // [OB]
-  uint64_t* bar_drain = bar_out_free + C::OB;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
-  int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
-
+  const DqBars<D> bar(smem);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int cta = blockIdx.x, n_ctas = gridDim.x;
-  if (threadIdx.x == 0) {
-    for (int b = 0; b < 2 * C::QB + 2 * C::KST + 2 * C::VST + 3; ++b) mbar_init(bars + b, 1);
-    mbar_init(bar_ds_full, kBwdComputeWarps);
-    for (int b = 0; b < C::OB; ++b) {
-      mbar_init(bar_out_full + b, 1);
-      mbar_init(bar_out_free + b, 4);
-    }
-    mbar_init(bar_drain, 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == kBwdComputeWarps + 5) tmem_alloc<512>(tmem_slot);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const SlotWalk walk(a.slots, a.n_items, a.Hq);
+  // the CTAs in opposite order to the other part's: a few items of both run side by side
+  const int cta = gridDim.x - 1 - blockIdx.x, n_ctas = gridDim.x;
+  const SlotWalk walk(a.slots, a.n_items, a.Hq, cta);
 
   if (warp == kBwdComputeWarps + 4) {
     // -------------------------------------------------------------- producer
@@ -561,34 +565,34 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int h = item % a.Hq;
         const Slot s = walk.take(item, k);
         const int qb = ni % C::QB;
-        if (ni >= C::QB && !mbar_wait(bar_q_free + qb, (ni / C::QB - 1) & 1, abort_flag)) break;
-        mbar_arrive_expect_tx(bar_q_full + qb, 2 * G::BYTES);
-        load_tile<D>(smem + C::OFF_Q + qb * G::BYTES, &mq, bar_q_full + qb, h, s.start + s.tile * kTile);
-        load_tile<D>(smem + C::OFF_DO + qb * G::BYTES, &mdo, bar_q_full + qb, h, s.start + s.tile * kTile);
+        if (ni >= C::QB && !mbar_wait(bar.q_free + qb, (ni / C::QB - 1) & 1, abort_flag)) break;
+        mbar_arrive_expect_tx(bar.q_full + qb, 2 * G::BYTES);
+        load_tile<D>(smem + C::OFF_Q + qb * G::BYTES, &mq, bar.q_full + qb, h, s.start + s.tile * kTile);
+        load_tile<D>(smem + C::OFF_DO + qb * G::BYTES, &mdo, bar.q_full + qb, h, s.start + s.tile * kTile);
         ++ni;
         for (int j = 0; ok && j <= s.tile; ++j) {
           const int row = s.start + j * kTile, sk = g % C::KST;
-          if (g >= C::KST && !mbar_wait(bar_k_free + sk, (g / C::KST - 1) & 1, abort_flag)) {
+          if (g >= C::KST && !mbar_wait(bar.k_free + sk, (g / C::KST - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(bar_k_full + sk, G::BYTES);
-          load_tile<D>(smem + C::OFF_K + sk * G::BYTES, &mk, bar_k_full + sk, h / a.G, row);
+          mbar_arrive_expect_tx(bar.k_full + sk, G::BYTES);
+          load_tile<D>(smem + C::OFF_K + sk * G::BYTES, &mk, bar.k_full + sk, h / a.G, row);
           ++g;
           const int sv = nv % C::VST;
-          if (nv >= C::VST && !mbar_wait(bar_v_free + sv, (nv / C::VST - 1) & 1, abort_flag)) {
+          if (nv >= C::VST && !mbar_wait(bar.v_free + sv, (nv / C::VST - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(bar_v_full + sv, G::BYTES);
-          load_tile<D>(smem + C::OFF_V + sv * G::BYTES, &mv, bar_v_full + sv, h / a.G, row);
+          mbar_arrive_expect_tx(bar.v_full + sv, G::BYTES);
+          load_tile<D>(smem + C::OFF_V + sv * G::BYTES, &mv, bar.v_full + sv, h / a.G, row);
           ++nv;
         }
       }
       if (*(volatile int*)abort_flag) {  // no copy may land after the CTA has gone
-        for (int i = ni > C::QB ? ni - C::QB : 0; i < ni; ++i) mbar_wait_drain(bar_q_full + i % C::QB, (i / C::QB) & 1);
-        for (int i = g > C::KST ? g - C::KST : 0; i < g; ++i) mbar_wait_drain(bar_k_full + i % C::KST, (i / C::KST) & 1);
-        for (int i = nv > C::VST ? nv - C::VST : 0; i < nv; ++i) mbar_wait_drain(bar_v_full + i % C::VST, (i / C::VST) & 1);
+        for (int i = ni > C::QB ? ni - C::QB : 0; i < ni; ++i) mbar_wait_drain(bar.q_full + i % C::QB, (i / C::QB) & 1);
+        for (int i = g > C::KST ? g - C::KST : 0; i < g; ++i) mbar_wait_drain(bar.k_full + i % C::KST, (i / C::KST) & 1);
+        for (int i = nv > C::VST ? nv - C::VST : 0; i < nv; ++i) mbar_wait_drain(bar.v_full + i % C::VST, (i / C::VST) & 1);
       }
     }
   } else if (warp == kBwdComputeWarps + 5) {
@@ -606,13 +610,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
       const Slot s = uniform(walk.take(item, k));
       const int n = s.tile + 1, qb = rq.st, ob = rb.st;
-      ok = mbar_wait_warp(bar_q_full + qb, rq.ph, abort_flag);
+      ok = mbar_wait_warp(bar.q_full + qb, rq.ph, abort_flag);
       if (!ok) break;
       const Desc q_k = G::kmajor(smem_u32(smem + C::OFF_Q) + qb * G::BYTES);
       const Desc do_k = G::kmajor(smem_u32(smem + C::OFF_DO) + qb * G::BYTES);
       auto issue_s = [&](int j) -> bool {
         const int st = ik.st;
-        if (!mbar_wait_warp(bar_k_full + st, ik.ph, abort_flag)) return false;
+        if (!mbar_wait_warp(bar.k_full + st, ik.ph, abort_flag)) return false;
         // keys behind the sequence's last: masked in S, but dS = 0 must not meet a NaN in dS K
         if (s.len - j * kTile < kTile) zero_rows<D>(smem + C::OFF_K + st * G::BYTES, s.len - j * kTile, lane);
         tc_fence_after();
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             mma_bf16_ss(tmem + is.st * 128, q_k.at(G::kstep(kk)), k_k.at(G::kstep(kk)), id_s, kk > 0);
-          mma_commit(bar_s_full + is.st);
+          mma_commit(bar.s_full + is.st);
         }
         __syncwarp();
         ik.next();
@@ -630,15 +634,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       };
       auto issue_dp = [&]() -> bool {
         const int st = iv.st;
-        if (!mbar_wait_warp(bar_v_full + st, iv.ph, abort_flag)) return false;
+        if (!mbar_wait_warp(bar.v_full + st, iv.ph, abort_flag)) return false;
         tc_fence_after();
         const Desc v_k = G::kmajor(smem_u32(smem + C::OFF_V) + st * G::BYTES);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             mma_bf16_ss(tmem + C::COL_DP, do_k.at(G::kstep(kk)), v_k.at(G::kstep(kk)), id_s, kk > 0);
-          mma_commit(bar_dp_full);
-          mma_commit(bar_v_free + st);
+          mma_commit(bar.dp_full);
+          mma_commit(bar.v_free + st);
         }
         __syncwarp();
         iv.next();
@@ -646,8 +650,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       };
       ok = issue_s(0) && issue_dp() && (n == 1 || issue_s(1));
       for (int j = 0; ok && j < n; ++j) {
-        ok = mbar_wait_warp(bar_ds_full, ph, abort_flag);
-        if (ok && j == 0 && ni >= C::OB) ok = mbar_wait_warp(bar_out_free + ob, rb.ph ^ 1, abort_flag);
+        ok = mbar_wait_warp(bar.ds_full, ph, abort_flag);
+        if (ok && j == 0 && ni >= C::OB) ok = mbar_wait_warp(bar.out_free + ob, rb.ph ^ 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (j + 1 < n && !(ok = issue_dp())) break;
@@ -657,7 +661,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int kk = 0; kk < kTile / 16; ++kk)
             mma_bf16_ts(tmem + C::COL_DQ + ob * D, tmem + rs.st * 128 + weight_col(kk), k_mn.at(G::mnstep(kk)),
                         id_o, j > 0 || kk > 0);
-          mma_commit(bar_k_free + rk.st);
+          mma_commit(bar.k_free + rk.st);
         }
         __syncwarp();
         rk.next();
@@ -666,15 +670,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (j + 2 < n && !(ok = issue_s(j + 2))) break;  // over dS, behind its product
       }
       if (ok && elect_one()) {
-        mma_commit(bar_q_free + qb);
-        mma_commit(bar_out_full + ob);
+        mma_commit(bar.q_free + qb);
+        mma_commit(bar.out_full + ob);
       }
       rq.next();
       rb.next();
     }
     if (elect_one()) {  // every MMA has completed before TMEM is released
-      mma_commit(bar_drain);
-      mbar_wait_drain(bar_drain, 0);
+      mma_commit(bar.drain);
+      mbar_wait_drain(bar.drain, 0);
     }
     __syncwarp();
   } else if (warp >= kBwdComputeWarps) {
@@ -686,14 +690,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
       const int h = item % a.Hq, ob = ni % C::OB;
       const Slot s = walk.take(item, k);
-      ok = mbar_wait(bar_out_full + ob, (ni / C::OB) & 1, abort_flag);
+      ok = mbar_wait(bar.out_full + ob, (ni / C::OB) & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
       const int i = s.tile * kTile + row;
       row_out<T, D>(static_cast<T*>(const_cast<void*>(a.dq.p)) + (static_cast<long long>(s.start) + i) * a.dq.rs + h * a.dq.hs,
                     tmem + lane_base + C::COL_DQ + ob * D, i < s.len, a.scale);
       tc_fence_before();
-      warp_arrive(bar_out_free + ob, lane);
+      warp_arrive(bar.out_free + ob, lane);
     }
   } else {
     // ---------------------------------------------------------- P and dS
@@ -718,7 +722,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int j = 0; ok && j <= s.tile; ++j) {
         const bool diag = j == s.tile;
         const uint32_t t_s = t_row + rs.st * 128;
-        ok = mbar_wait(bar_s_full + rs.st, rs.ph, abort_flag);
+        ok = mbar_wait(bar.s_full + rs.st, rs.ph, abort_flag);
         tc_fence_after();
         float p[kCols];
         tmem_ld_cols(t_s, p);
@@ -728,7 +732,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           p[2 * i] = e.x;
           p[2 * i + 1] = e.y;
         }
-        ok = ok && mbar_wait(bar_dp_full, ph, abort_flag);
+        ok = ok && mbar_wait(bar.dp_full, ph, abort_flag);
         tc_fence_after();
         float dp[kCols];
         tmem_ld_cols(t_row + C::COL_DP, dp);
@@ -744,12 +748,44 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int i = 0; i < kCols / 2; ++i) pk[i] = Elem<T>::pack(dp[2 * i], dp[2 * i + 1]);
         tmem_st_weights(t_s, pk);
         tc_fence_before();
-        warp_arrive(bar_ds_full, lane);
+        warp_arrive(bar.ds_full, lane);
         rs.next();
         ph ^= 1;
       }
     }
   }
+}
+
+// Both parts: a CTA's share of the dK/dV items, then of the dQ items, which
+// start as soon as it has none of the first kind left.  The parts share the
+// tile buffers and TMEM; their barriers lie side by side.
+template <typename T, int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    pa_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const DkvArgs a,
+                  const DqArgs b) {
+  using C = BwdCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
+  const int warp = uniform(threadIdx.x >> 5);
+  if (threadIdx.x == 0) {
+    DkvBars<D>(smem).init();
+    DqBars<D>(smem).init();
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kBwdComputeWarps + 5) tmem_alloc<512>(tmem_slot);
+  pdl_wait();  // lse and delta of the kernel before
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  dkv_part<T, D>(smem, tmem, abort_flag, mq, mk, mv, mdo, a);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (*(volatile int*)abort_flag == 0) dq_part<T, D>(smem, tmem, abort_flag, mq, mk, mv, mdo, b);
   tc_fence_before();
   __syncthreads();
   if (warp == kBwdComputeWarps + 5) {

@@ -259,12 +259,14 @@ struct Ring {
 // forward spills: 2 x 12288 rows, 8 heads of 64, 404 -> 474 us.)
 struct SlotWalk {
   const Slot* slots;
-  int n_items, per;  // items, items a slot
-  __device__ __forceinline__ SlotWalk(const Slot* p, int items, int per_slot) : slots(p), n_items(items), per(per_slot) {}
+  int n_items, per, cta;  // items, items a slot, this CTA's number
+  __device__ __forceinline__ SlotWalk(const Slot* p, int items, int per_slot) : SlotWalk(p, items, per_slot, blockIdx.x) {}
+  __device__ __forceinline__ SlotWalk(const Slot* p, int items, int per_slot, int cta_)
+      : slots(p), n_items(items), per(per_slot), cta(cta_) {}
   // the slot of item k of the share, item number `item`
   __device__ __forceinline__ Slot take(int item, int k) const {
     const int4 v = __ldg(reinterpret_cast<const int4*>(slots + item / per));
-    const int next = zigzag(k + 1, blockIdx.x, gridDim.x);
+    const int next = zigzag(k + 1, cta, gridDim.x);
     if (next < n_items) asm volatile("prefetch.global.L1 [%0];" ::"l"(slots + next / per));
     return Slot{v.x, v.y, v.z, v.w};
   }
