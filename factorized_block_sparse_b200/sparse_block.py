@@ -11,6 +11,7 @@ parameters and parameter gradients float32.  There is no CPU fallback.
 
 import ctypes
 import os
+from array import array
 
 import torch
 
@@ -261,9 +262,13 @@ def layer_norm_backward(x, g, dy, mean, rstd, bias=True, stream=None):
 
 
 # ------------------------------------------------- norm and clipping of gradients
+_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
 def _clip(grads, max_norm, out, stream):
+    in_place = out is grads
     grads = list(grads.values()) if isinstance(grads, dict) else list(grads)
-    outs = None if out is None else (list(out.values()) if isinstance(out, dict) else list(out))
+    outs = grads if in_place else None if out is None else list(out.values()) if isinstance(out, dict) else list(out)
     if not grads:
         raise ValueError("expected at least one gradient")
     if outs is not None and len(outs) != len(grads):
@@ -271,26 +276,29 @@ def _clip(grads, max_norm, out, stream):
     dev = grads[0].device
     if dev.type != "cuda":
         raise ValueError("gradients must be CUDA tensors")
+    index = dev.index
     for t in grads:
-        if t.device != dev or not t.is_contiguous():
+        if t.get_device() != index or not t.is_contiguous():
             raise ValueError(f"gradients must be contiguous tensors on {dev}")
-    n = len(grads)
-    dts = [_dtype(t) for t in grads]
-    if out is not grads and outs is not None:
+    codes = [_CODES.get(t.dtype, -1) for t in grads]
+    if -1 in codes:
+        raise ValueError(f"expected bf16, fp16 or float32 gradients, got {grads[codes.index(-1)].dtype}")
+    if outs is not None and not in_place:
         for t, o in zip(grads, outs):
-            if o.shape != t.shape or o.dtype is not t.dtype or o.device != dev or not o.is_contiguous():
+            if o.shape != t.shape or o.dtype is not t.dtype or o.get_device() != index or not o.is_contiguous():
                 raise ValueError("an output must be a contiguous tensor of its gradient's shape, type and device")
     if not _here(dev, stream):
         with _on(dev, stream):
-            return _clip(grads, max_norm, outs, None)
-    VPn = ctypes.c_void_p * n
-    gp = VPn(*[t.data_ptr() for t in grads])
-    op = None if outs is None else VPn(*[t.data_ptr() for t in outs])
+            return _clip(grads, max_norm, grads if in_place else outs, None)
+    # host arrays of pointers, counts and types; the call has read them when it returns
+    gp = array("Q", [t.data_ptr() for t in grads])
+    op = None if outs is None else gp if in_place else array("Q", [t.data_ptr() for t in outs])
+    counts, types = array("Q", [t.numel() for t in grads]), array("i", codes)
     norm = torch.empty((), dtype=torch.float32, device=dev)
     ws = torch.empty(CLIP_WORKSPACE, dtype=torch.uint8, device=dev)
-    sa._check(lib.sparse_block_clip_grads(n, gp, op, (ctypes.c_size_t * n)(*[t.numel() for t in grads]),
-                                          (ctypes.c_int * n)(*dts), float(max_norm), norm.data_ptr(), ws.data_ptr(),
-                                          CLIP_WORKSPACE, _raw_stream(dev.index)),
+    sa._check(lib.sparse_block_clip_grads(len(grads), gp.buffer_info()[0], None if op is None else op.buffer_info()[0],
+                                          counts.buffer_info()[0], types.buffer_info()[0], float(max_norm),
+                                          norm.data_ptr(), ws.data_ptr(), CLIP_WORKSPACE, _raw_stream(index)),
               "sparse_block_clip_grads")
     return norm
 
