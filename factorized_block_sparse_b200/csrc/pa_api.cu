@@ -188,7 +188,11 @@ int run_fwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tens
   a.scale_log2 = static_cast<float>(static_cast<double>(c.scale) * 1.4426950408889634);
   const long long tiles = static_cast<long long>(L->fwd.size());
   long long items;
-  if (tiles * c.Hq <= sms) {  // a CTA for every tile: nothing to pair
+  // A CTA for every tile where there are no more than SMs: nothing to pair (one sequence of 2048, 8 heads of 64: 25 us,
+  // 32 in pairs).  Else two heads of a K/V head share its tiles where the group is even, which leaves no item half
+  // empty (128 sequences of 128, 16 / 8 heads of 64: 45 us, 50 by row tiles; ten ragged sequences, 32 / 8 of 128: 412 and
+  // 423), and two row tiles of a head otherwise.
+  if (tiles * c.Hq <= sms) {
     a.pairing = kSingle;
     a.slots = dc.fwd;
     a.heads = c.Hq;
@@ -212,9 +216,29 @@ int run_fwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tens
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Workspace of the backward pass: packed lse and delta of every (head, tile).
-size_t bwd_ws(int Hq, const pa_layout* L) {
-  return align256(static_cast<size_t>(Hq) * L->fwd.size() * 2 * kTile * sizeof(float)) + 256;
+// Parts that a dK/dV item's steps are cut into.  An item is a key tile of a
+// K/V head with the query tiles of its whole group; where a few items are much
+// longer than an SM's share of all steps (but 8 steps at least, below which
+// the parts' own cost shows), the longest of them is the pass's time.
+// Measured, in one piece and in parts: one sequence of 4096, 4 heads on one
+// K/V head of 64, 141 and 54 us; one of 2048, 8 on 8 of 64 (longest 16 steps, share
+// 7), 29 and (forced) 52 us.
+int bwd_split(int Hq, int Hkv, const pa_layout* L) {
+  constexpr int kSms = 148;  // (a size rule: the workspace must not depend on the device)
+  if (L->bwd.empty()) return 1;
+  const int64_t longest = static_cast<int64_t>(Hq / Hkv) * ((L->longest + kTile - 1) / kTile);
+  const int64_t share = std::max<int64_t>(8, L->steps * Hq / kSms);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(longest / (2 * share), 16)));
+}
+
+// Workspace of the backward pass: packed lse and delta of every (head, tile),
+// then the float32 dV and dK of items in parts.
+size_t bwd_ws_ld(int Hq, const pa_layout* L) {
+  return align256(static_cast<size_t>(Hq) * L->fwd.size() * 2 * kTile * sizeof(float));
+}
+size_t bwd_ws(int Hq, int Hkv, int D, const pa_layout* L) {
+  const int split = bwd_split(Hq, Hkv, L);
+  return bwd_ws_ld(Hq, L) + (split > 1 ? static_cast<size_t>(split) * 2 * Hkv * L->rows * D * sizeof(float) : 0) + 256;
 }
 
 template <typename T, int D>
@@ -235,7 +259,10 @@ int run_bwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tens
   a.slots = dc.bwd;
   a.Hkv = c.Hkv;
   a.G = c.Hq / c.Hkv;
-  a.n_items = static_cast<int>(tiles) * c.Hkv;
+  a.split = bwd_split(c.Hq, c.Hkv, L);
+  a.n_items = static_cast<int>(tiles) * c.Hkv * a.split;
+  a.part = a.split > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + bwd_ws_ld(c.Hq, L)) : nullptr;
+  a.rows = L->rows;
   a.n_tiles = static_cast<int>(tiles);
   a.ld = ld;
   a.dk = view(dk);
@@ -265,7 +292,15 @@ int run_bwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tens
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pa_bwd_kernel<T, D>, mq, mk, mv, mdo, a, b) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, pa_bwd_kernel<T, D>, mq, mk, mv, mdo, a, b) != cudaSuccess) return SA_ERR_CUDA;
+  if (a.split == 1) return SA_OK;
+  cfg.gridDim = dim3(tiles, c.Hkv, kTile / kSumRows);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, pa_bwd_sum_kernel<T, D>, dc.bwd, static_cast<const float*>(a.part), a.split, c.Hkv, a.G,
+                            a.rows, a.dk, a.dv, c.scale) == cudaSuccess
+             ? SA_OK
+             : SA_ERR_CUDA;
 }
 
 template <typename F>
@@ -327,7 +362,7 @@ int packed_attn_fwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, 
 size_t packed_attn_bwd_workspace_size(int Hq, int Hkv, int D, const pa_layout* L) {
   const Call c{L ? static_cast<long long>(L->rows) : 0, Hq, Hkv, D, PA_BF16, 1.f, nullptr};
   if (check_call(c, L)) return 0;
-  return bwd_ws(Hq, L);
+  return bwd_ws(Hq, Hkv, D, L);
 }
 
 int packed_attn_bwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, const pa_tensor* o, const float* lse,

@@ -21,15 +21,26 @@
 // moves 512 D bytes of float32 reductions a tile pair, ran into them (12.9 ms
 // against 9.8 ms without, one sequence of 32768, 16 heads of 128), needs the
 // sums zeroed and converted, and leaves dq's last bits to their order.  Here
-// every sum has a fixed order, so the gradients are the same bits every time.
+// every sum has a fixed order: a call gives the same bits every time.
 //
-// P^T, dS^T and dS go back into TMEM, rounded, over columns that have been
-// read, and are the A operand of their products from there, so shared memory only holds
-// what TMA brings.  One thread issues all MMAs of a CTA; they execute in
-// order, so a product behind another that reads its destination columns needs
-// no wait.
+// P^T, dS^T and dS go back into TMEM, rounded to the tensors' type (the one
+// rounding before their products), over columns that have been read, and are
+// the A operand of their products from there; shared memory only holds what
+// TMA brings.  One thread issues all MMAs of a part; they execute in order, so
+// a product behind another that reads its destination columns needs no wait.
 //
-// Roles of both: compute groups of four warps (thread = row of the tile,
+// What bounds it.  D = 128: the products and the power they draw (executed
+// rate 1.3 PFLOP/s on one sequence of 32768, at about 1.5 GHz).  D <= 64: the
+// exponentials (16 a clock and SM, twice a score) and the arithmetic and waits
+// around them, 2.0 us a tile pair against 0.7 us of products.  Measured there
+// and not kept: the step in two halves of 64 columns with barriers of their
+// own (text shape 1.02 -> 1.50 ms: twice the waits of the issuing thread), a
+// second issuing warp (no change), 64 columns a compute thread (dK/dV part 597
+// -> 679 us).  Times: 2 x 12288 rows, 8 heads of 64, 1.02 ms; ten ragged
+// sequences of 16384 rows, 32 / 8 heads of 128, 1.44 ms; one of 32768, 16 / 2
+// heads of 128, 12.0 ms.
+//
+// Roles of both parts: compute groups of four warps (thread = row of the tile,
 // kCols columns of the step each), four warps for the read-out of an item's
 // result, one whose lane 0 is the TMA producer, one for TMEM and the MMAs.
 #pragma once
@@ -40,6 +51,10 @@
 
 namespace pa {
 
+// Of every 8 pairs of exponentials, those on the FMA pipe (P is rounded to
+// half the bits right after, and nothing is summed before).  Measured at none
+// and here: dK/dV part 687 and 658 us (D = 64, text shape), 839 and 813 (D =
+// 128, ragged); dQ part 477 and 466 (D = 64); at D = 128 any share costs.
 template <int D>
 constexpr int kDkvPoly = D <= 64 ? 1 : 3;
 template <int D>
@@ -101,6 +116,60 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// Steps of part sp of an item of `all` steps.
+__host__ __device__ __forceinline__ int part_first(int all, int sp, int split) {
+  return static_cast<int>(static_cast<long long>(all) * sp / split);
+}
+
+// fp16's P (at most 1) is scaled up for its product, away from the type's subnormals; dV is scaled back.
+template <typename T>
+constexpr float kWeightScale = std::is_same<T, __half>::value ? 4096.f : 1.f;
+
+// dV and dK of items in parts: the parts' sums in order, rounded once.  A block
+// takes kSumRows rows of a (key tile, K/V head), a thread 8 columns of one.
+constexpr int kSumRows = 16;
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+    pa_bwd_sum_kernel(const Slot* slots, const float* part, int split, int Hkv, int G, long long rows, View dk, View dv,
+                      float scale) {
+  pdl_wait();
+  const Slot s = slots[blockIdx.x];
+  const int hk = blockIdx.y, r0 = blockIdx.z * kSumRows, n_rows = min(kSumRows, s.len - s.tile * kTile - r0);
+  const int all = ((s.len + kTile - 1) / kTile - s.tile) * G;
+  const long long row0 = static_cast<long long>(s.start) + s.tile * kTile + r0, plane = Hkv * rows * D;
+  for (int i = threadIdx.x; i < 2 * n_rows * (D / 8); i += 256) {
+    const int c = i % (D / 8), which = i / (D / 8) / n_rows, r = i / (D / 8) % n_rows;
+    const float* p = part + which * plane + (hk * rows + row0 + r) * D + c * 8;
+    float x[8] = {};
+    for (int sp = 0; sp < split; ++sp) {
+      if (part_first(all, sp, split) == part_first(all, sp + 1, split)) continue;  // (never written)
+      const float4 u = *reinterpret_cast<const float4*>(p + sp * 2 * plane);
+      const float4 v = *reinterpret_cast<const float4*>(p + sp * 2 * plane + 4);
+      x[0] += u.x, x[1] += u.y, x[2] += u.z, x[3] += u.w, x[4] += v.x, x[5] += v.y, x[6] += v.z, x[7] += v.w;
+    }
+    const View& o = which ? dk : dv;
+    const float f = which ? scale : 1.f / kWeightScale<T>;
+    *reinterpret_cast<uint4*>(static_cast<T*>(const_cast<void*>(o.p)) + (row0 + r) * o.rs + hk * o.hs + c * 8) =
+        make_uint4(Elem<T>::pack(x[0] * f, x[1] * f), Elem<T>::pack(x[2] * f, x[3] * f),
+                   Elem<T>::pack(x[4] * f, x[5] * f), Elem<T>::pack(x[6] * f, x[7] * f));
+  }
+}
+
+// Writes one row's D float32 values from TMEM.
+template <int D>
+__device__ __forceinline__ void row_out_f32(float* out, uint32_t taddr, bool in) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    float x[32];
+    tmem_ld32(taddr + c * 32, x);
+    tmem_wait_ld();
+    if (in)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float4*>(out + c * 32 + 4 * i) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  }
+}
+
 // Writes one row's D float32 values from TMEM, times f, as T.
 template <typename T, int D>
 __device__ __forceinline__ void row_out(T* out, uint32_t taddr, bool in, float f) {
@@ -137,6 +206,11 @@ struct DkvArgs {
   const float* ld;  // [Hq][n_tiles][2][128]: -lse log2 e (padding -inf), -delta (padding 0)
   View dk, dv;
   float scale, scale_log2;
+  // Few key tiles and many steps each: the steps of an item in `split` parts,
+  // whose float32 sums pa_bwd_sum_kernel adds up in order.
+  int split;
+  float* part;     // [split][dv, dk][Hkv][rows][D], or null
+  long long rows;
 };
 
 template <int D>
@@ -167,15 +241,19 @@ struct DkvCfg {
 
 struct DkvItem {
   Slot s;
-  int hk, n, per;  // K/V head, steps, steps of one query head
+  int hk, per;       // K/V head, steps of one query head
+  int sp, first, n;  // which part of the steps, its first step and how many (0: nothing to do)
 };
 
 __device__ __forceinline__ DkvItem dkv_item(const DkvArgs& a, const Slot& s, int item) {
   DkvItem it;
-  it.hk = item % a.Hkv;
+  const int r = item % (a.Hkv * a.split);
+  it.hk = r / a.split;
+  it.sp = r % a.split;
   it.s = s;
   it.per = (it.s.len + kTile - 1) / kTile - it.s.tile;
-  it.n = it.per * a.G;
+  it.first = part_first(it.per * a.G, it.sp, a.split);
+  it.n = part_first(it.per * a.G, it.sp + 1, a.split) - it.first;
   return it;
 }
 
@@ -217,12 +295,11 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
                                          const DkvArgs& a) {
   using C = DkvCfg<D>;
   using G = TileGeo<D>;
-  // fp16's P (at most 1) is scaled up for its product, away from the type's subnormals; dV is scaled back
-  constexpr float kP = std::is_same<T, __half>::value ? 4096.f : 1.f;
+  constexpr float kP = kWeightScale<T>;
   const DkvBars<D> bar(smem);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int cta = blockIdx.x, n_ctas = gridDim.x;
-  const SlotWalk walk(a.slots, a.n_items, a.Hkv);
+  const SlotWalk walk(a.slots, a.n_items, a.Hkv * a.split);
 
   if (warp == kBwdComputeWarps + 4) {
     // -------------------------------------------------------------- producer
@@ -231,6 +308,7 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
       int g = 0, ni = 0, n_do = 0;
       for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
         const DkvItem it = dkv_item(a, walk.take(item, k), item);
+        if (it.n == 0) continue;
         const int kb = ni % C::KVB;
         if (ni >= C::KVB && !mbar_wait(bar.kv_free + kb, (ni / C::KVB - 1) & 1, abort_flag)) break;
         const int key0 = it.s.start + it.s.tile * kTile;
@@ -238,7 +316,7 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
         load_tile<D>(smem + C::OFF_K + kb * G::BYTES, &mk, bar.kv_full + kb, it.hk, key0);
         load_tile<D>(smem + C::OFF_V + kb * G::BYTES, &mv, bar.kv_full + kb, it.hk, key0);
         ++ni;
-        for (int j = 0; ok && j < it.n; ++j) {
+        for (int j = it.first; ok && j < it.first + it.n; ++j) {
           const int h = it.hk * a.G + j / it.per, qt = it.s.tile + j % it.per, row = it.s.start + qt * kTile;
           const float* ld = a.ld + (static_cast<long long>(h) * a.n_tiles + it.s.base + qt) * 2 * kTile;
           const int sq = g % C::QST;
@@ -280,11 +358,13 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
     Ring<C::NS> is, rs;
     Ring<C::KVB> rk;
     uint32_t ph = 0;
-    for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
+    for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
       DkvItem it = dkv_item(a, walk.take(item, k), item);
       it.s = uniform(it.s);
       it.per = uniform(it.per);
       it.n = uniform(it.n);
+      if (it.n == 0) continue;
+      const int skip = uniform(it.first) % it.per;  // query tiles before the first step's
       const int kb = rk.st;
       uint8_t* sK = smem + C::OFF_K + kb * G::BYTES;
       uint8_t* sV = smem + C::OFF_V + kb * G::BYTES;
@@ -297,7 +377,7 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
         zero_rows<D>(sK, keys, lane);
         zero_rows<D>(sV, keys, lane);
       }
-      int rows_s = it.s.len - it.s.tile * kTile, left_s = it.per, rows_p = rows_s, left_p = it.per;  // of the next query tile
+      int rows_s = keys - skip * kTile, left_s = it.per - skip, rows_p = rows_s, left_p = left_s;  // of the next query tile
       // S^T (dP^T) of the item's next step; a last, partial query tile is zeroed behind its rows first
       auto issue_s = [&]() -> bool {
         if (!mbar_wait_warp(bar.q_full + iq.st, iq.ph, abort_flag)) return false;
@@ -379,6 +459,7 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
         mma_commit(bar.kv_free + kb);
         mma_commit(bar.out_full);
       }
+      ++ni;
     }
     if (elect_one()) {  // every MMA has completed before TMEM is released
       mma_commit(bar.drain);
@@ -391,18 +472,26 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     bool ok = true;
     int ni = 0;
-    for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
+    for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
       const DkvItem it = dkv_item(a, walk.take(item, k), item);
+      if (it.n == 0) continue;
       ok = mbar_wait(bar.out_full, ni & 1, abort_flag);
       if (!ok) break;
+      ++ni;
       tc_fence_after();
       const int key = it.s.tile * kTile + row;
       const long long krow = static_cast<long long>(it.s.start) + key;
       const bool in = key < it.s.len;
-      row_out<T, D>(static_cast<T*>(const_cast<void*>(a.dv.p)) + krow * a.dv.rs + it.hk * a.dv.hs,
-                    tmem + lane_base + C::COL_DV, in, 1.f / kP);
-      row_out<T, D>(static_cast<T*>(const_cast<void*>(a.dk.p)) + krow * a.dk.rs + it.hk * a.dk.hs,
-                    tmem + lane_base + C::COL_DK, in, a.scale);
+      if (a.part) {
+        float* dst = a.part + ((static_cast<long long>(it.sp) * 2 * a.Hkv + it.hk) * a.rows + krow) * D;
+        row_out_f32<D>(dst, tmem + lane_base + C::COL_DV, in);
+        row_out_f32<D>(dst + a.Hkv * a.rows * D, tmem + lane_base + C::COL_DK, in);
+      } else {
+        row_out<T, D>(static_cast<T*>(const_cast<void*>(a.dv.p)) + krow * a.dv.rs + it.hk * a.dv.hs,
+                      tmem + lane_base + C::COL_DV, in, 1.f / kP);
+        row_out<T, D>(static_cast<T*>(const_cast<void*>(a.dk.p)) + krow * a.dk.rs + it.hk * a.dk.hs,
+                      tmem + lane_base + C::COL_DK, in, a.scale);
+      }
       tc_fence_before();
       warp_arrive(bar.out_free, lane);
     }
@@ -426,7 +515,7 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
     uint32_t ph = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
       const DkvItem it = dkv_item(a, walk.take(item, k), item);
-      for (int j = 0, in_head = 0; ok && j < it.n; ++j) {
+      for (int j = 0, in_head = it.first % it.per; ok && j < it.n; ++j) {
         const bool diag = in_head == 0;
         if (++in_head == it.per) in_head = 0;
         const uint32_t t_s = t_row + rs.st * 128, t_dp = t_row + C::COL_DP;

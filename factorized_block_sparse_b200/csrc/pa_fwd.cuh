@@ -5,21 +5,29 @@
 // heads of one K/V head (same rows), or two neighbouring row tiles of one
 // head.  Per key tile of 128 and unit u
 //   S_u = Q_u K^T     both operands in shared memory, fp32 in TMEM
-//   P = 2^(S c - m)   one thread a row; running maximum and sum of the online
-//                     softmax in registers; P over the S columns, rounded
+//   P = 2^(S c - m)   running maximum and sum of the online softmax in
+//                     registers; P back into TMEM, rounded
 //   O_u += P V        P read from TMEM, fp32 accumulator in TMEM
 // and o = O / sum at the end.  While one unit's softmax runs, the tensor core
 // works on the other unit.  The running maximum moves only when it grows by
-// more than 2^8, so O is rescaled rarely; numerator and
-// denominator use the same maximum, so the quotient is exact up to rounding.
+// more than 2^8, so O is rescaled rarely; numerator and denominator use the
+// same maximum, so the quotient is exact up to rounding.
 //
 // TMEM columns: S_u at 128 u.  D <= 64: P_u at 256 + 64 u and O_u at 384 + D u,
 // so the next S is computed while the softmax works on this one (which is in
-// registers by then), and each unit has an issuing warp of its own.  D = 128 has no room for that: P_u over S_u, O_u at 256
-// + 128 u.  There order makes waits unnecessary: one thread's MMAs execute in
-// order, so S_u(j+1) behind PV_u(j) cannot overwrite a P_u(j) still being read,
-// and the commit behind S_u(j+1) also says that O_u holds PV_u(j), which is
-// what a rescale needs.
+// registers by then), and each unit has an issuing warp of its own.  D = 128
+// has no room for that: P_u over S_u, O_u at 256 + 128 u.  There order makes
+// waits unnecessary: one thread's MMAs execute in order, so S_u(j+1) behind
+// PV_u(j) cannot overwrite a P_u(j) still being read, and the commit behind
+// S_u(j+1) also says that O_u holds PV_u(j), which is what a rescale needs.
+//
+// What bounds it.  D = 128: per unit the chain S -> softmax -> PV, 3.3k cycles
+// for 2.1k of products with two units in turn; one sequence of 32768, 16 / 2
+// heads, 3.3 to 3.9 ms (1.1 to 1.3 PFLOP/s; the clock falls with the power).
+// D <= 64: the softmax (1024 cycles of exponentials a tile pair of 1430 in
+// all); 2 x 12288 rows, 8 heads, 0.38 ms (820 TFLOP/s).  An eighth or more of
+// the exponentials on the FMA pipe did not help either and costs the row sums
+// their last bits.
 //
 // Roles: the softmax and epilogue of a unit in 4 NH warps, NH threads a query
 // row (TMEM lane 32 (w mod 4) + lane) with 128 / NH keys and D / NH output

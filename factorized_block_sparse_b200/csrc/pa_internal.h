@@ -33,6 +33,7 @@ struct DeviceTables {
 struct pa_layout {
   int64_t rows = 0;
   int64_t steps = 0;  // (query tile, key tile) pairs on or below the diagonal
+  int64_t longest = 0;  // rows of the longest sequence
   std::vector<int32_t> lengths;
   std::vector<pa::Slot> fwd, fwd2, bwd;
   mutable std::mutex mu;

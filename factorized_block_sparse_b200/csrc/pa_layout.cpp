@@ -44,6 +44,7 @@ extern "C" int packed_attn_layout(const int32_t* lengths, int n_seqs, pa_layout*
     L->fwd2 = tiles_of(L->lengths, 2 * kTile);
     L->bwd = L->fwd;
     for (const Slot& s : L->fwd) L->steps += s.tile + 1;
+    for (int32_t n : L->lengths) L->longest = std::max<int64_t>(L->longest, n);
     // a query tile meets tile + 1 key tiles, a key tile the query tiles from its own to the last
     auto by_tile = [](const Slot& a, const Slot& b) { return a.tile > b.tile; };
     std::stable_sort(L->fwd.begin(), L->fwd.end(), by_tile);

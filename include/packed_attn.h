@@ -29,7 +29,10 @@
  * extent is 1 is not looked at).  lse: float32 [Hq][lse_stride], natural
  * logarithm.  Score products, softmax and gradient sums are float32; P and
  * dS are rounded to the tensors' type before their second product, outputs
- * once at the end.
+ * once at the end.  Every sum has a fixed order: the same call on the same
+ * device gives the same bits.  fp16: dS = P (dP - delta) is rounded as it is,
+ * so gradients of outputs are to be scaled into fp16's range by the caller, as
+ * for every fp16 gradient.
  *
  * Every call is asynchronous on `stream` (a cudaStream_t, or NULL for the
  * legacy default stream), runs on the current device, and returns an

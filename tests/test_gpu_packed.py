@@ -50,6 +50,11 @@ CASES = [
     ([600, 1, 513], 24, 2, 64, torch.bfloat16),
     ([129, 384] * 6, 6, 6, 32, torch.bfloat16),
     ([700] * 3, 12, 6, 32, torch.float16),
+    # few key tiles with many steps each: their steps in parts, some of them empty
+    ([900, 300, 40], 6, 2, 128, torch.float16),
+    ([1999], 2, 1, 64, torch.bfloat16),
+    ([1500], 1, 1, 128, torch.bfloat16),
+    ([1100, 3], 4, 1, 32, torch.float16),
 ]
 
 
@@ -107,11 +112,11 @@ def test_forward_and_backward(cuda_device, pa, lengths, hq, hkv, d, dtype):
     grads = pa.backward(q, k, v, o, lse, dO, lay)
     assert pa.packed_attn_status() == 0
     check_backward(q, k, v, o, lse, dO, grads, lengths)
-    # dk, dv, o and lse do not depend on the order of atomics
+    # every sum has a fixed order: the same bits again
     o2, lse2 = pa.forward(q, k, v, lay)
     again = pa.backward(q, k, v, o, lse, dO, lay)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
-    assert torch.equal(grads[1], again[1]) and torch.equal(grads[2], again[2])
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
 
 
 @pytest.mark.parametrize("scale", [0.02, 0.5])
@@ -206,10 +211,7 @@ def test_sequences_do_not_touch_one_another(cuda_device, pa, d, value):
     got = (o2, *pa.backward(*y[:3], o2, lse2, y[3], lay))
     for name, a, b in zip(("o", "dq", "dk", "dv"), ref, got):
         for part in (slice(0, 130), slice(200, 400)):
-            if name == "dq":  # float32 sums in arrival order before the last rounding
-                torch.testing.assert_close(a[part], b[part], rtol=2 * U[torch.bfloat16], atol=1e-4)
-            else:
-                assert torch.equal(a[part], b[part]), name
+            assert torch.equal(a[part], b[part]), name
     assert torch.equal(lse[:, :130], lse2[:, :130]) and torch.equal(lse[:, 200:], lse2[:, 200:])
     assert pa.packed_attn_status() == 0
 
@@ -242,8 +244,7 @@ def test_another_stream_and_two_calls_at_once(cuda_device, pa):
         got.append((o, lse, *pa.backward(*x[:3], o, lse, x[3], lay, stream=s)))
     torch.cuda.synchronize()
     for a, b in zip(want, got):
-        assert all(torch.equal(a[i], b[i]) for i in (0, 1, 3, 4))
-        torch.testing.assert_close(a[2], b[2], rtol=2 * U[torch.bfloat16], atol=1e-4)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 def test_captured_and_replayed(cuda_device, pa):
@@ -294,8 +295,10 @@ def test_offsets_beyond_32_bits(cuda_device, pa):
     dO = q.flip(0)
     dq, dk, dv = pa.backward(q, k, v, o, lse, dO, lay)
     r = pa.backward(q[-n:], k[-n:], v[-n:], o2, lse2, dO[-n:], small)
-    torch.testing.assert_close(dq[-n:], r[0], rtol=2 * U[torch.bfloat16], atol=1e-4)
-    assert torch.equal(dk[-n:], r[1]) and torch.equal(dv[-n:], r[2])
+    assert torch.equal(dq[-n:], r[0])
+    # dk and dv: the small call, with few key tiles, takes their sums in parts, so in another order; both against the oracle
+    for dkv in ((dk[-n:], dv[-n:]), r[1:]):
+        check_backward(q[-n:], k[-n:], v[-n:], o2, lse2, dO[-n:], (dq[-n:], *dkv), lengths[-2:])
     assert pa.packed_attn_status() == 0
 
 
