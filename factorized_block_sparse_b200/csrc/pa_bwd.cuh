@@ -475,7 +475,7 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
       const DkvItem it = dkv_item(a, walk.take(item, k), item);
       if (it.n == 0) continue;
-      ok = mbar_wait(bar.out_full, ni & 1, abort_flag);
+      ok = mbar_wait_steps(bar.out_full, ni & 1, abort_flag, it.n);
       if (!ok) break;
       ++ni;
       tc_fence_after();
@@ -779,7 +779,7 @@ __device__ __forceinline__ void dq_part(uint8_t* smem, const uint32_t tmem, int*
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
       const int h = item % a.Hq, ob = ni % C::OB;
       const Slot s = walk.take(item, k);
-      ok = mbar_wait(bar.out_full + ob, (ni / C::OB) & 1, abort_flag);
+      ok = mbar_wait_steps(bar.out_full + ob, (ni / C::OB) & 1, abort_flag, s.tile + 1);
       if (!ok) break;
       tc_fence_after();
       const int i = s.tile * kTile + row;

@@ -101,6 +101,27 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, i
   }
 }
 
+// mbar_wait for something that takes `steps` steps of a kernel's inner loop:
+// an item of a very long sequence may run for more than mbar_wait's second.
+__device__ __forceinline__ bool mbar_wait_steps(uint64_t* bar, uint32_t parity, int* abort, int steps) {
+  const long long t0 = clock64(), limit = kWaitCycles * (1 + steps / 16384);
+  uint32_t spins = 0;
+  while (!mbar_try_wait_hint(bar, parity, 20000u)) {
+    if (((++spins) & 15u) == 0) {
+      if (*(volatile int*)abort || *(volatile int*)&g_status == kStatusTimeout) {
+        *(volatile int*)abort = 1;
+        return false;
+      }
+      if (clock64() - t0 > limit) {
+        atomicExch(&g_status, kStatusTimeout);
+        *(volatile int*)abort = 1;
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ Slot uniform(const Slot& s) {
   return Slot{uniform(s.start), uniform(s.len), uniform(s.tile), uniform(s.base)};

@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       };
       for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
         const FwdItem it = fwd_item(a, walk.take(item, k), item, k);
-        const int n = uniform(it.n[u]), n_all = uniform(max(it.n[0], it.n[1])), len = uniform(it.s.len);
+        const int n = uniform(u ? it.n[1] : it.n[0]), n_all = uniform(max(it.n[0], it.n[1])), len = uniform(it.s.len);
         if (n > 0) {
           ok = full(ring) && mbar_wait_warp(bar_q_full + u, ni & 1, abort_flag) &&
                (ns == 0 || mbar_wait_warp(bar_s_free + u, (ns - 1) & 1, abort_flag));
@@ -363,7 +363,8 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
     int ns = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
       const FwdItem it = fwd_item(a, walk.take(item, k), item, k);
-      const int n = it.n[u];
+      // (selected, not indexed: an index that is not a constant puts the arrays into memory)
+      const int n = u ? it.n[1] : it.n[0], qt = u ? it.qt[1] : it.qt[0], head = u ? it.h[1] : it.h[0];
       if (n == 0) continue;
       float m_used = -INFINITY, l_sum = 0.f;
       for (int j = 0; j < n; ++j, ++ns) {
@@ -436,14 +437,18 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         l_sum = l_sum * factor + (r0.x + r0.y);
       }
       // ------------------------------------------------------------ epilogue
-      if constexpr (NH == 2) l_sum += exchange(l_sum);
       ok = ok && mbar_wait(bar_pv_done + u, (ns - 1) & 1, abort_flag);
       tc_fence_after();
+      if constexpr (NH == 2) {  // (a negative sum: gave up after a timeout, and so does its partner at the barrier)
+        const float theirs = exchange(ok ? l_sum : -1.f);
+        ok = ok && !(theirs < 0.f);
+        l_sum += theirs;
+      }
       const float inv = 1.f / l_sum;
-      const int r0 = it.qt[u] * kTile + quarter * 32;  // the warp's first row in the sequence
+      const int r0 = qt * kTile + quarter * 32;  // the warp's first row in the sequence
       const long long row0 = static_cast<long long>(it.s.start) + r0;
       const int rows = min(32, it.s.len - r0);
-      T* out = static_cast<T*>(const_cast<void*>(a.o.p)) + row0 * a.o.rs + static_cast<long long>(it.h[u]) * a.o.hs +
+      T* out = static_cast<T*>(const_cast<void*>(a.o.p)) + row0 * a.o.rs + static_cast<long long>(head) * a.o.hs +
                half * (D / NH);
       constexpr int CHUNKS = C::STG_ROWB / 16;  // 16-byte chunks of a staged row
       constexpr int PASSES = D / NH / C::STG_COLS;
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         __syncwarp();
       }
       if (half == 0 && lane < rows)
-        a.lse[static_cast<long long>(it.h[u]) * a.ls + row0 + lane] =
+        a.lse[static_cast<long long>(head) * a.ls + row0 + lane] =
             (m_used + log2f(l_sum) - Elem<T>::kBias) * 0.6931471805599453f;
     }
   }

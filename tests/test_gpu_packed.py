@@ -324,3 +324,61 @@ def test_refusals_on_the_gpu(cuda_device, pa):
         pa.packed_attn_fwd(q, q, q, o, lse.double(), lay)
     with pytest.raises(sa.SparseAttnError):
         pa.backward(q, q, q, o, lse, q, lay, ws=torch.empty(64, dtype=torch.uint8, device=cuda_device))
+
+
+def test_a_layout_freed_during_a_capture(cuda_device, pa):
+    # a garbage collector may drop another batch's layout at any time: the capture under way stays whole
+    lengths, hq, hkv, d = [200, 90], 2, 1, 64
+    x = [t.to(cuda_device) for t in draw(sum(lengths), hq, hkv, d, torch.bfloat16)]
+    lay, other = pa.Layout(lengths), pa.Layout([64, 64])
+    lay.upload(cuda_device)
+    other.upload(cuda_device)
+    want = pa.forward(*x[:3], lay)
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        o, lse = pa.forward(*x[:3], lay)
+        other.close()
+        o2, _ = pa.forward(*x[:3], lay)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(o2, want[0]) and torch.equal(lse, want[1])
+
+
+def test_a_long_sequence_sampled(cuda_device, pa):
+    # 40000 rows in one sequence behind a short one: rows and keys here and there against the oracle's formulas
+    lengths, hq, hkv, d = [77, 40000], 2, 1, 64
+    q, k, v, dO = (t.to(cuda_device) for t in draw(sum(lengths), hq, hkv, d, torch.bfloat16))
+    lay = pa.Layout(lengths)
+    o, lse = pa.forward(q, k, v, lay)
+    dq, dk, dv = pa.backward(q, k, v, o, lse, dO, lay)
+    assert pa.packed_attn_status() == 0
+    u, c = U[torch.bfloat16], d ** -0.5
+    kk, vv = (t[77:, 0].double() for t in (k, v))
+    for h in range(hq):
+        qq, gg, oo = (t[77:, h].double() for t in (q, dO, o))
+        L = lse[h, 77:].double()
+        delta = (gg * oo).sum(-1)
+        for i in (0, 127, 128, 20001, 39999):  # a query row
+            s = c * (kk[:i + 1] @ qq[i])
+            p = torch.exp(s - torch.logsumexp(s, 0))
+            ref, mag = p @ vv[:i + 1], p @ vv[:i + 1].abs()
+            assert ((o[77 + i, h].double() - ref).abs() <= u * (mag + ref.abs()) + 2e-4 * mag).all()
+            assert abs(float(lse[h, 77 + i]) - float(torch.logsumexp(s, 0))) <= 1e-4
+            p = torch.exp(s - L[i])
+            ds = p * (vv[:i + 1] @ gg[i] - delta[i])
+            ref, mag = c * (ds @ kk[:i + 1]), c * (ds.abs() @ kk[:i + 1].abs())
+            noise = c * (p @ kk[:i + 1].abs())
+            assert ((dq[77 + i, h].double() - ref).abs() <= u * (mag + ref.abs()) + 5e-4 * noise).all()
+    for j in (0, 20001, 39990):  # a key: its sums run over both query heads
+        ref = {n: torch.zeros(d, dtype=torch.float64, device=cuda_device) for n in ("dk", "dv", "mk", "mv", "nk")}
+        for h in range(hq):
+            qq, gg, oo = (t[77 + j:, h].double() for t in (q, dO, o))
+            p = torch.exp(c * (qq @ kk[j]) - lse[h, 77 + j:].double())
+            ds = p * (gg @ vv[j] - (gg * oo).sum(-1))
+            for n, t in (("dk", c * (ds @ qq)), ("dv", p @ gg), ("mk", c * (ds.abs() @ qq.abs())), ("mv", p @ gg.abs()),
+                         ("nk", c * (p @ qq.abs()))):
+                ref[n] += t
+        assert ((dk[77 + j, 0].double() - ref["dk"]).abs() <= u * (ref["mk"] + ref["dk"].abs()) + 5e-4 * ref["nk"]).all()
+        assert ((dv[77 + j, 0].double() - ref["dv"]).abs() <= u * (ref["mv"] + ref["dv"].abs()) + 2e-4 * ref["mv"]).all()
