@@ -99,6 +99,8 @@ bool output_ok(const pa_tensor* t, const Call& c, int heads) {
   return (heads - 1) * hs + c.D <= rs || (c.rows - 1) <= (hs - c.D) / rs;
 }
 
+bool lse_ok(const float* lse) { return lse && (reinterpret_cast<uintptr_t>(lse) & 3) == 0; }
+
 int check_call(const Call& c, const pa_layout* L) {
   if (!L || c.Hq < 1 || c.Hkv < 1 || c.Hq > 65535 || c.Hq % c.Hkv || c.rows < L->rows ||
       c.rows > (int64_t(1) << 31) - 1024 || (c.dtype != PA_BF16 && c.dtype != PA_FP16))
@@ -348,7 +350,7 @@ int packed_attn_fwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, 
   int st = check_call(c, L);
   if (st) return st;
   if (L->rows == 0) return SA_OK;
-  if (!tensor_ok(q, c, Hq) || !tensor_ok(k, c, Hkv) || !tensor_ok(v, c, Hkv) || !output_ok(o, c, Hq) || !lse ||
+  if (!tensor_ok(q, c, Hq) || !tensor_ok(k, c, Hkv) || !tensor_ok(v, c, Hkv) || !output_ok(o, c, Hq) || !lse_ok(lse) ||
       lse_stride < rows || o->data == q->data || o->data == k->data || o->data == v->data)
     return SA_ERR_INVALID_ARG;
   if (!have_encode()) return SA_ERR_CUDA;
@@ -374,7 +376,7 @@ int packed_attn_bwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, 
   if (st) return st;
   if (L->rows == 0) return SA_OK;
   if (!tensor_ok(q, c, Hq) || !tensor_ok(k, c, Hkv) || !tensor_ok(v, c, Hkv) || !tensor_ok(o, c, Hq) ||
-      !tensor_ok(dO, c, Hq) || !output_ok(dq, c, Hq) || !output_ok(dk, c, Hkv) || !output_ok(dv, c, Hkv) || !lse ||
+      !tensor_ok(dO, c, Hq) || !output_ok(dq, c, Hq) || !output_ok(dk, c, Hkv) || !output_ok(dv, c, Hkv) || !lse_ok(lse) ||
       lse_stride < rows)
     return SA_ERR_INVALID_ARG;
   const pa_tensor* outs[3] = {dq, dk, dv};

@@ -174,19 +174,6 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int lane) {
   __syncwarp();
 }
 
-// Bulk reduction of float32 values from shared memory into global memory
-// (both 16-byte aligned, bytes a multiple of 16), in a bulk async-group.
-__device__ __forceinline__ void bulk_reduce_add(float* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)),
-               "r"(bytes)
-               : "memory");
-}
-// Wait until the sources of all but the N latest bulk groups have been read.
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-
 // 32 lanes x 32 bit, 32 consecutive columns: thread t gets lane (base + t).
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);

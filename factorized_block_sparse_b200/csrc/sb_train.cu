@@ -56,26 +56,42 @@ __device__ __forceinline__ float f2_sum(uint64_t v) {
   return t.x + t.y;
 }
 
-// The N elements of a 16-byte word.
+// The N elements of a 16-byte word, two of a 2-byte type from each 32-bit
+// register (taken and cast one by one they were a third of the backward
+// kernel's instructions).
 template <typename T, int N>
 __device__ __forceinline__ void unpack(const uint4& w, float* f) {
-  const T* e = reinterpret_cast<const T*>(&w);
+  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int u = 0; u < N; ++u) f[u] = to_f(e[u]);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+      f[2 * i] = __uint_as_float(r[i] << 16);
+      f[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+    } else if constexpr (std::is_same_v<T, __half>) {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    } else {
+      f[i] = __uint_as_float(r[i]);
+    }
+  }
 }
 template <typename T, int N>
 __device__ __forceinline__ uint4 pack(const float* f) {
-  uint4 w;
-  T* e = reinterpret_cast<T*>(&w);
+  uint32_t r[4];
 #pragma unroll
-  for (int u = 0; u < N; ++u) e[u] = static_cast<T>(f[u]);
-  return w;
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int w = 16; w >= 1; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
-  return v;
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+      const __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      r[i] = *reinterpret_cast<const uint32_t*>(&t);
+    } else if constexpr (std::is_same_v<T, __half>) {
+      const __half2 t = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      r[i] = *reinterpret_cast<const uint32_t*>(&t);
+    } else {
+      r[i] = __float_as_uint(f[i]);
+    }
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // Sums over the threads of a row: TPR lanes of a warp, or the block (TPR = 0;

@@ -19,6 +19,7 @@ Use::
 
 import ctypes
 import os
+from array import array
 
 import numpy as np
 import torch
@@ -33,10 +34,6 @@ EXPORTS = ("packed_attn_layout", "packed_attn_layout_free", "packed_attn_layout_
            "packed_attn_fwd", "packed_attn_bwd_workspace_size", "packed_attn_bwd", "packed_attn_status")
 
 
-class _Tensor(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
-
-
 def load_library(path=None):
     path = path or LIB_PATH
     if not os.path.exists(path):
@@ -44,7 +41,7 @@ def load_library(path=None):
                            "`python -m factorized_block_sparse_b200.build` (no CPU fallback exists)")
     lib = ctypes.CDLL(path)
     I, VP, SZ, L64, F = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64, ctypes.c_float
-    T = ctypes.POINTER(_Tensor)
+    T = VP  # pa_tensor, see _descs
     lib.packed_attn_layout.argtypes = [VP, I, ctypes.POINTER(VP)]
     lib.packed_attn_layout.restype = I
     lib.packed_attn_layout_free.argtypes = [VP]
@@ -116,7 +113,7 @@ def _check_tensors(q, k, v, layout, more=()):
         raise ValueError(f"k and v must be [{T}, Hkv, {D}], got {tuple(ks)} and {tuple(v.shape)}")
     if T < layout.rows:
         raise ValueError(f"the layout has {layout.rows} rows, the tensors {T}")
-    dt, dev = q.dtype, q.device
+    dt, index = q.dtype, q.get_device() if q.is_cuda else None
     if dt is torch.bfloat16:
         code = 0
     elif dt is torch.float16:
@@ -126,16 +123,23 @@ def _check_tensors(q, k, v, layout, more=()):
     for name, t, shape in (("q", q, qs), ("k", k, ks), ("v", v, ks), *more):
         if t.shape != shape:
             raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-        if t.dtype is not dt or not t.is_cuda or t.device != dev:
+        if t.dtype is not dt or t.get_device() != index:
             raise ValueError(f"{name} must be a {dt} tensor on the CUDA device of q")
         if t.stride(2) != 1 and D > 1:
             raise ValueError(f"the last dimension of {name} must be contiguous")
     return T, Hq, Hkv, D, code
 
 
-def _desc(t):
-    """The C view of a ``[T, H, D]`` tensor; the strides of extents of 1 carry no meaning and are not read."""
-    return _Tensor(t.data_ptr(), t.stride(0), t.stride(1))
+def _descs(*tensors):
+    """The C views (``pa_tensor``: address, row and head stride) of ``[T, H, D]`` tensors: an array and their addresses
+    in it.  The strides of extents of 1 carry no meaning and are not read."""
+    flat = []
+    for t in tensors:
+        rows, heads, _ = t.stride()
+        flat += t.data_ptr(), rows, heads
+    a = array("q", flat)
+    at = a.buffer_info()[0]
+    return a, range(at, at + 24 * len(tensors), 24)
 
 
 def _check_lse(lse, Hq, T, q):
@@ -168,17 +172,18 @@ def _call(device, stream, what, fn, *args):
 
 def _fwd(q, k, v, o, lse, ls, dims, layout, stream, scale):
     T, Hq, Hkv, D, code = dims
-    _call(q.device, stream, "packed_attn_fwd", lib.packed_attn_fwd, _desc(q), _desc(k), _desc(v), _desc(o), lse.data_ptr(),
-          ls, T, Hq, Hkv, D, code, D ** -0.5 if scale is None else float(scale), layout.handle)
+    views, at = _descs(q, k, v, o)  # (kept until the call has read them)
+    _call(q.device, stream, "packed_attn_fwd", lib.packed_attn_fwd, *at, lse.data_ptr(), ls, T, Hq, Hkv, D, code,
+          D ** -0.5 if scale is None else float(scale), layout.handle)
 
 
 def _bwd(q, k, v, o, lse, ls, dO, dq, dk, dv, dims, layout, ws, stream, scale):
     T, Hq, Hkv, D, code = dims
     if ws.device != q.device or not ws.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the device of q")
-    _call(q.device, stream, "packed_attn_bwd", lib.packed_attn_bwd, _desc(q), _desc(k), _desc(v), _desc(o),
-          lse.data_ptr(), ls, _desc(dO), _desc(dq), _desc(dk), _desc(dv), T, Hq, Hkv, D, code,
-          D ** -0.5 if scale is None else float(scale), layout.handle, ws.data_ptr(), ws.numel() * ws.element_size())
+    views, at = _descs(q, k, v, o, dO, dq, dk, dv)  # (kept until the call has read them)
+    _call(q.device, stream, "packed_attn_bwd", lib.packed_attn_bwd, *at[:4], lse.data_ptr(), ls, *at[4:], T, Hq, Hkv,
+          D, code, D ** -0.5 if scale is None else float(scale), layout.handle, ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def packed_attn_fwd(q, k, v, o, lse, layout, stream=None, scale=None):
@@ -200,25 +205,20 @@ def packed_attn_status(stream=None):
 
 # ------------------------------------------------------------ conveniences
 def _on_stream(stream, device):
-    """torch work of a call (allocation, zeroing) on the stream that the call runs on."""
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+    """A context of the stream that a call runs on, for its allocations and its launches."""
+    if isinstance(stream, int):
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device))
+    if stream.device != device:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
 
 
-def _outputs(q, layout, shapes):
-    """Tensors of ``(shape, dtype, dimension of the rows)``, zero in the rows behind the last sequence."""
-    dev, rows = q.device, layout.rows
-    outs = [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype, _ in shapes]
-    for t, (shape, _, dim) in zip(outs, shapes):
-        if rows < shape[dim]:
-            t.narrow(dim, rows, shape[dim] - rows).zero_()
-    return outs
-
-
-def _allocate(q, layout, shapes, stream):
-    if stream is None:
-        return _outputs(q, layout, shapes)
-    with _on_stream(stream, q.device):
-        return _outputs(q, layout, shapes)
+def _new(like, rows):
+    """A contiguous tensor of the shape, type and device of another, zero in the rows behind the last sequence."""
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    if rows < t.shape[0]:
+        t[rows:].zero_()
+    return t
 
 
 def workspace(Hq, Hkv, D, layout, device):
@@ -231,9 +231,15 @@ def workspace(Hq, Hkv, D, layout, device):
 def forward(q, k, v, layout, stream=None, scale=None):
     """Allocates ``o`` and ``lse`` (zero in rows behind the last sequence) and runs the forward pass."""
     dims = _check_tensors(q, k, v, layout)
-    T, Hq, _, D, _ = dims
-    o, lse = _allocate(q, layout, (((T, Hq, D), q.dtype, 0), ((Hq, T), torch.float32, 1)), stream)
-    _fwd(q, k, v, o, lse, T, dims, layout, stream, scale)
+    if stream is not None:
+        with _on_stream(stream, q.device):
+            return forward(q, k, v, layout, scale=scale)
+    T, Hq, rows = dims[0], dims[1], layout.rows
+    o = _new(q, rows)
+    lse = torch.empty(Hq, T, dtype=torch.float32, device=q.device)
+    if rows < T:
+        lse[:, rows:].zero_()
+    _fwd(q, k, v, o, lse, T, dims, layout, None, scale)
     return o, lse
 
 
@@ -242,13 +248,12 @@ def backward(q, k, v, o, lse, dO, layout, ws=None, stream=None, scale=None):
     dims = _check_tensors(q, k, v, layout, (("o", o, q.shape), ("dO", dO, q.shape)))
     T, Hq, Hkv, D, _ = dims
     ls = _check_lse(lse, Hq, T, q)
-    kv = ((T, Hkv, D), q.dtype, 0)
-    dq, dk, dv = _allocate(q, layout, (((T, Hq, D), q.dtype, 0), kv, kv), stream)
+    if stream is not None:
+        with _on_stream(stream, q.device):
+            return backward(q, k, v, o, lse, dO, layout, ws, scale=scale)
+    rows = layout.rows
+    dq, dk, dv = _new(q, rows), _new(k, rows), _new(v, rows)
     if ws is None:
-        if stream is None:
-            ws = workspace(Hq, Hkv, D, layout, q.device)
-        else:
-            with _on_stream(stream, q.device):
-                ws = workspace(Hq, Hkv, D, layout, q.device)
-    _bwd(q, k, v, o, lse, ls, dO, dq, dk, dv, dims, layout, ws, stream, scale)
+        ws = workspace(Hq, Hkv, D, layout, q.device)
+    _bwd(q, k, v, o, lse, ls, dO, dq, dk, dv, dims, layout, ws, None, scale)
     return dq, dk, dv

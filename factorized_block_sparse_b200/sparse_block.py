@@ -187,6 +187,8 @@ def _on(device, stream):
     """A context of the device and the stream that a call runs on, for its allocations and its launch."""
     import contextlib
 
+    if stream is not None and not isinstance(stream, int) and stream.device != device:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on {device}")
     cm = contextlib.ExitStack()
     if device.index != torch.cuda.current_device():
         cm.enter_context(torch.cuda.device(device))
@@ -218,14 +220,17 @@ def layer_norm(x, g, b=None, eps=1e-5, stream=None):
     if not _here(dev, stream):
         with _on(dev, stream):
             return layer_norm(x, g, b, eps)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev)
-    mp = stats.data_ptr()
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if x.dim() == 2:
+        mean = torch.empty(M, dtype=torch.float32, device=dev)
+    else:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    rstd = torch.empty_like(mean)
     if M:
-        sa._check(lib.sparse_block_layer_norm_fwd(x.data_ptr(), ld, gp, bp, y.data_ptr(), C, mp, mp + 4 * M, M, C, eps,
-                                                  dt, _raw_stream(dev.index)),
-                  "sparse_block_layer_norm_fwd")
-    mean, rstd = stats.unbind(0)
+        st = lib.sparse_block_layer_norm_fwd(x.data_ptr(), ld, gp, bp, y.data_ptr(), C, mean.data_ptr(), rstd.data_ptr(),
+                                             M, C, eps, dt, _raw_stream(dev.index))
+        if st:
+            raise sa.SparseAttnError(st, "sparse_block_layer_norm_fwd")
     return y, mean, rstd
 
 
@@ -245,19 +250,18 @@ def layer_norm_backward(x, g, dy, mean, rstd, bias=True, stream=None):
     if not _here(dev, stream):
         with _on(dev, stream):
             return layer_norm_backward(x, g, dy, mean, rstd, bias)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    grads = torch.empty((2, C) if bias else (1, C), dtype=torch.float32, device=dev)
-    dg, db = grads[0], (grads[1] if bias else None)
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     if M == 0:
-        grads.zero_()
-        return dx, dg, db
+        return dx, torch.zeros_like(g), torch.zeros_like(g) if bias else None
+    dg = torch.empty_like(g)
+    db = torch.empty_like(g) if bias else None
     n = lib.sparse_block_layer_norm_bwd_workspace_size(M, C)
-    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
-    gptr = grads.data_ptr()
-    sa._check(lib.sparse_block_layer_norm_bwd(x.data_ptr(), ld, gp, dy.data_ptr(), ldd, mean.data_ptr(), rstd.data_ptr(),
-                                              dx.data_ptr(), C, gptr, gptr + 4 * C if bias else None, M, C, dt,
-                                              ws.data_ptr(), max(n, 256), _raw_stream(dev.index)),
-              "sparse_block_layer_norm_bwd")
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    st = lib.sparse_block_layer_norm_bwd(x.data_ptr(), ld, gp, dy.data_ptr(), ldd, mean.data_ptr(), rstd.data_ptr(),
+                                         dx.data_ptr(), C, dg.data_ptr(), db.data_ptr() if bias else None, M, C, dt,
+                                         ws.data_ptr(), n, _raw_stream(dev.index))
+    if st:
+        raise sa.SparseAttnError(st, "sparse_block_layer_norm_bwd")
     return dx, dg, db
 
 
@@ -296,10 +300,11 @@ def _clip(grads, max_norm, out, stream):
     counts, types = array("Q", [t.numel() for t in grads]), array("i", codes)
     norm = torch.empty((), dtype=torch.float32, device=dev)
     ws = torch.empty(CLIP_WORKSPACE, dtype=torch.uint8, device=dev)
-    sa._check(lib.sparse_block_clip_grads(len(grads), gp.buffer_info()[0], None if op is None else op.buffer_info()[0],
-                                          counts.buffer_info()[0], types.buffer_info()[0], float(max_norm),
-                                          norm.data_ptr(), ws.data_ptr(), CLIP_WORKSPACE, _raw_stream(index)),
-              "sparse_block_clip_grads")
+    st = lib.sparse_block_clip_grads(len(grads), gp.buffer_info()[0], None if op is None else op.buffer_info()[0],
+                                     counts.buffer_info()[0], types.buffer_info()[0], float(max_norm), norm.data_ptr(),
+                                     ws.data_ptr(), CLIP_WORKSPACE, _raw_stream(index))
+    if st:
+        raise sa.SparseAttnError(st, "sparse_block_clip_grads")
     return norm
 
 

@@ -84,8 +84,9 @@ int packed_attn_layout_upload(const pa_layout* layout, void* stream);
  * Errors: SA_ERR_INVALID_ARG (null pointer, head counts below 1 or Hq not a
  * multiple of Hkv, more than 65535 heads, rows below the layout's, unknown
  * type, misaligned address or stride, an output whose rows would overlap or
- * that is one of the inputs, scale not finite and positive, lse_stride below
- * rows), SA_ERR_UNSUPPORTED (D), SA_ERR_CUDA.
+ * that begins where an input does, scale not finite and positive, lse_stride
+ * below rows), SA_ERR_UNSUPPORTED (D), SA_ERR_CUDA.  Outputs must not overlap
+ * inputs or one another in any other way either, which is not looked for.
  */
 int packed_attn_fwd(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, const pa_tensor* o, float* lse,
                     int64_t lse_stride, int64_t rows, int Hq, int Hkv, int D, int dtype, float scale,

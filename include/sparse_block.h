@@ -177,7 +177,7 @@ size_t sparse_block_clip_workspace_size(void);
  * vanish in float32 and has a fixed order.  A norm that is not finite acts as
  * the formula says: c = 0 for inf, NaN for NaN.
  * Errors: SA_ERR_INVALID_ARG (a null array, a null pointer with a count above
- * 0, n < 0, an unknown type, a pointer not aligned to its element, outputs
+ * 0, a count above 2^40, n < 0, an unknown type, a pointer not aligned to its element, outputs
  * that overlap, max_norm negative or NaN), SA_ERR_WORKSPACE, SA_ERR_CUDA.
  */
 int sparse_block_clip_grads(int n, const void* const* grads, void* const* outs, const size_t* numel,

@@ -78,10 +78,12 @@ def test_workspace_size(pa):
         pa.workspace(8, 3, 64, lay, "cpu")
 
 
-def _t(addr, rs=256, hs=64):
-    from factorized_block_sparse_b200.packed_attn import _Tensor
+class _View(ctypes.Structure):  # pa_tensor
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
-    return _Tensor(addr, rs, hs)
+
+def _t(addr, rs=256, hs=64):
+    return ctypes.byref(_View(addr, rs, hs))
 
 
 def test_argument_checks(pa):
@@ -125,6 +127,27 @@ def test_argument_checks(pa):
     # nothing to do: no device work either
     none = pa.Layout([0])
     assert fwd(lay=none.handle, rows=0) == sa.SA_OK and bwd(lay=none.handle, rows=0) == sa.SA_OK
+
+
+def test_misaligned_lse(pa):
+    from factorized_block_sparse_b200 import sparse_attn as sa
+
+    lay = pa.Layout([100])
+    q, k, v, o = _t(0x10000), _t(0x20000, 128), _t(0x30000, 128), _t(0x40000)
+    for lse in (0x50001, 0x50002):
+        assert pa.lib.packed_attn_fwd(q, k, v, o, lse, 100, 100, 4, 2, 64, 0, 0.125, lay.handle,
+                                      None) == sa.SA_ERR_INVALID_ARG
+        assert pa.lib.packed_attn_bwd(q, k, v, o, lse, 100, _t(0x60000), _t(0x70000), _t(0x80000, 128),
+                                      _t(0x90000, 128), 100, 4, 2, 64, 0, 0.125, lay.handle, 0x100000, 1 << 40,
+                                      None) == sa.SA_ERR_INVALID_ARG
+
+
+def test_stream_of_another_device(pa):
+    from types import SimpleNamespace
+
+    s = SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError):
+        pa._on_stream(s, torch.device("cuda", 0))
 
 
 def test_binding_refusals(pa):
