@@ -140,9 +140,11 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* slots, int& turn)
 // holds another row's elements.
 constexpr int kDepth = 3;
 
-// Rows a thread takes at a time: their sums share a barrier, their words the
-// gains in registers.
-__host__ __device__ constexpr int rows_at_once(int nv) { return nv >= 4 ? 1 : 2; }
+// Rows a thread takes at a time in the forward pass: their sums share a
+// barrier, their words the gains in registers (65536 x 2048 bf16, two words a
+// thread: 88 us, 95 one row at a time; three and more words leave no registers
+// for a second row: 16384 x 6144 70 us, 72 with two).
+__host__ __device__ constexpr int rows_at_once(int nv) { return nv >= 3 ? 1 : 2; }
 
 // 1 / sqrt(v) to float32's last bit or so: the hardware's approximation and
 // one step of Newton's method (0 and infinity pass through).
@@ -173,24 +175,37 @@ template <typename T, int NV, bool EDGE>
 struct Words {
   static constexpr int N = 16 / sizeof(T);
   int i0, n, words, shift, C;
+  uint32_t part = 0;  // bit j: word j holds other rows' elements too
   __device__ __forceinline__ Words(const T* row, int C_, int i0_, int n_) : i0(i0_), n(n_), C(C_) {
     shift = EDGE ? static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15) / static_cast<int>(sizeof(T)) : 0;
     words = (shift + C + N - 1) / N;
+    if (EDGE)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (has(j) && (channel(j, 0) < 0 || channel(j, N - 1) >= C)) part |= 1u << j;
   }
   __device__ __forceinline__ bool has(int j) const { return i0 + j * n < words; }
   __device__ __forceinline__ int channel(int j, int u) const { return (i0 + j * n) * N - shift + u; }
   __device__ __forceinline__ bool in(int j, int u) const {
     return EDGE ? static_cast<unsigned>(channel(j, u)) < static_cast<unsigned>(C) : has(j);
   }
-  __device__ __forceinline__ bool whole(int j) const { return !EDGE || (channel(j, 0) >= 0 && channel(j, N - 1) < C); }
-  // values of word j in pairs, zero outside the row
+  __device__ __forceinline__ bool whole(int j) const { return !EDGE || !((part >> j) & 1); }
+  // zeroes what is not of the row in the thread's words of a ring slot (the other rows' elements may be NaN)
+  __device__ __forceinline__ void clean(uint4* slot) const {
+    if (!EDGE || part == 0) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (!whole(j)) {
+        T* e = reinterpret_cast<T*>(slot + j * blockDim.x);
+        for (int u = 0; u < N; ++u)
+          if (!in(j, u)) e[u] = static_cast<T>(0.f);
+      }
+  }
+  // values of word j in pairs
   __device__ __forceinline__ void values(const uint4* slot, int j, uint64_t* v) const {
     const uint4 w = slot[j * blockDim.x];
     float f[N];
     unpack<T, N>(w, f);
-    if (!whole(j))
-#pragma unroll
-      for (int u = 0; u < N; ++u) f[u] = in(j, u) ? f[u] : 0.f;
 #pragma unroll
     for (int u = 0; u < N / 2; ++u) v[u] = f2(f[2 * u], f[2 * u + 1]);
   }
@@ -264,13 +279,19 @@ struct Share {
 };
 
 // Blocks an SM that a kernel's registers are to allow: gains, biases and the row (column sums) of NV words.
-__host__ __device__ constexpr int min_blocks(int nv, int maxt, bool bwd) {
-  return maxt <= 256 ? (nv == 1 ? (bwd ? 3 : 4) : 2) : (maxt <= 384 ? 2 : 1);
+__host__ __device__ constexpr int min_blocks(int nv, int maxt, bool bwd, bool edge) {
+  if (maxt <= 128) return nv <= 2 ? 4 : 3;
+  if (maxt <= 256) return nv == 1 ? (bwd ? 3 : 4) - edge : nv <= 3 || !edge ? 2 : 1;
+  return 1;
 }
 
 // y = (x - mean) rstd g + b, and the row's mean and rstd.  TPR threads a row (0: the block, of at most MAXT).
+// Bound by HBM where rows lie on 16 bytes: x is read and y written once, the row stays in registers between its two
+// sums.  bf16: 2^17 x 1024 88 us, 65536 x 2048 87, 16384 x 6144 74 (94, 94 and 83 % of the copy rate); 24576 x 512
+// 11.5 us (67 %: filling and emptying the rings).  With EDGE about half of that (16384 x 6143 144 us): the words at a
+// row's ends hold up the block at its barriers, and registers leave fewer warps.
 template <typename T, int NV, int TPR, bool EDGE, int MAXT>
-__global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, false))
+__global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, false, EDGE))
     norm_fwd_kernel(const T* x, long long ldx, const float* __restrict__ g, const float* __restrict__ b, T* y,
                     long long ldy, float* mean_out, float* rstd_out, long long M, int C, float eps) {
   constexpr int N = 16 / sizeof(T);
@@ -315,6 +336,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, false))
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       uint64_t sum = 0;
+      if (i + k < sh.mine) ws.clean(ring + at * slot_words + k * row_words);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if (i + k < sh.mine && ws.has(j)) ws.values(ring + at * slot_words + k * row_words, j, f[k] + j * H);
@@ -338,12 +360,19 @@ __global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, false))
         for (int u = 0; u < H; ++u) {
           uint64_t& v = f[k][j * H + u];
           v = f2_add(v, neg);
-          if (EDGE || !ws.has(j)) {  // outside the row there is no deviation
-            const float2 t = f2_get(v);
-            v = f2(ws.in(j, 2 * u) ? t.x : 0.f, ws.in(j, 2 * u + 1) ? t.y : 0.f);
-          }
-          sum = f2_fma(v, v, sum);
+          if (!ws.has(j)) v = 0;  // outside the row there is no deviation
         }
+      if (EDGE && ws.part != 0)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (!ws.whole(j))
+#pragma unroll
+            for (int u = 0; u < H; ++u) {
+              const float2 t = f2_get(f[k][j * H + u]);
+              f[k][j * H + u] = f2(ws.in(j, 2 * u) ? t.x : 0.f, ws.in(j, 2 * u + 1) ? t.y : 0.f);
+            }
+#pragma unroll
+      for (int c = 0; c < NV * H; ++c) sum = f2_fma(f[k][c], f[k][c], sum);
       q[k] = f2_sum(sum);
     }
     row_sums<TPR>(q, slots, turn);
@@ -400,19 +429,23 @@ __global__ void __launch_bounds__(512)
 }
 
 // Rows in flight of the backward kernel (x and dy; four words a thread fill shared memory with two).
-__host__ __device__ constexpr int bwd_depth(int nv) { return nv >= 4 ? 2 : 4; }
+__host__ __device__ constexpr int bwd_depth(int nv, int maxt) { return nv >= 4 ? (maxt <= 256 ? 3 : 2) : 4; }
 
 // dx per row, and this block's sums of dy xh and dy per channel into
 // part[blockIdx.x][2][C].
 // x and dy are read from the ring twice, before and after the row's two sums,
-// so that only the gains and the column sums stay in registers.
+// so that only the gains and the column sums stay in registers.  Bound by HBM and,
+// next to it, by the issue of its instructions (about 25 an element pair): bf16
+// 2^18 x 512 129 us, 65536 x 2048 142, 16384 x 6144 119 (96, 87 and 77 % of the
+// copy rate), float32 16384 x 4096 132 (93 %); with EDGE 16384 x 6143 203 us.
+// EDGE in place of the exact variant, measured on one state of both: 262144 x 512 217 us for 133.
 template <typename T, int NV, int TPR, bool EDGE, int MAXT>
-__global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, true))
+__global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, true, EDGE))
     norm_bwd_kernel(const T* x, long long ldx, const float* __restrict__ g, const T* dy, long long lddy,
                     const float* __restrict__ mean_in, const float* __restrict__ rstd_in, T* dx, long long lddx,
                     float* part, long long M, int C) {
   constexpr int N = 16 / sizeof(T);
-  constexpr int kRing = bwd_depth(NV);
+  constexpr int kRing = bwd_depth(NV, MAXT);
   extern __shared__ uint4 ring_[];  // [kRing][rows at once][x, dy][NV][threads]; then the row groups' sums [groups][2][C]
   __shared__ __align__(16) float slots[256];
   pdl_trigger();
@@ -421,7 +454,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, true))
   const Words<T, NV, EDGE> ws(x + sh.first * ldx, C, sh.i0, sh.n);
   Feed<T, NV, EDGE> xs(x, ldx, M, sh.first, sh.step, ws), ds(dy, lddy, M, sh.first, sh.step, ws);
   uint4* ring = ring_ + threadIdx.x;
-  constexpr int R = 1;  // (two at a time: the ring leaves room for one block an SM, 16384 x 6144 bf16 192 us for 158)
+  constexpr int R = 1;  // (two at a time: the ring leaves room for one block an SM, 192 us for 158 when that was measured)
   const int row_words = NV * blockDim.x, slot_words = 2 * R * row_words;
   float m_next[kRing - 1][R], r_next[kRing - 1][R];  // statistics of the rows in flight
   const float *pm = mean_in + sh.first, *pr = rstd_in + sh.first;
@@ -471,7 +504,10 @@ __global__ void __launch_bounds__(MAXT, min_blocks(NV, MAXT, true))
     }
     request(ring + (at == 0 ? kRing - 1 : at - 1) * slot_words, m_next[kRing - 2], r_next[kRing - 2]);
     cp_wait<kRing - 1>();
-    const uint4* xw = ring + at * slot_words;
+    uint4* xw = ring + at * slot_words;
+#pragma unroll
+    for (int k = 0; k < 2 * R; ++k)
+      if (i + k / 2 < sh.mine) ws.clean(xw + k * row_words);
     float s[2 * R];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
@@ -606,7 +642,9 @@ __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* part, i
 
 // --------------------------------------------------------------- clipping
 constexpr int kTensors = 120;   // tensors a launch (their table is a kernel argument)
-constexpr int kClipBlocks = 592;
+// Three blocks an SM are what the kernels' registers allow, and one wave of them shares the chunks evenly (352 M bf16
+// elements, norm and clip: 106 and 351 us; 592 blocks 127 and 367, 296 blocks 110 and 386).
+constexpr int kClipBlocks = 444;
 
 struct ClipTensor {
   const void* g;
@@ -825,27 +863,47 @@ int esize(int dtype) { return dtype == SB_FP32 ? 4 : 2; }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// go(words a thread, threads a row, EDGE, block's threads at most) for a row of `words` words; -1 above the widest.
-// Narrow rows share a warp; up to 64 words a warp takes a row, above that a block: with 384 threads two blocks of it
-// fit an SM, which hides the row's barriers (16384 x 6144 bf16 backward: one block of 512 threads 273 us).
-template <typename T, typename F, typename E>
+// go(words a thread, threads a row, EDGE, block's threads at most) for a row of
+// `words` words; -1 above the widest.  Narrow rows share a warp, up to 96 words
+// a warp takes a row, above that a block of 128 to 512 threads.  Measured (bf16,
+// forward and backward, the other side in brackets):
+//   2^20 x 64, 8 lanes a row: 49 and 77 us [a warp a row: 190 and 293];
+//   2^18 x 512, a warp a row: 99 and 129 us [a block: 115 and 253];
+//   2^17 x 768, a warp, three words a thread: 75 and 102 us [a block: 87 and 135; with EDGE the backward spills
+//   there: 349 us, 216 in a block];
+//   65536 x 2048, 128 threads of two words: 88 and 142 us [256 of one: 120 and 189];
+//   16384 x 6144, 256 threads of three words: 70 and 119 us [384 of two: 87 and 143];
+//   32768 x 4095 (EDGE), forward 192 threads of three words: 172 us [512 of two: 247], backward the other way: 318 [410];
+//   16384 x 8192, forward 256 threads of four words: 86 us [512 of two: 120], backward the other way: 170 [177].
+// A row's sums cost a thread the same whatever its words, so more words a
+// thread are better until their registers leave too few warps.
+template <bool BWD, typename F, typename E>
 int by_width(int words, F&& go, E edge) {
   using std::integral_constant;
   using I1 = integral_constant<int, 1>;
   using I2 = integral_constant<int, 2>;
+  using I3 = integral_constant<int, 3>;
+  using I4 = integral_constant<int, 4>;
   using Warp = integral_constant<int, 32>;
   using Block = integral_constant<int, 0>;
+  using T128 = integral_constant<int, 128>;
   using T256 = integral_constant<int, 256>;
-  using T384 = integral_constant<int, 384>;
   using T512 = integral_constant<int, 512>;
   if (words <= 8) return go(I1{}, integral_constant<int, 8>{}, edge, T256{});
   if (words <= 16) return go(I1{}, integral_constant<int, 16>{}, edge, T256{});
   if (words <= 32) return go(I1{}, Warp{}, edge, T256{});
   if (words <= 64) return go(I2{}, Warp{}, edge, T256{});
-  if (words <= 256) return go(I1{}, Block{}, edge, T256{});
-  if (words <= 768) return go(I2{}, Block{}, edge, T384{});
+  if constexpr (!BWD || !E::value)
+    if (words <= 96) return go(I3{}, Warp{}, edge, T256{});
+  if (words <= 256) return go(I2{}, Block{}, edge, T128{});
+  if (words <= 384) return go(I3{}, Block{}, edge, T128{});
+  if (words <= 512) return go(I2{}, Block{}, edge, T256{});
+  if constexpr (!BWD || !E::value)
+    if (words <= 768) return go(I3{}, Block{}, edge, T256{});
+  if constexpr (!BWD && !E::value)
+    if (words <= 1024) return go(I4{}, Block{}, edge, T256{});
   if (words <= 1024) return go(I2{}, Block{}, edge, T512{});
-  if (words <= 2048) return go(integral_constant<int, 4>{}, Block{}, edge, T512{});
+  if (words <= 2048) return go(I4{}, Block{}, edge, T512{});
   return -1;
 }
 
@@ -854,7 +912,7 @@ bool alike(const void* a, int64_t lda, const void* b, int64_t ldb, int es) {
   return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0 && ((lda - ldb) * es) % 16 == 0;
 }
 
-constexpr int kParts = 592;  // blocks of a backward launch, at most
+constexpr int kParts = 1184;  // blocks of a backward launch, at most
 
 // The words of a row, at most (it may begin anywhere in its first one).
 int words_of(const void* p, int64_t ld, int C, int es) {
@@ -901,7 +959,7 @@ int sparse_block_layer_norm_fwd(const void* x, int64_t ldx, const float* g, cons
       return launched();
     };
     if (same) {
-      const int st = edge ? by_width<T>(words, go, std::true_type{}) : by_width<T>(words, go, std::false_type{});
+      const int st = edge ? by_width<false>(words, go, std::true_type{}) : by_width<false>(words, go, std::false_type{});
       if (st >= 0) return st;
     }
     const int grid = static_cast<int>(std::min<long long>(M, static_cast<long long>(n_sm) * 4));
@@ -946,7 +1004,7 @@ int sparse_block_layer_norm_bwd(const void* x, int64_t ldx, const float* g, cons
         const int threads = TPR ? 256 : (words + 32 * NV - 1) / (32 * NV) * 32;
         const int rows = TPR ? 256 / (TPR ? TPR : 1) : 1;
         // the ring, and in its place afterwards the row groups' sums of up to NV TPR words
-        const size_t ring = 2 * static_cast<size_t>(bwd_depth(NV)) * NV * threads * 16;
+        const size_t ring = 2 * static_cast<size_t>(bwd_depth(NV, maxt.value)) * NV * threads * 16;
         const size_t sums = TPR ? static_cast<size_t>(rows) * 2 * (NV * TPR * 16 / sizeof(T)) * sizeof(float) : 0;
         const size_t smem = std::max(ring, sums);
         const int per = resident<K>(dev, threads, smem);
@@ -958,8 +1016,8 @@ int sparse_block_layer_norm_bwd(const void* x, int64_t ldx, const float* g, cons
                                    static_cast<T*>(dx), lddx, part, M, C);
         return launched();
       };
-      if (same && (sizeof(T) == 4 || words <= 1024)) {
-        const int r = edge ? by_width<T>(words, go, std::true_type{}) : by_width<T>(words, go, std::false_type{});
+      if (same) {
+        const int r = edge ? by_width<true>(words, go, std::true_type{}) : by_width<true>(words, go, std::false_type{});
         if (r >= 0) return r;
       }
       constexpr auto K = norm_bwd_wide_kernel<T>;

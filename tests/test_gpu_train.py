@@ -106,6 +106,21 @@ def test_layer_norm(cuda_device, sb, M, C, pad, dtype):
     assert none is None and torch.equal(dx, dx2) and torch.equal(dg, dg2)
 
 
+@pytest.mark.parametrize("M,C,pad", [(4000, 768, 0), (4000, 765, 0), (3600, 1000, 1), (2500, 2968, 8), (2500, 2967, 2),
+                                     (1200, 4095, 1), (1100, 6144, 0), (1100, 6143, 1), (700, 8192, 0), (500, 9000, 3)])
+def test_many_wide_rows(cuda_device, sb, M, C, pad):
+    # several rows a block, so that the rings go round; what lies between the rows is NaN.  A column's sum runs over at
+    # most 27 rows of a block, then 37 blocks' sums of a group and the 32 groups: under check_bwd's 128 roundings.
+    x, dy, g, b = draw(M, C, torch.bfloat16, pad, cuda_device)
+    if pad:
+        for t in (x, dy):
+            t.as_strided((M, pad), (C + pad, 1), t.storage_offset() + C).fill_(float("nan"))
+    y, mean, rstd = sb.layer_norm(x, g, b)
+    check_fwd(x, g, b, y, mean, rstd)
+    out = sb.layer_norm_backward(x, g, dy, mean, rstd)
+    check_bwd(x, g, dy, mean, rstd, *out)
+
+
 @pytest.mark.parametrize("M,C", [(20000, 64), (9001, 512), (5000, 1001), (3000, 2048)])
 def test_many_rows(cuda_device, sb, M, C):
     x, dy, g, b = draw(M, C, torch.bfloat16, 0, cuda_device)
