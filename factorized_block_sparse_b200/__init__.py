@@ -15,7 +15,12 @@ Use::
     o, lse = sa.forward(q, k, v, lay)                        # bf16 [B, H, N, D]
     dq, dk, dv = sa.backward(q, k, v, o, lse, dO, lay)
 
-``python -m factorized_block_sparse_b200.build`` compiles the library in
+``sparse_block`` is the Sparse Transformer block around the op, with layer
+norm, the norm of all gradients and their clipping as calls of their own;
+``packed_attn`` is causal attention over packed sequences of different
+lengths with grouped K/V heads, forward and backward.
+
+``python -m factorized_block_sparse_b200.build`` compiles the libraries in
 place (nvcc, sm_100a).
 
 Submodules are imported on demand (``from factorized_block_sparse_b200
@@ -25,4 +30,4 @@ compute call fails loudly when the library is missing; there is no CPU
 fallback.
 """
 
-__all__ = ["sparse_attn", "synth", "build"]
+__all__ = ["sparse_attn", "sparse_block", "packed_attn", "synth", "build"]

@@ -1,7 +1,8 @@
-"""Builds the in-tree shared library ``libsparse_attn.so`` for sm_100a.
+"""Builds the in-tree shared libraries for sm_100a: ``libsparse_attn.so``, its
+test build, ``libsparse_block.so`` and ``libpacked_attn.so``.
 
-One nvcc invocation compiles the CUDA translation unit (kernels and C ABI)
-and the host layout builder.  The CUDA runtime is linked statically and the
+For each, one nvcc invocation compiles the CUDA translation units (kernels and
+C ABI) and the host layout builder.  The CUDA runtime is linked statically and the
 driver is reached through ``cudaGetDriverEntryPoint``, so the library loads
 on a host without a GPU (for the CPU tests of the layout builder and the
 exported symbols) and needs only the NVIDIA driver on a GPU host.
@@ -98,7 +99,8 @@ def build_block_lib(force=False, verbose=False):
 PACKED_LIB = os.path.join(HERE, "libpacked_attn.so")
 PACKED_SOURCES = [os.path.join(HERE, "csrc", f) for f in ("pa_api.cu", "pa_layout.cpp")]
 PACKED_HEADERS = [os.path.join(ROOT, "include", f) for f in ("packed_attn.h", "sparse_attn.h")] + [
-    os.path.join(HERE, "csrc", f) for f in ("pa_internal.h", "pa_device.cuh", "pa_fwd.cuh", "pa_bwd.cuh", "sa_device.cuh", "sa_internal.h")]
+    os.path.join(HERE, "csrc", f) for f in ("pa_internal.h", "pa_device.cuh", "pa_fwd.cuh", "pa_bwd.cuh", "sa_device.cuh",
+                                            "sa_internal.h")]
 
 
 def build_packed_lib(force=False, verbose=False, extra=()):
