@@ -36,12 +36,18 @@
 // shared memory): it is bound by the softmax, and two warps a scheduler do not
 // hide its latencies (2 x 12288 rows, 8 heads of 64: 389 us, 417 with NH = 1).
 // D = 128 takes NH = 1: there the exchange only lengthens the chain S ->
-// softmax -> PV (ten ragged sequences, 32 / 8 heads: 426 us, 466 with NH = 2).
+// softmax -> PV (ten ragged sequences, 32 / 8 heads: 426 us, 466 with NH = 2;
+// 415 since PV begins with the first quarter of P).
 #pragma once
 
 #include "pa_device.cuh"
 
 namespace pa {
+
+// D = 128: k-steps of PV that are issued as soon as the first 32 keys' P is there, while the softmax goes on with the
+// others: the product's end, which the unit's next step waits for, comes earlier (one sequence of 8192, 16 / 2 heads:
+// 217 us; all at once 223, in halves 218 to 222, three quarters first 226).
+constexpr int kEarly = 2;
 
 enum Pairing : int { kSingle = 0, kHeads = 1, kTiles = 2 };
 
@@ -70,7 +76,7 @@ struct FwdCfg {
   static constexpr int OFF_STG = OFF_KV + STAGES * G::BYTES;
   static constexpr int OFF_RED = OFF_STG + SOFT_WARPS * STG_BYTES;  // [2 tiles in turn][2 units][2 halves][128 rows]
   static constexpr int OFF_BAR = OFF_RED + (NH - 1) * 8 * kTile * 4;
-  static constexpr int N_BARS = 2 + 2 + 2 * STAGES + 2 * 5 + 2;
+  static constexpr int N_BARS = 2 + 2 + 2 * STAGES + 2 * 6 + 2;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
   static constexpr int SMEM = OFF_MISC + 16;
   static constexpr bool SEP = D <= 64;  // P in columns of its own
@@ -137,7 +143,8 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
   uint64_t* bar_p_full = bar_s_free + 2;              // [2] P of a tile
   uint64_t* bar_pv_done = bar_p_full + 2;             // [2] PV of a tile
   uint64_t* bar_o_free = bar_pv_done + 2;             // [2] the epilogue has read O
-  uint64_t* bar_drain = bar_o_free + 2;               // [2]
+  uint64_t* bar_p_early = bar_o_free + 2;             // [2] the first 32 keys' P (not SEP)
+  uint64_t* bar_drain = bar_p_early + 2;              // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
 
@@ -150,6 +157,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       mbar_init(bar_s_full + u, 1);
       mbar_init(bar_s_free + u, 4 * C::NH);
       mbar_init(bar_p_full + u, 4 * C::NH);
+      mbar_init(bar_p_early + u, 4 * C::NH);
       mbar_init(bar_pv_done + u, 1);
       mbar_init(bar_o_free + u, 4 * C::NH);
       mbar_init(bar_drain + u, 1);
@@ -221,16 +229,17 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       }
       __syncwarp();
     };
-    // O of unit u, from the V tile at ring position r; keys behind the sequence's last are zeroed in it
-    auto issue_pv = [&](int u, int r, bool first) {
+    // k-steps k0 .. k1 - 1 of O of unit u, from the V tile at ring position r; keys behind the sequence's last are zeroed in it
+    auto issue_pv = [&](int u, int r, bool first, int k0, int k1) {
       const Desc v_mn = G::mnmajor(smem_u32(sKV) + r % C::STAGES * G::BYTES);
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_bf16_ts(tmem + C::COL_O + u * D, tmem + C::COL_P + u * C::P_STRIDE + kk * 8, v_mn.at(G::mnstep(kk)), id_o,
-                      (!first || kk > 0));
-        mma_commit(bar_pv_done + u);
+          if (kk >= k0 && kk < k1)
+            mma_bf16_ts(tmem + C::COL_O + u * D, tmem + C::COL_P + u * C::P_STRIDE + kk * 8, v_mn.at(G::mnstep(kk)), id_o,
+                        (!first || kk > 0));
+        if (k1 == kTile / 16) mma_commit(bar_pv_done + u);
       }
       __syncwarp();
     };
@@ -279,7 +288,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
                  (j > 0 || ni == 0 || mbar_wait_warp(bar_o_free + u, (ni - 1) & 1, abort_flag));
             if (!ok) break;
             ++np;
-            issue_pv(u, ring + 1, j == 0);
+            issue_pv(u, ring + 1, j == 0, 0, kTile / 16);
             commit(bar_kv_free + sv);
           } else {
             ok = skip(ring + 1);
@@ -316,11 +325,13 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
           for (int u = 0; u < 2; ++u) {
             const int nu = u ? n1 : n0;
             if (!ok || j >= nu) continue;
-            ok = mbar_wait_warp(bar_p_full + u, np[u] & 1, abort_flag) &&
+            ok = mbar_wait_warp(bar_p_early + u, np[u] & 1, abort_flag) &&
                  (j > 0 || ni[u] == 0 || mbar_wait_warp(bar_o_free + u, (ni[u] - 1) & 1, abort_flag));
             if (!ok) break;
+            issue_pv(u, ring + 1, j == 0, 0, kEarly);
+            if (!(ok = mbar_wait_warp(bar_p_full + u, np[u] & 1, abort_flag))) break;
             ++np[u];
-            issue_pv(u, ring + 1, j == 0);
+            issue_pv(u, ring + 1, j == 0, kEarly, kTile / 16);
             if (j + 1 < nu) {
               issue_s(u, ring + 2);
               if (j + 2 == nu) commit(bar_q_free + u);
@@ -429,6 +440,11 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
           }
           tmem_st8(t_p + c * 16, pk);
           tmem_st8(t_p + c * 16 + 8, pk + 8);
+          if (!C::SEP && c == 0) {  // the product with the first 32 keys can begin
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(bar_p_early + u, lane);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
