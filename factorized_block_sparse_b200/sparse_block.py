@@ -271,7 +271,14 @@ _CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 def _clip(grads, max_norm, out, stream):
     in_place = out is grads
-    grads = list(grads.values()) if isinstance(grads, dict) else list(grads)
+    if isinstance(grads, dict):
+        if isinstance(out, dict) and not in_place:  # by name: the two may be in different orders
+            if out.keys() != grads.keys():
+                raise ValueError("the outputs must have the gradients' names")
+            out = [out[n] for n in grads]
+        grads = list(grads.values())
+    else:
+        grads = list(grads)
     outs = grads if in_place else None if out is None else list(out.values()) if isinstance(out, dict) else list(out)
     if not grads:
         raise ValueError("expected at least one gradient")
@@ -298,14 +305,14 @@ def _clip(grads, max_norm, out, stream):
     gp = array("Q", [t.data_ptr() for t in grads])
     op = None if outs is None else gp if in_place else array("Q", [t.data_ptr() for t in outs])
     counts, types = array("Q", [t.numel() for t in grads]), array("i", codes)
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    ws = torch.empty(CLIP_WORKSPACE, dtype=torch.uint8, device=dev)
+    buf = torch.empty(64 + CLIP_WORKSPACE // 4, dtype=torch.float32, device=dev)  # the norm, and 256 bytes behind it the workspace
+    at = buf.data_ptr()
     st = lib.sparse_block_clip_grads(len(grads), gp.buffer_info()[0], None if op is None else op.buffer_info()[0],
-                                     counts.buffer_info()[0], types.buffer_info()[0], float(max_norm), norm.data_ptr(),
-                                     ws.data_ptr(), CLIP_WORKSPACE, _raw_stream(index))
+                                     counts.buffer_info()[0], types.buffer_info()[0], float(max_norm), at, at + 256,
+                                     CLIP_WORKSPACE, _raw_stream(index))
     if st:
         raise sa.SparseAttnError(st, "sparse_block_clip_grads")
-    return norm
+    return buf[0]
 
 
 CLIP_WORKSPACE = int(lib.sparse_block_clip_workspace_size())

@@ -84,7 +84,7 @@ def draw(M, C, dtype, pad, device, seed=0):
     return x, dy, g, b
 
 
-# every width path: a warp or a block a row, one to twelve words a thread, odd widths, widths read again per pass
+# every width path: a warp or a block a row, one to four words a thread, odd widths, widths read again per pass
 SHAPES = [(1, 1, 0), (3, 2, 0), (5, 31, 0), (7, 33, 3), (1, 64, 0), (9, 100, 4), (130, 128, 0), (33, 136, 8), (64, 255, 0),
           (300, 256, 0), (17, 512, 0), (40, 520, 24), (3, 1001, 0), (50, 1024, 0), (21, 1032, 0), (11, 2048, 0),
           (6, 2047, 1), (9, 2049, 0), (5, 4096, 0), (4, 4104, 16), (3, 6143, 0), (7, 6144, 0), (2, 6145, 0), (5, 8192, 0),
@@ -281,6 +281,18 @@ def test_clip_misaligned_and_shaped(cuda_device, sb):
 def test_clip_sums_do_not_overflow_or_vanish(cuda_device, sb, scale):
     grads = [t * scale for t in grads_of([1000, 4096, 50], [torch.float32, torch.bfloat16], cuda_device)]
     check_clip(sb, grads, scale)
+
+
+def test_clip_outputs_by_name(cuda_device, sb):
+    # dicts whose names come in different orders, of one shape
+    a, b = grads_of([300, 300], [torch.float32], cuda_device)
+    out = {"b": torch.empty_like(b), "a": torch.empty_like(a)}
+    norm = sb.clip_grads({"a": a, "b": b}, 0.5, out=out)
+    same = [torch.empty_like(a), torch.empty_like(b)]
+    assert torch.equal(norm, sb.clip_grads([a, b], 0.5, out=same))
+    assert torch.equal(out["a"], same[0]) and torch.equal(out["b"], same[1])
+    with pytest.raises(ValueError):
+        sb.clip_grads({"a": a, "b": b}, 0.5, out={"a": same[0], "c": same[1]})
 
 
 def test_clip_values_that_are_not_finite(cuda_device, sb):
