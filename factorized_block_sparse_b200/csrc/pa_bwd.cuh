@@ -33,15 +33,15 @@
 // rate 1.3 PFLOP/s on one sequence of 32768, at about 1.5 GHz).  D <= 64: the
 // exponentials (16 a clock and SM, twice a score) and the arithmetic and waits
 // around them, 2.0 us a tile pair against 0.7 us of products (tensor pipe 46 %,
-// exponential unit 47 %, issue slots 52 % busy: the phases of a step follow one
-// another in all compute warps at once).  Measured there
-// and not kept: the step in two halves of 64 columns with barriers of their
+// exponential unit 47 %, issue slots 52 % busy).  Measured there and not kept:
+// the step in two halves of 64 columns with barriers of their
 // own (text shape 1.02 -> 1.50 ms: twice the waits of the issuing thread), a
 // second issuing warp (no change), 64 columns a compute thread (dK/dV part 597
-// -> 679 us), dQ's steps in turn by two halves of the warps (1.03 -> 1.09 ms),
-// the groups' exponentials one group after another (1.03 -> 1.11 ms).  Times: 2 x 12288 rows, 8 heads of 64, 1.02 ms; ten ragged
-// sequences of 16384 rows, 32 / 8 heads of 128, 1.44 ms; one of 32768, 16 / 2
-// heads of 128, 12.0 ms.
+// -> 679 us), dQ's steps in turn by two halves of the warps (1.04 -> 1.07 ms),
+// the exponentials of two groups after those of the other two (1.04 -> 1.07
+// ms).  Times: 2 x 12288 rows, 8 heads of 64, 1.04 ms; ten ragged sequences of
+// 16384 rows, 32 / 8 heads of 128, 1.43 ms; one of 32768, 16 / 2 heads of 128,
+// 12.0 ms.
 //
 // Roles of both parts: compute groups of four warps (thread = row of the tile,
 // kCols columns of the step each), four warps for the read-out of an item's
