@@ -39,7 +39,7 @@
 // second issuing warp (no change), 64 columns a compute thread (dK/dV part 597
 // -> 679 us), dQ's steps in turn by two halves of the warps (1.04 -> 1.07 ms),
 // the exponentials of two groups after those of the other two (1.04 -> 1.07
-// ms).  Times: 2 x 12288 rows, 8 heads of 64, 1.04 ms; ten ragged sequences of
+// ms).  Times: 2 x 12288 rows, 8 heads of 64, 1.02 ms; ten ragged sequences of
 // 16384 rows, 32 / 8 heads of 128, 1.43 ms; one of 32768, 16 / 2 heads of 128,
 // 12.0 ms.
 //
@@ -62,6 +62,11 @@ template <int D>
 constexpr int kDkvPoly = D <= 64 ? 1 : 3;
 template <int D>
 constexpr int kDqPoly = D <= 64 ? 1 : 0;
+// Whether the issuing warp waits for the next tiles before it waits for a
+// step's weights, so that no other wait stands between them and their products
+// (D = 64, text shape: 1013 us, 1033 without; D = 128, ragged: 1434 and 1409 us).
+template <int D>
+constexpr bool kTilesAhead = D <= 64;
 // Columns of the step that a compute thread takes.
 constexpr int kCols = 32;
 constexpr int kBwdComputeWarps = 4 * 128 / kCols, kBwdThreads = 32 * (kBwdComputeWarps + 6);
@@ -382,8 +387,9 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
       }
       int rows_s = keys - skip * kTile, left_s = it.per - skip, rows_p = rows_s, left_p = left_s;  // of the next query tile
       // S^T (dP^T) of the item's next step; a last, partial query tile is zeroed behind its rows first
-      auto issue_s = [&]() -> bool {
-        if (!mbar_wait_warp(bar.q_full + iq.st, iq.ph, abort_flag)) return false;
+      auto has_q = [&]() { return mbar_wait_warp(bar.q_full + iq.st, iq.ph, abort_flag); };
+      auto has_do = [&]() { return mbar_wait_warp(bar.do_full + io.st, io.ph, abort_flag); };
+      auto issue_s = [&]() {
         uint8_t* sQ = smem + C::OFF_Q + iq.st * G::BYTES;
         if (rows_s < kTile) zero_rows<D>(sQ, rows_s, lane);
         rows_s -= kTile;
@@ -399,10 +405,8 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
         __syncwarp();
         iq.next();
         is.next();
-        return true;
       };
-      auto issue_dp = [&]() -> bool {
-        if (!mbar_wait_warp(bar.do_full + io.st, io.ph, abort_flag)) return false;
+      auto issue_dp = [&]() {
         uint8_t* sDO = smem + C::OFF_DO + io.st * G::BYTES;
         if (rows_p < kTile) zero_rows<D>(sDO, rows_p, lane);
         rows_p -= kTile;
@@ -417,11 +421,18 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
         }
         __syncwarp();
         io.next();
-        return true;
       };
-      ok = issue_s() && issue_dp() && (C::NS == 1 || it.n == 1 || issue_s());
+      if (!(ok = has_q())) break;
+      issue_s();
+      if (!(ok = has_do())) break;
+      issue_dp();
+      if (C::NS > 1 && it.n > 1) {
+        if (!(ok = has_q())) break;
+        issue_s();
+      }
       for (int j = 0; ok && j < it.n; ++j) {
-        ok = mbar_wait_warp(bar.p_full, ph, abort_flag);
+        if (kTilesAhead<D>) ok = (j + C::NS >= it.n || has_q()) && (j + 1 >= it.n || has_do());
+        ok = ok && mbar_wait_warp(bar.p_full, ph, abort_flag);
         if (ok && j == 0 && ni > 0) ok = mbar_wait_warp(bar.out_free, (ni - 1) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -434,9 +445,15 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
           mma_commit(bar.do_free + ro.st);
         }
         __syncwarp();
-        if (!C::DS_IN_S && j + 1 < it.n && !(ok = issue_s())) break;  // over P^T, behind its product
+        if (!C::DS_IN_S && j + 1 < it.n) {  // over P^T, behind its product
+          if (!kTilesAhead<D> && !(ok = has_q())) break;
+          issue_s();
+        }
         if (!(ok = mbar_wait_warp(bar.ds_full, ph, abort_flag))) break;
-        if (C::DS_IN_S && j + 1 < it.n && !(ok = issue_dp())) break;
+        if (C::DS_IN_S && j + 1 < it.n) {
+          if (!kTilesAhead<D> && !(ok = has_do())) break;
+          issue_dp();
+        }
         tc_fence_after();
         const Desc q_mn = G::mnmajor(smem_u32(smem + C::OFF_Q) + rq.st * G::BYTES);
         const uint32_t t_ds = tmem + (C::DS_IN_S ? rs.st * 128 + kCols / 2 : C::COL_DP);
@@ -452,10 +469,13 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
         ro.next();
         rs.next();
         ph ^= 1;
-        if (C::DS_IN_S) {
-          if (j + 2 < it.n) ok = issue_s();  // over P^T and dS^T, behind their products
-        } else if (j + 1 < it.n) {
-          ok = issue_dp();  // over dS^T, behind its product
+        if (C::DS_IN_S && j + 2 < it.n) {  // over P^T and dS^T, behind their products
+          if (!kTilesAhead<D> && !(ok = has_q())) break;
+          issue_s();
+        }
+        if (!C::DS_IN_S && j + 1 < it.n) {  // over dS^T, behind its product
+          if (!kTilesAhead<D> && !(ok = has_do())) break;
+          issue_dp();
         }
       }
       if (ok && elect_one()) {
@@ -706,9 +726,10 @@ __device__ __forceinline__ void dq_part(uint8_t* smem, const uint32_t tmem, int*
       if (!ok) break;
       const Desc q_k = G::kmajor(smem_u32(smem + C::OFF_Q) + qb * G::BYTES);
       const Desc do_k = G::kmajor(smem_u32(smem + C::OFF_DO) + qb * G::BYTES);
-      auto issue_s = [&](int j) -> bool {
+      auto has_k = [&]() { return mbar_wait_warp(bar.k_full + ik.st, ik.ph, abort_flag); };
+      auto has_v = [&]() { return mbar_wait_warp(bar.v_full + iv.st, iv.ph, abort_flag); };
+      auto issue_s = [&](int j) {
         const int st = ik.st;
-        if (!mbar_wait_warp(bar.k_full + st, ik.ph, abort_flag)) return false;
         // keys behind the sequence's last: masked in S, but dS = 0 must not meet a NaN in dS K
         if (s.len - j * kTile < kTile) zero_rows<D>(smem + C::OFF_K + st * G::BYTES, s.len - j * kTile, lane);
         tc_fence_after();
@@ -722,11 +743,9 @@ __device__ __forceinline__ void dq_part(uint8_t* smem, const uint32_t tmem, int*
         __syncwarp();
         ik.next();
         is.next();
-        return true;
       };
-      auto issue_dp = [&]() -> bool {
+      auto issue_dp = [&]() {
         const int st = iv.st;
-        if (!mbar_wait_warp(bar.v_full + st, iv.ph, abort_flag)) return false;
         tc_fence_after();
         const Desc v_k = G::kmajor(smem_u32(smem + C::OFF_V) + st * G::BYTES);
         if (elect_one()) {
@@ -738,15 +757,25 @@ __device__ __forceinline__ void dq_part(uint8_t* smem, const uint32_t tmem, int*
         }
         __syncwarp();
         iv.next();
-        return true;
       };
-      ok = issue_s(0) && issue_dp() && (n == 1 || issue_s(1));
+      if (!(ok = has_k())) break;
+      issue_s(0);
+      if (!(ok = has_v())) break;
+      issue_dp();
+      if (n > 1) {
+        if (!(ok = has_k())) break;
+        issue_s(1);
+      }
       for (int j = 0; ok && j < n; ++j) {
-        ok = mbar_wait_warp(bar.ds_full, ph, abort_flag);
+        if (kTilesAhead<D>) ok = (j + 1 >= n || has_v()) && (j + 2 >= n || has_k());
+        ok = ok && mbar_wait_warp(bar.ds_full, ph, abort_flag);
         if (ok && j == 0 && ni >= C::OB) ok = mbar_wait_warp(bar.out_free + ob, rb.ph ^ 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        if (j + 1 < n && !(ok = issue_dp())) break;
+        if (j + 1 < n) {
+          if (!kTilesAhead<D> && !(ok = has_v())) break;
+          issue_dp();
+        }
         const Desc k_mn = G::mnmajor(smem_u32(smem + C::OFF_K) + rk.st * G::BYTES);
         if (elect_one()) {
 #pragma unroll
@@ -759,7 +788,10 @@ __device__ __forceinline__ void dq_part(uint8_t* smem, const uint32_t tmem, int*
         rk.next();
         rs.next();
         ph ^= 1;
-        if (j + 2 < n && !(ok = issue_s(j + 2))) break;  // over dS, behind its product
+        if (j + 2 < n) {  // over dS, behind its product
+          if (!kTilesAhead<D> && !(ok = has_k())) break;
+          issue_s(j + 2);
+        }
       }
       if (ok && elect_one()) {
         mma_commit(bar.q_free + qb);
