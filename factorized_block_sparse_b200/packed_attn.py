@@ -69,11 +69,13 @@ class Layout:
 
     def __init__(self, lengths):
         self._h = ctypes.c_void_p()
-        wide = np.asarray(lengths, dtype=np.int64).reshape(-1)
+        wide = np.asarray(lengths).reshape(-1)
+        if wide.size and wide.dtype.kind not in "iu":
+            raise ValueError(f"sequence lengths must be integers, got {wide.dtype}")
         if wide.size and (wide.min() < 0 or wide.max() > np.iinfo(np.int32).max):
             raise ValueError("sequence lengths must be at least 0 and fit 32 bits")
         self.lengths = tuple(int(n) for n in wide)
-        arr = np.ascontiguousarray(wide, dtype=np.int32)
+        arr = np.ascontiguousarray(wide, dtype=np.int32)  # (after the range check)
         h = ctypes.c_void_p()
         sa._check(lib.packed_attn_layout(arr.ctypes.data, int(arr.size), ctypes.byref(h)), "packed_attn_layout")
         self._h = h

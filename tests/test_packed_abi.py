@@ -129,6 +129,14 @@ def test_argument_checks(pa):
     assert fwd(lay=none.handle, rows=0) == sa.SA_OK and bwd(lay=none.handle, rows=0) == sa.SA_OK
 
 
+def test_lengths_that_are_not_integers(pa):
+    for bad in ([1.5, 2.0], [True, False], ["3"], np.array([4.0]), torch.tensor([2.5])):
+        with pytest.raises(ValueError):
+            pa.Layout(bad)
+    for good in ([3, 0], (3,), np.array([3], dtype=np.uint8), torch.tensor([3]), np.array([3], dtype=np.int64), [], range(3)):
+        assert pa.Layout(good).rows == 3 * (len(good) > 0)
+
+
 def test_misaligned_lse(pa):
     from factorized_block_sparse_b200 import sparse_attn as sa
 
