@@ -134,3 +134,34 @@ def test_training_step_captured(cuda_device):
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]) and torch.equal(out[3], want[3])
         for name in want[2]:
             assert torch.equal(out[2][name], want[2][name]), name
+
+
+def test_streams_given_as_handles(cuda_device):
+    # 0 is the legacy default stream; another stream's handle stands for it
+    from factorized_block_sparse_b200 import packed_attn as pa
+    from factorized_block_sparse_b200 import sparse_block as sb
+
+    lay = pa.Layout([200, 57])
+    q, k, v, dO = (torch.from_numpy(synth.normal_f32((257, 2, 64), 90 + i)).to(torch.bfloat16).to(cuda_device)
+                   for i in range(4))
+    x = q.reshape(257, 128)
+    g = torch.ones(128, device=cuda_device)
+
+    def run(stream):
+        o, lse = pa.forward(q, k, v, lay, stream=stream)
+        d = pa.backward(q, k, v, o, lse, dO, lay, stream=stream)
+        y, mean, rstd = sb.layer_norm(x, g, stream=stream)
+        e = sb.layer_norm_backward(x, g, y, mean, rstd, stream=stream)
+        out = [torch.empty_like(t) for t in d]
+        norm = sb.clip_grads(d, 0.1, out=out, stream=stream)
+        torch.cuda.synchronize()
+        return [o, lse, *d, y, mean, rstd, *e, *out, norm]
+
+    ref = run(None)
+    side = torch.cuda.Stream(device=cuda_device)
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (0, side.cuda_stream, side):
+        before = torch.cuda.current_stream()
+        for a, b in zip(ref, run(stream)):
+            assert torch.equal(a, b)
+        assert torch.cuda.current_stream() == before
