@@ -912,7 +912,9 @@ bool alike(const void* a, int64_t lda, const void* b, int64_t ldb, int es) {
   return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0 && ((lda - ldb) * es) % 16 == 0;
 }
 
-constexpr int kParts = 1184;  // blocks of a backward launch, at most
+// Blocks of a backward launch at most, each with 2 C float32 sums in the workspace: eight an SM where blocks are of 64
+// threads (2^17 x 1024 bf16: 139 us, 169 with four), no more than an SM holds of the wider ones.
+int64_t parts(int C) { return C <= 2048 ? 1184 : C <= 4096 ? 592 : 296; }
 
 // The words of a row, at most (it may begin anywhere in its first one).
 int words_of(const void* p, int64_t ld, int C, int es) {
@@ -971,7 +973,7 @@ int sparse_block_layer_norm_fwd(const void* x, int64_t ldx, const float* g, cons
 
 size_t sparse_block_layer_norm_bwd_workspace_size(int64_t M, int C) {
   if (M < 0 || C < 1 || C > kMaxC) return 0;
-  return static_cast<size_t>(std::max<int64_t>(1, std::min<int64_t>(M, kParts))) * 2 * C * sizeof(float);
+  return static_cast<size_t>(std::max<int64_t>(1, std::min<int64_t>(M, parts(C)))) * 2 * C * sizeof(float);
 }
 
 int sparse_block_layer_norm_bwd(const void* x, int64_t ldx, const float* g, const void* dy, int64_t lddy,
@@ -1009,7 +1011,7 @@ int sparse_block_layer_norm_bwd(const void* x, int64_t ldx, const float* g, cons
         const size_t smem = std::max(ring, sums);
         const int per = resident<K>(dev, threads, smem);
         if (per == 0) return SA_ERR_CUDA;
-        long long grid = std::min<long long>(std::min<long long>((M + rows - 1) / rows, kParts), static_cast<long long>(n_sm) * per);
+        long long grid = std::min<long long>(std::min<long long>((M + rows - 1) / rows, parts(C)), static_cast<long long>(n_sm) * per);
         if (TPR == 0 && grid < M) grid = std::max<long long>(grid / 8 * 8, 8);
         P = static_cast<int>(grid);
         K<<<P, threads, smem, s>>>(static_cast<const T*>(x), ldx, g, static_cast<const T*>(dy), lddy, mean, rstd,
@@ -1023,7 +1025,7 @@ int sparse_block_layer_norm_bwd(const void* x, int64_t ldx, const float* g, cons
       constexpr auto K = norm_bwd_wide_kernel<T>;
       const size_t smem = 2 * static_cast<size_t>(C) * sizeof(float);
       if (resident<K>(dev, 512, smem) == 0) return SA_ERR_CUDA;
-      P = static_cast<int>(std::min<long long>(std::min<long long>(M, kParts), n_sm));
+      P = static_cast<int>(std::min<long long>(std::min<long long>(M, parts(C)), n_sm));
       K<<<P, 512, smem, s>>>(static_cast<const T*>(x), ldx, g, static_cast<const T*>(dy), lddy, mean, rstd,
                              static_cast<T*>(dx), lddx, part, M, C);
       return launched();
