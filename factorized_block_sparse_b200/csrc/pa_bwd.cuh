@@ -236,7 +236,7 @@ struct DkvCfg {
   static constexpr int OFF_DELTA = OFF_DO + OST * G::BYTES;
   static constexpr int OFF_LSE = OFF_DELTA + QST * VEC;
   static constexpr int END = OFF_LSE + OST * VEC;  // of the tiles
-  static constexpr int N_BARS = 2 * KVB + 2 * QST + 2 * OST + NS + 3 + 2 + 1;
+  static constexpr int N_BARS = 2 * KVB + 2 * QST + 2 * OST + 2 * NS + 2 + 2 + 1;
   static constexpr int OFF_BAR = BwdSmem<D>::OFF_BARS;
   static constexpr int COL_DP = NS * 128, COL_DV = COL_DP + 128, COL_DK = COL_DV + D;
   // P^T takes the first 16 of each group's 32 columns of its S^T buffer.  With
@@ -266,6 +266,10 @@ __device__ __forceinline__ DkvItem dkv_item(const DkvArgs& a, const Slot& s, int
 }
 
 // One part of the kernel: its barriers (their place in shared memory), initialised by one thread.
+// p_full has one for each S^T buffer: with two buffers S^T of step j + 1 is there before the issuing warp has seen the
+// weights of step j, so a compute warp may write P^T of both before then.  On one barrier its second arrival could stand
+// for a slower warp's first, or two phases could pass unseen; S^T of step j + 2, which the buffer's next arrivals wait
+// for, is issued behind dS^T of step j, that is behind all arrivals of step j and the wait for them.
 template <int D>
 struct DkvBars {
   using C = DkvCfg<D>;
@@ -279,8 +283,8 @@ struct DkvBars {
     do_full = q_free + C::QST;                                 // [OST]
     do_free = do_full + C::OST;                                // [OST]
     s_full = do_free + C::OST;                                 // [NS] S^T of a step
-    p_full = s_full + C::NS;                                   // P^T of a step written
-    dp_full = p_full + 1;                                      // dP^T of a step
+    p_full = s_full + C::NS;                                   // [NS] P^T of a step written
+    dp_full = p_full + C::NS;                                  // dP^T of a step
     ds_full = dp_full + 1;                                     // dS^T of a step written
     out_full = ds_full + 1;                                    // the item's dK, dV
     out_free = out_full + 1;
@@ -288,7 +292,7 @@ struct DkvBars {
   }
   __device__ __forceinline__ void init() const {
     for (uint64_t* b = kv_full; b < p_full; ++b) mbar_init(b, 1);
-    mbar_init(p_full, kBwdComputeWarps);
+    for (int b = 0; b < C::NS; ++b) mbar_init(p_full + b, kBwdComputeWarps);
     mbar_init(dp_full, 1);
     mbar_init(ds_full, kBwdComputeWarps);
     mbar_init(out_full, 1);
@@ -432,7 +436,7 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
       }
       for (int j = 0; ok && j < it.n; ++j) {
         if (kTilesAhead<D>) ok = (j + C::NS >= it.n || has_q()) && (j + 1 >= it.n || has_do());
-        ok = ok && mbar_wait_warp(bar.p_full, ph, abort_flag);
+        ok = ok && mbar_wait_warp(bar.p_full + rs.st, rs.ph, abort_flag);
         if (ok && j == 0 && ni > 0) ok = mbar_wait_warp(bar.out_free, (ni - 1) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -565,7 +569,7 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
         for (int i = 0; i < kCols / 2; ++i) pk[i] = Elem<T>::pack(p[2 * i] * kP, p[2 * i + 1] * kP);
         tmem_st_weights(t_s, pk);
         tc_fence_before();
-        warp_arrive(bar.p_full, lane);
+        warp_arrive(bar.p_full + rs.st, lane);
 
         ok = ok && mbar_wait(bar.q_full + rq.st, rq.ph, abort_flag) && mbar_wait(bar.dp_full, ph, abort_flag);
         tc_fence_after();
