@@ -425,7 +425,8 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
             tmem_st16(t_o + i * 16, ov);
           }
         }
-        const float neg = Elem<T>::kBias - m_used;
+        // a row whose keys so far all score -inf: weights of 0, not 2^(-inf + inf)
+        const float neg = m_used == -INFINITY ? Elem<T>::kBias : Elem<T>::kBias - m_used;
         const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), ng2 = f2_pack(neg, neg);
         uint64_t rs[4] = {0, 0, 0, 0};
 #pragma unroll

@@ -20,6 +20,8 @@
  * sequence into another, not even from rows that hold infinities or NaN.
  * Within one sequence a value that is not finite may reach rows of its own
  * 128-row tile that come before it (0 * inf in the masked half of a tile).
+ * Scores of -inf weigh nothing; a row that has no others has lse = -inf and
+ * no o (NaN).
  *
  * Tensors.  bf16 or fp16 (one type a call), D in {32, 64, 128}; a tensor is
  * its first element, the distance of two rows and of two heads in elements

@@ -5,7 +5,7 @@ ordinary cases.  Helpers and the tolerances' derivation: test_gpu_packed.py.
 import pytest
 import torch
 
-from test_gpu_packed import draw, pa  # noqa: F401
+from test_gpu_packed import check_backward, check_forward, draw, pa  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,43 @@ def test_backward_under_memory_traffic(cuda_device, pa, lengths, hq, hkv, d, dty
     for g in got:
         assert all(torch.equal(x, y) for x, y in zip(want, g))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("lengths,hq,hkv,first", [([500], 2, 2, 128), ([500], 1, 1, 256), ([390, 520] * 8, 8, 4, 256),
+                                                  ([390, 131] * 8, 9, 9, 128)])
+def test_first_key_tiles_without_weight(cuda_device, pa, lengths, hq, hkv, d, dtype, first):  # noqa: F811
+    # Rows from `first` on score -inf on every key before `first`: their whole first key tiles have no weight, and the
+    # result is that of the later keys alone.  Rows before `first` see nothing but -inf; they are not looked at.
+    q, k, v, _ = draw(sum(lengths), hq, hkv, d, dtype)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    at = 0
+    for n in lengths:
+        k[at:at + min(first, n), :, 0] = float("-inf")
+        at += n
+    lay = pa.Layout(lengths)
+    q, k, v = (t.to(cuda_device) for t in (q, k, v))
+    o, lse = pa.forward(q, k, v, lay)
+    assert pa.packed_attn_status() == 0
+    at = 0
+    for n in lengths:
+        if n > first:  # the later keys as a sequence of their own
+            part = slice(at + first, at + n)
+            check_forward(q[part], k[part], v[part], o[part], lse[:, part], [n - first])
+        at += n
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_products_that_leave_float32(cuda_device, pa, d):  # noqa: F811
+    # finite bf16 values, scores of -2^140 on the first 256 keys for the rows from 256 on: no weight, forward and backward
+    lengths, hq, hkv = [700], 4, 2
+    q, k, v, dO = draw(700, hq, hkv, d, torch.bfloat16)
+    q[:256, :, 0], k[256:, :, 0] = 0.0, 0.0
+    q[256:, :, 0], k[:256, :, 0] = 2.0 ** 70, -2.0 ** 70
+    q, k, v, dO = (t.to(cuda_device) for t in (q, k, v, dO))
+    lay = pa.Layout(lengths)
+    o, lse = pa.forward(q, k, v, lay)
+    check_forward(q, k, v, o, lse, lengths)
+    check_backward(q, k, v, o, lse, dO, pa.backward(q, k, v, o, lse, dO, lay), lengths)
+    assert pa.packed_attn_status() == 0
