@@ -234,13 +234,18 @@ int bwd_split(int Hq, int Hkv, const pa_layout* L) {
 }
 
 // Workspace of the backward pass: packed lse and delta of every (head, tile),
-// then the float32 dV and dK of items in parts.
+// the largest squared norms of its rows of dO and v, then the float32 dV and
+// dK of items in parts.
 size_t bwd_ws_ld(int Hq, const pa_layout* L) {
   return align256(static_cast<size_t>(Hq) * L->fwd.size() * 2 * kTile * sizeof(float));
 }
+size_t bwd_ws_peak(int Hq, int Hkv, const pa_layout* L) {
+  return align256(static_cast<size_t>(Hq + Hkv) * L->fwd.size() * sizeof(float));
+}
 size_t bwd_ws(int Hq, int Hkv, int D, const pa_layout* L) {
   const int split = bwd_split(Hq, Hkv, L);
-  return bwd_ws_ld(Hq, L) + (split > 1 ? static_cast<size_t>(split) * 2 * Hkv * L->rows * D * sizeof(float) : 0) + 256;
+  return bwd_ws_ld(Hq, L) + bwd_ws_peak(Hq, Hkv, L) +
+         (split > 1 ? static_cast<size_t>(split) * 2 * Hkv * L->rows * D * sizeof(float) : 0) + 256;
 }
 
 template <typename T, int D>
@@ -256,6 +261,8 @@ int run_bwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tens
   const unsigned tiles = static_cast<unsigned>(L->fwd.size());
   if (static_cast<long long>(tiles) * c.Hq > (1ll << 30)) return SA_ERR_UNSUPPORTED;  // item numbers stay in 31 bits
   float* ld = static_cast<float*>(ws);
+  uint8_t* behind_ld = static_cast<uint8_t*>(ws) + bwd_ws_ld(c.Hq, L);
+  float* peak = reinterpret_cast<float*>(behind_ld);
   const float scale_log2 = static_cast<float>(static_cast<double>(c.scale) * 1.4426950408889634);
   DkvArgs a;
   a.slots = dc.bwd;
@@ -263,10 +270,12 @@ int run_bwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tens
   a.G = c.Hq / c.Hkv;
   a.split = bwd_split(c.Hq, c.Hkv, L);
   a.n_items = static_cast<int>(tiles) * c.Hkv * a.split;
-  a.part = a.split > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + bwd_ws_ld(c.Hq, L)) : nullptr;
+  a.part = a.split > 1 ? reinterpret_cast<float*>(behind_ld + bwd_ws_peak(c.Hq, c.Hkv, L)) : nullptr;
   a.rows = L->rows;
   a.n_tiles = static_cast<int>(tiles);
   a.ld = ld;
+  a.peak_do = peak;
+  a.peak_v = peak + static_cast<size_t>(c.Hq) * tiles;
   a.dk = view(dk);
   a.dv = view(dv);
   a.scale = c.scale;
@@ -278,10 +287,13 @@ int run_bwd(const Call& c, const pa_tensor* q, const pa_tensor* k, const pa_tens
   b.n_items = static_cast<int>(tiles) * c.Hq;
   b.n_tiles = a.n_tiles;
   b.ld = ld;
+  b.peak_do = a.peak_do;
+  b.peak_v = a.peak_v;
   b.dq = view(dq);
   b.scale = c.scale;
   b.scale_log2 = scale_log2;
-  pa_bwd_pre_kernel<T, D><<<dim3(tiles, c.Hq), 256, 0, c.s>>>(dc.fwd, view(o), view(dO), lse, ls, ld, a.n_tiles);
+  pa_bwd_pre_kernel<T, D><<<dim3(tiles, c.Hq), 256, 0, c.s>>>(dc.fwd, view(o), view(dO), view(v), lse, ls, ld, peak, a.n_tiles,
+                                                              c.Hkv);
   if ((st = launched())) return st;
   // The main kernel sets itself up while the one before it drains (programmatic stream serialisation).
   cudaLaunchConfig_t cfg = {};

@@ -1,7 +1,7 @@
 // Backward kernels of packed causal attention on tcgen05.
 //
 // pa_bwd_pre_kernel   per (query tile, head): delta_i = <dO_i, o_i> and
-//                     -lse_i log2 e, padded to whole tiles.
+//                     -lse_i log2 e, padded to whole tiles (fp16: also largest norms).
 // pa_bwd_kernel, dkv_part
 //                     an item is a tile of 128 keys of one K/V head and all
 //                     query tiles of all query heads that see it (head by
@@ -91,19 +91,71 @@ __device__ __forceinline__ void keep_bits(float* v, const uint32_t* m) {
   for (int i = 0; i < kCols; ++i) v[i] = ((m[i / 32] >> (i % 32)) & 1u) ? v[i] : 0.f;
 }
 
-// TPR threads a row, 8 columns each.
+// fp16's P (at most 1) is scaled up for its product, away from the type's subnormals, by an addition to the stored
+// -lse log2 e; dV is scaled back.
+template <typename T>
+constexpr int kWeightBits = std::is_same<T, __half>::value ? 12 : 0;
+
+// fp16's dS is scaled, bf16's is not: dO of size 2^-10 over some thousands of keys makes it 2^-20, deep in fp16's
+// subnormals, and dO and v of size 2^8 take it out of fp16's range.  |dS| <= P |dP - delta| <= 2 max|dO_i| max|v_j|
+// (delta is a mean of dP), so the power of two that takes this bound to [2^14, 2^15) can neither overflow nor cost
+// anything, and every sum is divided by it at the end.  The norms are those of the rows that an item's dS is made of
+// (finite rows: the others make NaN of theirs whatever the factor).
+template <typename T>
+constexpr bool kScaleDs = std::is_same<T, __half>::value;
+
+// The exponent of that factor from the largest squared norms.
+__device__ __forceinline__ int ds_exponent(float do2, float v2) {
+  const float m = do2 * v2;  // within 2^-96 .. 2^78
+  if (!(m > 0.f)) return 0;
+  const int k = static_cast<int>(__float_as_uint(m) >> 23) - 127;  // the bound is below 2^((k + 3) / 2)
+  return 15 - ((k + 4) >> 1);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// The exponent from the largest of `rows` runs of n values of p, `step` apart, and the largest of nv values of v, by a whole
+// warp: an item starts with it, so eight loads are under way at a time, and its code is there once (2 x 12288 rows, 8
+// heads of 64, fp16: 1300 us; copies at its four places 1340, a constant in its place 1275, dS unscaled, mostly
+// subnormals that cost less power, 1260).
+__device__ __noinline__ int ds_exponent(const float* p, int rows, int n, long long step, const float* v, int nv, int lane) {
+  float m[2] = {0.f, 0.f};
+  const int all = rows * n;
+  for (int i = lane; i - lane < max(all, nv); i += 128) {
+    float x[4], y[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = i + 32 * u, r = j / n;
+      x[u] = j < all ? p[r * step + (j - r * n)] : 0.f;
+      y[u] = j < nv ? v[j] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m[0] = fmaxf(m[0], x[u]), m[1] = fmaxf(m[1], y[u]);
+  }
+  return ds_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m[0]))),  // (no value is negative)
+                     __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m[1]))));
+}
+
+// TPR threads a row, 8 columns each.  kScaleDs: peak [Hq + Hkv][n_tiles] takes the largest squared norm of a (head, tile)'s
+// rows of dO, and of v behind them.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
-    pa_bwd_pre_kernel(const Slot* slots, View o, View dO, const float* lse, long long ls, float* ld, int n_tiles) {
+    pa_bwd_pre_kernel(const Slot* slots, View o, View dO, View v, const float* lse, long long ls, float* ld, float* peak,
+                      int n_tiles, int Hkv) {
   constexpr int TPR = D / 8, RPI = 256 / TPR;
   pdl_trigger();
   const Slot s = slots[blockIdx.x];
   const int h = blockIdx.y, tid = threadIdx.x;
   float* out = ld + (static_cast<long long>(h) * n_tiles + s.base + s.tile) * 2 * kTile;
+  float most[2] = {0.f, 0.f};  // of dO and v
+  auto row_norm = [&](float ss, float& m) {  // ss: the sum of a thread's 8 squares
+#pragma unroll
+    for (int w = TPR / 2; w >= 1; w >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, w);
+    if (ss < INFINITY) m = fmaxf(m, ss);  // (neither NaN)
+  };
   for (int r = tid / TPR; r < kTile; r += RPI) {
     const int i = s.tile * kTile + r;
     const bool in = i < s.len;
-    float d = 0.f;
+    float d = 0.f, ss = 0.f, sv = 0.f;
     if (in) {
       const long long row = static_cast<long long>(s.start) + i;
       const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const T*>(o.p) + row * o.rs + h * o.hs + (tid % TPR) * 8);
@@ -113,13 +165,43 @@ __global__ void __launch_bounds__(256)
       for (int u = 0; u < 4; ++u) {
         const float2 x = Elem<T>::unpack(aw[u]), y = Elem<T>::unpack(bw[u]);
         d += x.x * y.x + x.y * y.y;
+        if constexpr (kScaleDs<T>) ss += y.x * y.x + y.y * y.y;
       }
+      if constexpr (kScaleDs<T>)
+        if (h < Hkv) {
+          const uint4 e = *reinterpret_cast<const uint4*>(static_cast<const T*>(v.p) + row * v.rs + h * v.hs + (tid % TPR) * 8);
+          const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float2 x = Elem<T>::unpack(ew[u]);
+            sv += x.x * x.x + x.y * x.y;
+          }
+        }
+    }
+    if constexpr (kScaleDs<T>) {
+      row_norm(ss, most[0]);
+      if (h < Hkv) row_norm(sv, most[1]);
     }
 #pragma unroll
     for (int w = TPR / 2; w >= 1; w >>= 1) d += __shfl_xor_sync(0xffffffffu, d, w);
     if (tid % TPR == 0) {
-      out[r] = in ? -1.4426950408889634f * lse[static_cast<long long>(h) * ls + s.start + i] : -INFINITY;
+      out[r] = in ? kWeightBits<T> - 1.4426950408889634f * lse[static_cast<long long>(h) * ls + s.start + i] : -INFINITY;
       out[kTile + r] = -d;
+    }
+  }
+  if constexpr (kScaleDs<T>) {
+    __shared__ float warps[2][8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(most[k]));
+      if ((tid & 31) == 0) warps[k][tid >> 5] = __uint_as_float(m);
+    }
+    __syncthreads();
+    if (tid < 2 && (tid == 0 || h < Hkv)) {
+      float m = warps[tid][0];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) m = fmaxf(m, warps[tid][w]);
+      peak[static_cast<long long>(tid == 0 ? h : static_cast<int>(gridDim.y) + h) * n_tiles + s.base + s.tile] = m;
     }
   }
 }
@@ -128,10 +210,6 @@ __global__ void __launch_bounds__(256)
 __host__ __device__ __forceinline__ int part_first(int all, int sp, int split) {
   return static_cast<int>(static_cast<long long>(all) * sp / split);
 }
-
-// fp16's P (at most 1) is scaled up for its product, away from the type's subnormals; dV is scaled back.
-template <typename T>
-constexpr float kWeightScale = std::is_same<T, __half>::value ? 4096.f : 1.f;
 
 // dV and dK of items in parts: the parts' sums in order, rounded once.  A block
 // takes kSumRows rows of a (key tile, K/V head), a thread 8 columns of one.
@@ -156,16 +234,16 @@ __global__ void __launch_bounds__(256)
       x[0] += u.x, x[1] += u.y, x[2] += u.z, x[3] += u.w, x[4] += v.x, x[5] += v.y, x[6] += v.z, x[7] += v.w;
     }
     const View& o = which ? dk : dv;
-    const float f = which ? scale : 1.f / kWeightScale<T>;
+    const float f = which ? scale : 1.f / (1 << kWeightBits<T>);
     *reinterpret_cast<uint4*>(static_cast<T*>(const_cast<void*>(o.p)) + (row0 + r) * o.rs + hk * o.hs + c * 8) =
         make_uint4(Elem<T>::pack(x[0] * f, x[1] * f), Elem<T>::pack(x[2] * f, x[3] * f),
                    Elem<T>::pack(x[4] * f, x[5] * f), Elem<T>::pack(x[6] * f, x[7] * f));
   }
 }
 
-// Writes one row's D float32 values from TMEM.
+// Writes one row's D float32 values from TMEM, times f.
 template <int D>
-__device__ __forceinline__ void row_out_f32(float* out, uint32_t taddr, bool in) {
+__device__ __forceinline__ void row_out_f32(float* out, uint32_t taddr, bool in, float f) {
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) {
     float x[32];
@@ -174,7 +252,7 @@ __device__ __forceinline__ void row_out_f32(float* out, uint32_t taddr, bool in)
     if (in)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<float4*>(out + c * 32 + 4 * i) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        *reinterpret_cast<float4*>(out + c * 32 + 4 * i) = make_float4(x[4 * i] * f, x[4 * i + 1] * f, x[4 * i + 2] * f, x[4 * i + 3] * f);
   }
 }
 
@@ -211,7 +289,8 @@ struct DkvArgs {
   const Slot* slots;
   int n_items, Hkv, G;
   int n_tiles;      // 128-row tiles of all sequences
-  const float* ld;  // [Hq][n_tiles][2][128]: -lse log2 e (padding -inf), -delta (padding 0)
+  const float* ld;  // [Hq][n_tiles][2][128]: kWeightBits - lse log2 e (padding -inf), -delta (padding 0)
+  const float *peak_do, *peak_v;  // [Hq][n_tiles], [Hkv][n_tiles]: largest squared norms of the rows (kScaleDs)
   View dk, dv;
   float scale, scale_log2;
   // Few key tiles and many steps each: the steps of an item in `split` parts,
@@ -265,6 +344,14 @@ __device__ __forceinline__ DkvItem dkv_item(const DkvArgs& a, const Slot& s, int
   return it;
 }
 
+// Exponent of an item's factor of dS: dO of the group's heads from the key tile on, v of the whole sequence (delta).
+template <typename T>
+__device__ __forceinline__ int ds_exponent(const DkvArgs& a, const DkvItem& it, int lane) {
+  if constexpr (!kScaleDs<T>) return 0;
+  return ds_exponent(a.peak_do + static_cast<long long>(it.hk) * a.G * a.n_tiles + it.s.base + it.s.tile, a.G, it.per, a.n_tiles,
+                     a.peak_v + static_cast<long long>(it.hk) * a.n_tiles + it.s.base, it.s.tile + it.per, lane);
+}
+
 // One part of the kernel: its barriers (their place in shared memory), initialised by one thread.
 // p_full has one for each S^T buffer: with two buffers S^T of step j + 1 is there before the issuing warp has seen the
 // weights of step j, so a compute warp may write P^T of both before then.  On one barrier its second arrival could stand
@@ -307,7 +394,6 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
                                          const DkvArgs& a) {
   using C = DkvCfg<D>;
   using G = TileGeo<D>;
-  constexpr float kP = kWeightScale<T>;
   const DkvBars<D> bar(smem);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int cta = blockIdx.x, n_ctas = gridDim.x;
@@ -502,6 +588,7 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
       const DkvItem it = dkv_item(a, walk.take(item, k), item);
       if (it.n == 0) continue;
+      const float unscale = pow2(-ds_exponent<T>(a, it, lane));
       ok = mbar_wait_steps(bar.out_full, ni & 1, abort_flag, it.n);
       if (!ok) break;
       ++ni;
@@ -511,13 +598,13 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
       const bool in = key < it.s.len;
       if (a.part) {
         float* dst = a.part + ((static_cast<long long>(it.sp) * 2 * a.Hkv + it.hk) * a.rows + krow) * D;
-        row_out_f32<D>(dst, tmem + lane_base + C::COL_DV, in);
-        row_out_f32<D>(dst + a.Hkv * a.rows * D, tmem + lane_base + C::COL_DK, in);
+        row_out_f32<D>(dst, tmem + lane_base + C::COL_DV, in, 1.f);
+        row_out_f32<D>(dst + a.Hkv * a.rows * D, tmem + lane_base + C::COL_DK, in, unscale);
       } else {
         row_out<T, D>(static_cast<T*>(const_cast<void*>(a.dv.p)) + krow * a.dv.rs + it.hk * a.dv.hs,
-                      tmem + lane_base + C::COL_DV, in, 1.f / kP);
+                      tmem + lane_base + C::COL_DV, in, 1.f / (1 << kWeightBits<T>));
         row_out<T, D>(static_cast<T*>(const_cast<void*>(a.dk.p)) + krow * a.dk.rs + it.hk * a.dk.hs,
-                      tmem + lane_base + C::COL_DK, in, a.scale);
+                      tmem + lane_base + C::COL_DK, in, a.scale * unscale);
       }
       tc_fence_before();
       warp_arrive(bar.out_free, lane);
@@ -542,6 +629,7 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
     uint32_t ph = 0;
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas)) {
       const DkvItem it = dkv_item(a, walk.take(item, k), item);
+      const float up = it.n > 0 ? pow2(ds_exponent<T>(a, it, lane) - kWeightBits<T>) : 1.f;  // of dS
       for (int j = 0, in_head = it.first % it.per; ok && j < it.n; ++j) {
         const bool diag = in_head == 0;
         if (++in_head == it.per) in_head = 0;
@@ -566,7 +654,7 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
         if (diag) keep_bits(p, behind);
         uint32_t pk[kCols / 2];
 #pragma unroll
-        for (int i = 0; i < kCols / 2; ++i) pk[i] = Elem<T>::pack(p[2 * i] * kP, p[2 * i + 1] * kP);
+        for (int i = 0; i < kCols / 2; ++i) pk[i] = Elem<T>::pack(p[2 * i], p[2 * i + 1]);
         tmem_st_weights(t_s, pk);
         tc_fence_before();
         warp_arrive(bar.p_full + rs.st, lane);
@@ -589,7 +677,14 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
         }
         if (diag) keep_bits(dp, behind);  // a masked place stays 0 whatever dP holds there
 #pragma unroll
-        for (int i = 0; i < kCols / 2; ++i) pk[i] = Elem<T>::pack(dp[2 * i], dp[2 * i + 1]);
+        for (int i = 0; i < kCols / 2; ++i) {
+          if constexpr (kScaleDs<T>) {
+            const float2 d = f2_unpack(f2_mul(f2_pack(dp[2 * i], dp[2 * i + 1]), f2_pack(up, up)));
+            pk[i] = Elem<T>::pack(d.x, d.y);
+          } else {
+            pk[i] = Elem<T>::pack(dp[2 * i], dp[2 * i + 1]);
+          }
+        }
         tmem_st_weights(C::DS_IN_S ? t_s + kCols / 2 : t_dp, pk);
         tc_fence_before();
         warp_arrive(bar.ds_full, lane);
@@ -607,10 +702,18 @@ struct DqArgs {
   const Slot* slots;
   int n_items, Hq, G;
   int n_tiles;
-  const float* ld;  // as DkvArgs
+  const float *ld, *peak_do, *peak_v;  // as DkvArgs
   View dq;
   float scale, scale_log2;
 };
+
+// Exponent of an item's factor of dS: dO of the tile's rows, v of the rows that they see.
+template <typename T>
+__device__ __forceinline__ int ds_exponent(const DqArgs& a, const Slot& s, int h, int lane) {
+  if constexpr (!kScaleDs<T>) return 0;
+  return ds_exponent(a.peak_do + static_cast<long long>(h) * a.n_tiles + s.base + s.tile, 1, 1, 0,
+                     a.peak_v + static_cast<long long>(h / a.G) * a.n_tiles + s.base, s.tile + 1, lane);
+}
 
 template <int D>
 struct DqCfg {
@@ -818,12 +921,13 @@ __device__ __forceinline__ void dq_part(uint8_t* smem, const uint32_t tmem, int*
     for (int k = 0, item = cta; ok && item < a.n_items; item = zigzag(++k, cta, n_ctas), ++ni) {
       const int h = item % a.Hq, ob = ni % C::OB;
       const Slot s = walk.take(item, k);
+      const float unscale = pow2(-ds_exponent<T>(a, s, h, lane));
       ok = mbar_wait_steps(bar.out_full + ob, (ni / C::OB) & 1, abort_flag, s.tile + 1);
       if (!ok) break;
       tc_fence_after();
       const int i = s.tile * kTile + row;
       row_out<T, D>(static_cast<T*>(const_cast<void*>(a.dq.p)) + (static_cast<long long>(s.start) + i) * a.dq.rs + h * a.dq.hs,
-                    tmem + lane_base + C::COL_DQ + ob * D, i < s.len, a.scale);
+                    tmem + lane_base + C::COL_DQ + ob * D, i < s.len, a.scale * unscale);
       tc_fence_before();
       warp_arrive(bar.out_free + ob, lane);
     }
@@ -846,7 +950,8 @@ __device__ __forceinline__ void dq_part(uint8_t* smem, const uint32_t tmem, int*
       const Slot s = walk.take(item, k);
       const float* ld = a.ld + (static_cast<long long>(h) * a.n_tiles + s.base + s.tile) * 2 * kTile;
       const float neg_lse = ld[row], neg_delta = ld[kTile + row];
-      const uint64_t l2 = f2_pack(neg_lse, neg_lse), d2 = f2_pack(neg_delta, neg_delta);
+      const float up = pow2(ds_exponent<T>(a, s, h, lane) - kWeightBits<T>);  // dS up = P (dP up - delta up)
+      const uint64_t l2 = f2_pack(neg_lse, neg_lse), d2 = f2_pack(neg_delta * up, neg_delta * up);
       for (int j = 0; ok && j <= s.tile; ++j) {
         const bool diag = j == s.tile;
         const uint32_t t_s = t_row + rs.st * 128;
@@ -866,7 +971,9 @@ __device__ __forceinline__ void dq_part(uint8_t* smem, const uint32_t tmem, int*
         tmem_ld_cols(t_row + C::COL_DP, dp);
 #pragma unroll
         for (int i = 0; i < kCols / 2; ++i) {
-          const float2 v = f2_unpack(f2_mul(f2_pack(p[2 * i], p[2 * i + 1]), f2_add(f2_pack(dp[2 * i], dp[2 * i + 1]), d2)));
+          const uint64_t t = f2_pack(dp[2 * i], dp[2 * i + 1]);
+          const uint64_t diff = kScaleDs<T> ? f2_fma(t, f2_pack(up, up), d2) : f2_add(t, d2);
+          const float2 v = f2_unpack(f2_mul(f2_pack(p[2 * i], p[2 * i + 1]), diff));
           dp[2 * i] = v.x;
           dp[2 * i + 1] = v.y;
         }

@@ -32,9 +32,10 @@
  * logarithm.  Score products, softmax and gradient sums are float32; P and
  * dS are rounded to the tensors' type before their second product, outputs
  * once at the end.  Every sum has a fixed order: the same call on the same
- * device gives the same bits.  fp16: dS = P (dP - delta) is rounded as it is,
- * so gradients of outputs are to be scaled into fp16's range by the caller, as
- * for every fp16 gradient.
+ * device gives the same bits.  fp16: P and dS = P (dP - delta) are scaled by
+ * powers of two for their products (dS by the largest norms of the rows of dO
+ * and v that it is made of) and the sums scaled back, so dO may be of any size
+ * whose gradients fp16 holds.
  *
  * Every call is asynchronous on `stream` (a cudaStream_t, or NULL for the
  * legacy default stream), runs on the current device, and returns an

@@ -2,10 +2,12 @@
 ordinary cases.  Helpers and the tolerances' derivation: test_gpu_packed.py.
 """
 
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_packed import check_backward, check_forward, draw, pa  # noqa: F401
+from oracle import packed
+from test_gpu_packed import U, check, check_backward, check_forward, draw, f64, pa  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +75,58 @@ def test_products_that_leave_float32(cuda_device, pa, d):  # noqa: F811
     check_forward(q, k, v, o, lse, lengths)
     check_backward(q, k, v, o, lse, dO, pa.backward(q, k, v, o, lse, dO, lay), lengths)
     assert pa.packed_attn_status() == 0
+
+
+# sizes of dO, v, q, k
+FP16_SIZES = [(2.0 ** -13, 1.0, 2.0 ** -4, 2.0 ** 4), (2.0 ** -13, 1.0, 2.0 ** 4, 2.0 ** -4),
+              (2.0 ** -16, 1.0, 2.0 ** -4, 2.0 ** 4), (2.0 ** -16, 2.0 ** -5, 2.0 ** 5, 2.0 ** -5),
+              (2.0 ** 8, 2.0 ** 8, 2.0 ** -3, 2.0 ** -3), (0.0, 1.0, 1.0, 1.0)]
+
+
+@pytest.mark.parametrize("lengths,hq,hkv,d", [([1500, 40], 2, 2, 64), ([1999], 2, 1, 64), ([1300, 300], 4, 2, 128),
+                                              ([1100], 2, 1, 32)])
+@pytest.mark.parametrize("f,fv,fq,fk", FP16_SIZES)
+def test_fp16_gradients_of_any_size(cuda_device, pa, lengths, hq, hkv, d, f, fv, fq, fk):  # noqa: F811
+    # dS keeps its relative precision whatever the size of dO and v: the factor of a sequence and K/V head takes the
+    # bound 2 max|dO_i| max|v_j| of |dS| to [2^14, 2^15), so a dS that rounds to a subnormal is off by at most
+    # 2^-25 2 max|dO_i| max|v_j| / 2^14.  P is scaled by 2^12.  The other terms as at the head of test_gpu_packed.py, the
+    # cancellation of dP - delta as 1e-5 of the largest term.
+    q, k, v, dO = draw(sum(lengths), hq, hkv, d, torch.float16)
+    q, k, v, dO = ((t.float() * s).half().to(cuda_device) for t, s in ((q, fq), (k, fk), (v, fv), (dO, f)))
+    lay = pa.Layout(lengths)
+    o, lse = pa.forward(q, k, v, lay)
+    grads = pa.backward(q, k, v, o, lse, dO, lay)
+    assert pa.packed_attn_status() == 0
+    x = [f64(t) for t in (q, k, v, o, lse, dO)]
+    *ref, m = packed.backward(*x, lengths)
+    vv = np.repeat(x[2], hq // hkv, axis=1)
+    term = max(float(np.abs(x[5][:, h] @ vv[:, h].T).max()) for h in range(hq))
+    sub = 2.0 ** -38 * np.sqrt((x[5] ** 2).sum(-1)).max() * np.sqrt((x[2] ** 2).sum(-1)).max()
+    u, tiny = U[torch.float16], 2.0 ** -25
+    for name, got, r, ds, p, n in (("dq", grads[0], ref[0], "dq_ds", "dq_p", "dq_n"), ("dk", grads[1], ref[1], "dk_ds", "dk_p", "dk_n")):
+        check(name, got, r, u * (m[ds] + np.abs(r)) + 1e-5 * term * m[p] + sub * m[n] + tiny)
+    r = ref[2]
+    check("dv", grads[2], r, u * (m["dv_p"] + np.abs(r)) + 2e-4 * m["dv_p"] + 2.0 ** -37 * m["dv_n"] + tiny)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 60000.0])
+def test_fp16_factors_stay_in_their_sequence(cuda_device, pa, value):  # noqa: F811
+    # small gradients beside a sequence of large ones, or of values that are not finite: the same bits as without it
+    lengths, hq, hkv, d = [130, 70, 200], 4, 2, 64
+    q, k, v, dO = draw(sum(lengths), hq, hkv, d, torch.float16)
+    x = [t.to(cuda_device) for t in (q, k, v, dO * 2.0 ** -10)]
+    lay = pa.Layout(lengths)
+    o, lse = pa.forward(*x[:3], lay)
+    ref = pa.backward(*x[:3], o, lse, x[3], lay)
+    y = [t.clone() for t in x]
+    for t in y[2:]:
+        t[130:200] = value
+    got = pa.backward(*y[:3], o, lse, y[3], lay)
+    for a, b in zip(ref, got):
+        for part in (slice(0, 130), slice(200, 400)):
+            assert torch.equal(a[part], b[part])
+    # a row of the same sequence that is not finite costs the others nothing either
+    z = x[3].clone()
+    z[399] = float("inf")
+    late = pa.backward(*x[:3], o, lse, z, lay)
+    assert torch.equal(late[0][:399], ref[0][:399])
