@@ -1,5 +1,5 @@
-"""Builds the in-tree shared libraries for sm_100a: ``libsparse_attn.so``, its
-test build, ``libsparse_block.so`` and ``libpacked_attn.so``.
+"""Builds the in-tree shared libraries for sm_100a: ``libsparse_attn.so`` and
+its test build, ``libsparse_block.so``, ``libpacked_attn.so`` and its test build.
 
 For each, one nvcc invocation compiles the CUDA translation units (kernels and
 C ABI) and the host layout builder.  The CUDA runtime is linked statically and the
@@ -97,25 +97,31 @@ def build_block_lib(force=False, verbose=False):
 
 # Causal attention over packed sequences: its own library.
 PACKED_LIB = os.path.join(HERE, "libpacked_attn.so")
+PACKED_TEST_LIB = os.path.join(HERE, "libpacked_attn_test.so")  # short waits, withheld loads; never used by the product path
 PACKED_SOURCES = [os.path.join(HERE, "csrc", f) for f in ("pa_api.cu", "pa_layout.cpp")]
 PACKED_HEADERS = [os.path.join(ROOT, "include", f) for f in ("packed_attn.h", "sparse_attn.h")] + [
     os.path.join(HERE, "csrc", f) for f in ("pa_internal.h", "pa_device.cuh", "pa_fwd.cuh", "pa_bwd.cuh", "sa_device.cuh",
                                             "sa_internal.h")]
 
 
-def build_packed_lib(force=False, verbose=False, extra=()):
+def build_packed_lib(force=False, verbose=False, extra=(), out=PACKED_LIB):
     """Compile libpacked_attn.so if out of date; return its path."""
-    if not force and os.path.exists(PACKED_LIB):
-        t = os.path.getmtime(PACKED_LIB)
+    if not force and os.path.exists(out):
+        t = os.path.getmtime(out)
         if all(os.path.getmtime(p) <= t for p in PACKED_SOURCES + PACKED_HEADERS):
-            return PACKED_LIB
+            return out
     cmd = [nvcc_path(), "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
-           "-Xcompiler", "-fPIC,-O3", "-shared", "-cudart", "static", "-Xlinker", "-soname=libpacked_attn.so",
-           "-I", os.path.join(ROOT, "include"), "-o", PACKED_LIB, *extra, *PACKED_SOURCES]
+           "-Xcompiler", "-fPIC,-O3", "-shared", "-cudart", "static", "-Xlinker", "-soname=" + os.path.basename(out),
+           "-I", os.path.join(ROOT, "include"), "-o", out, *extra, *PACKED_SOURCES]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    return PACKED_LIB
+    return out
+
+
+def build_packed_test_lib(force=False, verbose=False):
+    """Compile the failure-detection tests' build (-DSA_TEST_HOOKS) if it is out of date; return its path."""
+    return build_packed_lib(force, verbose, ("-DSA_TEST_HOOKS",), PACKED_TEST_LIB)
 
 
 if __name__ == "__main__":
@@ -125,3 +131,4 @@ if __name__ == "__main__":
     build_block_lib(force="--force" in sys.argv, verbose=True)
     build_packed_lib(force="--force" in sys.argv, verbose=True,
                      extra=["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else [])
+    build_packed_test_lib(force="--force" in sys.argv, verbose=True)

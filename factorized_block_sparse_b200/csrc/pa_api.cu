@@ -421,4 +421,11 @@ int packed_attn_status(void* stream) {
   return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
+#ifdef SA_TEST_HOOKS
+// Test build only (not declared in the header): which first load the producers withhold (pa::Withhold; 0: none).
+int packed_attn_test_withhold(int what) {
+  return cudaMemcpyToSymbol(sa::g_test_withhold, &what, sizeof(int)) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+#endif
+
 }  // extern "C"

@@ -410,9 +410,11 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
         const int kb = ni % C::KVB;
         if (ni >= C::KVB && !mbar_wait(bar.kv_free + kb, (ni / C::KVB - 1) & 1, abort_flag)) break;
         const int key0 = it.s.start + it.s.tile * kTile;
-        mbar_arrive_expect_tx(bar.kv_full + kb, 2 * G::BYTES);
-        load_tile<D>(smem + C::OFF_K + kb * G::BYTES, &mk, bar.kv_full + kb, it.hk, key0);
-        load_tile<D>(smem + C::OFF_V + kb * G::BYTES, &mv, bar.kv_full + kb, it.hk, key0);
+        if (!PA_WITHHELD(kHoldDkvK, ni)) {
+          mbar_arrive_expect_tx(bar.kv_full + kb, 2 * G::BYTES);
+          load_tile<D>(smem + C::OFF_K + kb * G::BYTES, &mk, bar.kv_full + kb, it.hk, key0);
+          load_tile<D>(smem + C::OFF_V + kb * G::BYTES, &mv, bar.kv_full + kb, it.hk, key0);
+        }
         ++ni;
         for (int j = it.first; ok && j < it.first + it.n; ++j) {
           const int h = it.hk * a.G + j / it.per, qt = it.s.tile + j % it.per, row = it.s.start + qt * kTile;
@@ -431,18 +433,19 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(bar.do_full + so, G::BYTES + C::VEC);
-          load_tile<D>(smem + C::OFF_DO + so * G::BYTES, &mdo, bar.do_full + so, h, row);
-          bulk_load(smem + C::OFF_LSE + so * C::VEC, ld, C::VEC, bar.do_full + so);
+          if (!PA_WITHHELD(kHoldDkvDO, n_do)) {
+            mbar_arrive_expect_tx(bar.do_full + so, G::BYTES + C::VEC);
+            load_tile<D>(smem + C::OFF_DO + so * G::BYTES, &mdo, bar.do_full + so, h, row);
+            bulk_load(smem + C::OFF_LSE + so * C::VEC, ld, C::VEC, bar.do_full + so);
+          }
           ++n_do;
         }
       }
-      if (*(volatile int*)abort_flag) {  // no copy may land after the CTA has gone
-        for (int i = ni > C::KVB ? ni - C::KVB : 0; i < ni; ++i) mbar_wait_drain(bar.kv_full + i % C::KVB, (i / C::KVB) & 1);
-        for (int i = g > C::QST ? g - C::QST : 0; i < g; ++i) mbar_wait_drain(bar.q_full + i % C::QST, (i / C::QST) & 1);
-        for (int i = n_do > C::OST ? n_do - C::OST : 0; i < n_do; ++i)
-          mbar_wait_drain(bar.do_full + i % C::OST, (i / C::OST) & 1);
-      }
+      // no copy may land after the CTA has gone or the other part has begun, whichever role gives up, and when
+      for (int i = ni > C::KVB ? ni - C::KVB : 0; i < ni; ++i) mbar_wait_drain(bar.kv_full + i % C::KVB, (i / C::KVB) & 1);
+      for (int i = g > C::QST ? g - C::QST : 0; i < g; ++i) mbar_wait_drain(bar.q_full + i % C::QST, (i / C::QST) & 1);
+      for (int i = n_do > C::OST ? n_do - C::OST : 0; i < n_do; ++i)
+        mbar_wait_drain(bar.do_full + i % C::OST, (i / C::OST) & 1);
     }
   } else if (warp == kBwdComputeWarps + 5) {
     // ------------------------------------------------------------------ MMAs
@@ -589,7 +592,7 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
       const DkvItem it = dkv_item(a, walk.take(item, k), item);
       if (it.n == 0) continue;
       const float unscale = pow2(-ds_exponent<T>(a, it, lane));
-      ok = mbar_wait_steps(bar.out_full, ni & 1, abort_flag, it.n);
+      ok = warp_ok(mbar_wait_steps(bar.out_full, ni & 1, abort_flag, it.n));
       if (!ok) break;
       ++ni;
       tc_fence_after();
@@ -659,7 +662,7 @@ __device__ __forceinline__ void dkv_part(uint8_t* smem, const uint32_t tmem, int
         tc_fence_before();
         warp_arrive(bar.p_full + rs.st, lane);
 
-        ok = ok && mbar_wait(bar.q_full + rq.st, rq.ph, abort_flag) && mbar_wait(bar.dp_full, ph, abort_flag);
+        ok = warp_ok(ok && mbar_wait(bar.q_full + rq.st, rq.ph, abort_flag) && mbar_wait(bar.dp_full, ph, abort_flag));
         tc_fence_after();
         float dp[kCols];
         tmem_ld_cols(t_dp, dp);
@@ -785,9 +788,11 @@ __device__ __forceinline__ void dq_part(uint8_t* smem, const uint32_t tmem, int*
         const Slot s = walk.take(item, k);
         const int qb = ni % C::QB;
         if (ni >= C::QB && !mbar_wait(bar.q_free + qb, (ni / C::QB - 1) & 1, abort_flag)) break;
-        mbar_arrive_expect_tx(bar.q_full + qb, 2 * G::BYTES);
-        load_tile<D>(smem + C::OFF_Q + qb * G::BYTES, &mq, bar.q_full + qb, h, s.start + s.tile * kTile);
-        load_tile<D>(smem + C::OFF_DO + qb * G::BYTES, &mdo, bar.q_full + qb, h, s.start + s.tile * kTile);
+        if (!PA_WITHHELD(kHoldDqQ, ni)) {
+          mbar_arrive_expect_tx(bar.q_full + qb, 2 * G::BYTES);
+          load_tile<D>(smem + C::OFF_Q + qb * G::BYTES, &mq, bar.q_full + qb, h, s.start + s.tile * kTile);
+          load_tile<D>(smem + C::OFF_DO + qb * G::BYTES, &mdo, bar.q_full + qb, h, s.start + s.tile * kTile);
+        }
         ++ni;
         for (int j = 0; ok && j <= s.tile; ++j) {
           const int row = s.start + j * kTile, sk = g % C::KST;
@@ -803,16 +808,17 @@ __device__ __forceinline__ void dq_part(uint8_t* smem, const uint32_t tmem, int*
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(bar.v_full + sv, G::BYTES);
-          load_tile<D>(smem + C::OFF_V + sv * G::BYTES, &mv, bar.v_full + sv, h / a.G, row);
+          if (!PA_WITHHELD(kHoldDqV, nv)) {
+            mbar_arrive_expect_tx(bar.v_full + sv, G::BYTES);
+            load_tile<D>(smem + C::OFF_V + sv * G::BYTES, &mv, bar.v_full + sv, h / a.G, row);
+          }
           ++nv;
         }
       }
-      if (*(volatile int*)abort_flag) {  // no copy may land after the CTA has gone
-        for (int i = ni > C::QB ? ni - C::QB : 0; i < ni; ++i) mbar_wait_drain(bar.q_full + i % C::QB, (i / C::QB) & 1);
-        for (int i = g > C::KST ? g - C::KST : 0; i < g; ++i) mbar_wait_drain(bar.k_full + i % C::KST, (i / C::KST) & 1);
-        for (int i = nv > C::VST ? nv - C::VST : 0; i < nv; ++i) mbar_wait_drain(bar.v_full + i % C::VST, (i / C::VST) & 1);
-      }
+      // no copy may land after the CTA has gone, whichever role gives up, and when
+      for (int i = ni > C::QB ? ni - C::QB : 0; i < ni; ++i) mbar_wait_drain(bar.q_full + i % C::QB, (i / C::QB) & 1);
+      for (int i = g > C::KST ? g - C::KST : 0; i < g; ++i) mbar_wait_drain(bar.k_full + i % C::KST, (i / C::KST) & 1);
+      for (int i = nv > C::VST ? nv - C::VST : 0; i < nv; ++i) mbar_wait_drain(bar.v_full + i % C::VST, (i / C::VST) & 1);
     }
   } else if (warp == kBwdComputeWarps + 5) {
     // ------------------------------------------------------------------ MMAs
@@ -922,7 +928,7 @@ __device__ __forceinline__ void dq_part(uint8_t* smem, const uint32_t tmem, int*
       const int h = item % a.Hq, ob = ni % C::OB;
       const Slot s = walk.take(item, k);
       const float unscale = pow2(-ds_exponent<T>(a, s, h, lane));
-      ok = mbar_wait_steps(bar.out_full + ob, (ni / C::OB) & 1, abort_flag, s.tile + 1);
+      ok = warp_ok(mbar_wait_steps(bar.out_full + ob, (ni / C::OB) & 1, abort_flag, s.tile + 1));
       if (!ok) break;
       tc_fence_after();
       const int i = s.tile * kTile + row;
@@ -965,7 +971,7 @@ __device__ __forceinline__ void dq_part(uint8_t* smem, const uint32_t tmem, int*
           p[2 * i] = e.x;
           p[2 * i + 1] = e.y;
         }
-        ok = ok && mbar_wait(bar.dp_full, ph, abort_flag);
+        ok = warp_ok(ok && mbar_wait(bar.dp_full, ph, abort_flag));
         tc_fence_after();
         float dp[kCols];
         tmem_ld_cols(t_row + C::COL_DP, dp);
@@ -1018,9 +1024,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t tmem = *tmem_slot;
   dkv_part<T, D>(smem, tmem, abort_flag, mq, mk, mv, mdo, a);
   tc_fence_before();
-  __syncthreads();
+  const bool gave_up = __syncthreads_or(*(volatile int*)abort_flag);  // one answer for the block
   tc_fence_after();
-  if (*(volatile int*)abort_flag == 0) dq_part<T, D>(smem, tmem, abort_flag, mq, mk, mv, mdo, b);
+  if (!gave_up) dq_part<T, D>(smem, tmem, abort_flag, mq, mk, mv, mdo, b);
   tc_fence_before();
   __syncthreads();
   if (warp == kBwdComputeWarps + 5) {

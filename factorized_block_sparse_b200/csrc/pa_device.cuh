@@ -101,6 +101,23 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, i
   }
 }
 
+// One answer for a warp whose lanes waited each for itself (they may part ways
+// where a wait runs out): what follows, collective instructions and the roles'
+// loops, is for the whole warp.
+__device__ __forceinline__ bool warp_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+#ifdef SA_TEST_HOOKS
+// Test build: whether a producer withholds load number n (its first one) of
+// kind `what` in the CTA that takes a part's first item, so that a wait runs out.
+enum Withhold : int { kHoldQ = 1, kHoldV = 2, kHoldDkvDO = 3, kHoldDkvK = 4, kHoldDqV = 5, kHoldDqQ = 6 };
+__device__ __forceinline__ bool withheld(int what, int n, int cta) {
+  return n == 0 && cta == 0 && *(volatile int*)&g_test_withhold == what;
+}
+#define PA_WITHHELD(what, n) withheld(what, n, cta)
+#else
+#define PA_WITHHELD(what, n) false
+#endif
+
 // mbar_wait for something that takes `steps` steps of a kernel's inner loop:
 // an item of a very long sequence may run for more than mbar_wait's second.
 __device__ __forceinline__ bool mbar_wait_steps(uint64_t* bar, uint32_t parity, int* abort, int steps) {

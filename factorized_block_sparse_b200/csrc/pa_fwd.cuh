@@ -187,8 +187,10 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
           if (it.n[u] == 0) continue;
           if (nq[u] > 0) ok = mbar_wait(bar_q_free + u, (nq[u] - 1) & 1, abort_flag);
           if (!ok) break;
-          mbar_arrive_expect_tx(bar_q_full + u, G::BYTES);
-          load_tile<D>(sQ + u * G::BYTES, &mq, bar_q_full + u, it.h[u], it.s.start + it.qt[u] * kTile);
+          if (!PA_WITHHELD(kHoldQ, nq[u])) {
+            mbar_arrive_expect_tx(bar_q_full + u, G::BYTES);
+            load_tile<D>(sQ + u * G::BYTES, &mq, bar_q_full + u, it.h[u], it.s.start + it.qt[u] * kTile);
+          }
           ++nq[u];
         }
         const int n = max(it.n[0], it.n[1]);
@@ -198,16 +200,16 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
             ok = false;
             break;
           }
+          if (PA_WITHHELD(kHoldV, ring - 1)) continue;
           mbar_arrive_expect_tx(bar_kv_full + st, G::BYTES);
           load_tile<D>(sKV + st * G::BYTES, (j & 1) ? &mv : &mk, bar_kv_full + st, it.hk, it.s.start + (j >> 1) * kTile);
         }
       }
-      if (*(volatile int*)abort_flag) {  // no copy may land after the CTA has gone
-        for (int u = 0; u < 2; ++u)
-          if (nq[u] > 0) mbar_wait_drain(bar_q_full + u, (nq[u] - 1) & 1);
-        for (int h = ring > C::STAGES ? ring - C::STAGES : 0; h < ring; ++h)
-          mbar_wait_drain(bar_kv_full + h % C::STAGES, (h / C::STAGES) & 1);
-      }
+      // no copy may land after the CTA has gone, whichever role gives up, and when
+      for (int u = 0; u < 2; ++u)
+        if (nq[u] > 0) mbar_wait_drain(bar_q_full + u, (nq[u] - 1) & 1);
+      for (int h = ring > C::STAGES ? ring - C::STAGES : 0; h < ring; ++h)
+        mbar_wait_drain(bar_kv_full + h % C::STAGES, (h / C::STAGES) & 1);
     }
   } else if (warp > C::SOFT_WARPS) {
     // ------------------------------------------------------------------ MMAs
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         l_sum = l_sum * factor + (r0.x + r0.y);
       }
       // ------------------------------------------------------------ epilogue
-      ok = ok && mbar_wait(bar_pv_done + u, (ns - 1) & 1, abort_flag);
+      ok = warp_ok(ok && mbar_wait(bar_pv_done + u, (ns - 1) & 1, abort_flag));
       tc_fence_after();
       if constexpr (NH == 2) {  // (a negative sum: gave up after a timeout, and so does its partner at the barrier)
         const float theirs = exchange(ok ? l_sum : -1.f);
