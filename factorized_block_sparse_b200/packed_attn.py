@@ -7,8 +7,11 @@ Argument marshalling only: the computation runs in the CUDA kernels of
 at any stride that is a multiple of 8 elements, so slices of a fused
 projection are taken as they are); the sequences of the layout lie one
 behind another in the rows.  ``lse`` is float32 ``[Hq, T]``.  The stream is
-torch's current stream of the tensors' device unless one is given.  There is
-no CPU fallback: if the library is missing, loading this module raises.
+torch's current stream of the tensors' device unless one is given.  On a
+given stream the caller orders the work before and behind a call (the inputs
+are to be ready there, and results belong to it); tensors may be dropped as soon
+as the call has returned.  There is no CPU fallback: if the library is missing,
+loading this module raises.
 
 Use::
 
@@ -192,6 +195,8 @@ def packed_attn_fwd(q, k, v, o, lse, layout, stream=None, scale=None):
     """Writes ``o`` and ``lse`` in place (C ABI call); ``scale`` None is 1/sqrt(D)."""
     dims = _check_tensors(q, k, v, layout, (("o", o, q.shape),))
     _fwd(q, k, v, o, lse, _check_lse(lse, dims[1], dims[0], q), dims, layout, stream, scale)
+    if stream is not None:
+        sa._record(stream, q.device, q, k, v, o, lse)
 
 
 def packed_attn_bwd(q, k, v, o, lse, dO, dq, dk, dv, layout, ws, stream=None, scale=None):
@@ -199,6 +204,8 @@ def packed_attn_bwd(q, k, v, o, lse, dO, dq, dk, dv, layout, ws, stream=None, sc
     dims = _check_tensors(q, k, v, layout, (("o", o, q.shape), ("dO", dO, q.shape), ("dq", dq, q.shape),
                                             ("dk", dk, k.shape), ("dv", dv, k.shape)))
     _bwd(q, k, v, o, lse, _check_lse(lse, dims[1], dims[0], q), dO, dq, dk, dv, dims, layout, ws, stream, scale)
+    if stream is not None:
+        sa._record(stream, q.device, q, k, v, o, lse, dO, dq, dk, dv, ws)
 
 
 def packed_attn_status(stream=None):
@@ -235,7 +242,9 @@ def forward(q, k, v, layout, stream=None, scale=None):
     dims = _check_tensors(q, k, v, layout)
     if stream is not None:
         with _on_stream(stream, q.device):
-            return forward(q, k, v, layout, scale=scale)
+            out = forward(q, k, v, layout, scale=scale)
+        sa._record(stream, q.device, q, k, v)
+        return out
     T, Hq, rows = dims[0], dims[1], layout.rows
     o = _new(q, rows)
     lse = torch.empty(Hq, T, dtype=torch.float32, device=q.device)
@@ -252,7 +261,9 @@ def backward(q, k, v, o, lse, dO, layout, ws=None, stream=None, scale=None):
     ls = _check_lse(lse, Hq, T, q)
     if stream is not None:
         with _on_stream(stream, q.device):
-            return backward(q, k, v, o, lse, dO, layout, ws, scale=scale)
+            out = backward(q, k, v, o, lse, dO, layout, ws, scale=scale)
+        sa._record(stream, q.device, q, k, v, o, lse, dO, ws)
+        return out
     rows = layout.rows
     dq, dk, dv = _new(q, rows), _new(k, rows), _new(v, rows)
     if ws is None:

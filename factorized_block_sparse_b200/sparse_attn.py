@@ -176,6 +176,18 @@ def _stream_ptr(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _record(stream, device, *tensors):
+    """Tells torch's allocator that work on ``stream`` uses the tensors: memory that is dropped behind a call stays
+    theirs until the stream has passed it, whichever stream they were allocated on."""
+    import torch
+
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 

@@ -219,7 +219,10 @@ def layer_norm(x, g, b=None, eps=1e-5, stream=None):
     bp = None if b is None else _vector("b", b, C, dev)
     if not _here(dev, stream):
         with _on(dev, stream):
-            return layer_norm(x, g, b, eps)
+            out = layer_norm(x, g, b, eps)
+        if stream is not None:
+            sa._record(stream, dev, x, g, b)
+        return out
     y = torch.empty_like(x, memory_format=torch.contiguous_format)
     if x.dim() == 2:
         mean = torch.empty(M, dtype=torch.float32, device=dev)
@@ -249,7 +252,10 @@ def layer_norm_backward(x, g, dy, mean, rstd, bias=True, stream=None):
             raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(x.shape[:-1])} on {dev}")
     if not _here(dev, stream):
         with _on(dev, stream):
-            return layer_norm_backward(x, g, dy, mean, rstd, bias)
+            out = layer_norm_backward(x, g, dy, mean, rstd, bias)
+        if stream is not None:
+            sa._record(stream, dev, x, g, dy, mean, rstd)
+        return out
     dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     if M == 0:
         return dx, torch.zeros_like(g), torch.zeros_like(g) if bias else None
@@ -300,7 +306,10 @@ def _clip(grads, max_norm, out, stream):
                 raise ValueError("an output must be a contiguous tensor of its gradient's shape, type and device")
     if not _here(dev, stream):
         with _on(dev, stream):
-            return _clip(grads, max_norm, grads if in_place else outs, None)
+            norm = _clip(grads, max_norm, grads if in_place else outs, None)
+        if stream is not None:
+            sa._record(stream, dev, *grads, *(() if in_place or outs is None else outs))
+        return norm
     # host arrays of pointers, counts and types; the call has read them when it returns
     gp = array("Q", [t.data_ptr() for t in grads])
     op = None if outs is None else gp if in_place else array("Q", [t.data_ptr() for t in outs])
