@@ -255,6 +255,8 @@ def forward(q, k, v, layout, stream=None, scale=None):
     o = torch.empty_like(q)
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     sparse_attn_fwd(q, k, v, o, lse, layout, stream, scale)
+    if stream is not None:
+        _record(stream, q.device, q, k, v, o, lse)
     return o, lse
 
 
@@ -274,6 +276,8 @@ def backward(q, k, v, o, lse, dO, layout, ws=None, stream=None, scale=None):
         ws = workspace(B, H, N, D, layout, q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     sparse_attn_bwd(q, k, v, o, lse, dO, dq, dk, dv, layout, ws, stream, scale)
+    if stream is not None:
+        _record(stream, q.device, q, k, v, o, lse, dO, dq, dk, dv, ws)
     return dq, dk, dv
 
 

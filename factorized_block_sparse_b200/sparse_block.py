@@ -106,6 +106,8 @@ def forward(x, params, H, layout, ws=None, stream=None):
     ws = workspace(B, N, H, D, layout, x.device) if ws is None else ws
     y = torch.empty_like(x)
     sparse_block_fwd(x, params, y, H, layout, ws, stream)
+    if stream is not None:
+        sa._record(stream, x.device, x, *(params[n] for n in PARAMS), y, ws)
     return y
 
 
@@ -120,6 +122,8 @@ def backward(x, dy, params, H, layout, ws=None, stream=None, max_norm=None):
     dx = torch.empty_like(x)
     grads = {n: torch.empty(params[n].shape, dtype=torch.float32, device=x.device) for n in PARAMS}
     sparse_block_bwd(x, dy, params, dx, grads, H, layout, ws, stream)
+    if stream is not None:
+        sa._record(stream, x.device, x, dy, *(params[n] for n in PARAMS), dx, *grads.values(), ws)
     if max_norm is not None:
         return dx, grads, clip_grads(grads, max_norm, stream=stream)
     return dx, grads

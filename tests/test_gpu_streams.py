@@ -46,7 +46,28 @@ def calls():
         pa.packed_attn_bwd(*i, *outs, lay, pa.workspace(8, 8, 64, lay, i[0].device), stream=s)
         return outs
 
+    from factorized_block_sparse_b200 import sparse_attn as sa
+    from factorized_block_sparse_b200 import synth
+
+    strided = sa.Layout("strided", M, 64, 0, 64)
+
+    def dense(dev):
+        return [torch.randn(1, 8, M, 64, device=dev).to(torch.bfloat16) for _ in range(3)]
+
+    def dense_bwd(dev):
+        i = dense(dev)
+        o, lse = sa.forward(*i, strided)
+        return [*i, o, lse, torch.randn_like(o)]
+
+    def block(dev):
+        p = {n: t.to(dev) for n, t in synth.block_params(C).items()}
+        return [torch.randn(1, M, C, device=dev).to(torch.bfloat16) for _ in range(2)] + [p]
+
     return {
+        "sparse_attn.forward": (dense, lambda i, s: sa.forward(*i, strided, stream=s), (0, 1, 2)),
+        "sparse_attn.backward": (dense_bwd, lambda i, s: sa.backward(*i, strided, stream=s), (0, 1, 2, 3, 5)),
+        "block forward": (block, lambda i, s: sb.forward(i[0], i[2], 8, strided, stream=s), (0,)),
+        "block backward": (block, lambda i, s: sb.backward(*i, 8, strided, stream=s, max_norm=0.5), (0, 1)),
         "forward": (qkv, lambda i, s: pa.forward(*i, lay, stream=s), (0, 1, 2)),
         "backward": (attn, lambda i, s: pa.backward(*i, lay, stream=s), (0, 1, 2, 3, 4, 5)),
         "packed_attn_fwd": (qkv, low, (0, 1, 2)),
@@ -60,7 +81,8 @@ def calls():
 
 @pytest.mark.parametrize("as_handle", [False, True])
 @pytest.mark.parametrize("name", ["forward", "backward", "packed_attn_fwd", "packed_attn_bwd", "layer_norm",
-                                  "layer_norm_backward", "grad_norm", "clip_grads"])
+                                  "layer_norm_backward", "grad_norm", "clip_grads", "sparse_attn.forward",
+                                  "sparse_attn.backward", "block forward", "block backward"])
 def test_dropped_tensors_keep_their_memory(cuda_device, calls, name, as_handle):
     make, call, which = calls[name]
     side = torch.cuda.Stream(device=cuda_device)
