@@ -660,21 +660,27 @@ struct ClipTable {
   unsigned chunk;  // elements a block takes at a time, a multiple of 8
 };
 
-// The squares of a word summed in float32, or in float64 where one is too
-// large or too small for that (2^-40 .. 2^60 keeps them and their sum exact to
-// float32's rounding); zeros are the common small values.
+// The squares of a word: each half's summed in float32 by a tree, the halves
+// in float64; all in float64 where one is too large or too small for that
+// (2^-40 .. 2^60 keeps squares and sums inside float32); zeros are the common
+// small values.  A half's sum takes two roundings of 2^-24 whatever its values
+// (2-byte types: their squares are exact, two additions; float32: a square and
+// an addition), one in the norm, which with its own rounding is good to 2^-23.
+// A word summed in one float32 chain would lose up to 3.5 2^-24 of the norm.
 template <typename T>
 __device__ __forceinline__ double word_squares(const uint4& w) {
   constexpr int N = 16 / sizeof(T);
-  float f[N], big = 0.f;
+  float f[N], big = 0.f, pair[N / 2];
   unpack<T, N>(w, f);
-  float s = 0.f;
 #pragma unroll
-  for (int u = 0; u < N; ++u) {
-    s = fmaf(f[u], f[u], s);
-    big = fmaxf(big, fabsf(f[u]));
+  for (int u = 0; u < N; u += 2) {
+    pair[u / 2] = fmaf(f[u], f[u], f[u + 1] * f[u + 1]);
+    big = fmaxf(big, fmaxf(fabsf(f[u]), fabsf(f[u + 1])));
   }
-  if (big == 0.f || (big > 9.1e-13f && big < 1.1e18f)) return s;  // (a NaN beside numbers passes: s is NaN)
+  if (big == 0.f || (big > 9.1e-13f && big < 1.1e18f)) {  // (a NaN beside numbers passes: the sum is NaN)
+    if constexpr (N == 8) return static_cast<double>(pair[0] + pair[1]) + static_cast<double>(pair[2] + pair[3]);
+    else return static_cast<double>(pair[0]) + static_cast<double>(pair[1]);
+  }
   double d = 0.;
 #pragma unroll
   for (int u = 0; u < N; ++u) d += static_cast<double>(f[u]) * f[u];

@@ -173,9 +173,9 @@ size_t sparse_block_clip_workspace_size(void);
  * sb_dtype values, read before the call returns; outs null computes the norm
  * alone.  out_i may be grads_i (in place; nothing is written where c = 1);
  * other than that no output may overlap a gradient or another output.
- * norm: one float32 on the device.  The sum of squares does not overflow or
- * vanish in float32 and has a fixed order.  A norm that is not finite acts as
- * the formula says: c = 0 for inf, NaN for NaN.
+ * norm: one float32 on the device, good to 2^-23 of its value.  The sum of
+ * squares does not overflow or vanish in float32 and has a fixed order.  A
+ * norm that is not finite acts as the formula says: c = 0 for inf, NaN for NaN.
  * Errors: SA_ERR_INVALID_ARG (a null array, a null pointer with a count above
  * 0, a count above 2^40, n < 0, an unknown type, a pointer not aligned to its element, outputs
  * that overlap, max_norm negative or NaN), SA_ERR_WORKSPACE, SA_ERR_CUDA.
