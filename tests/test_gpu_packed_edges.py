@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import packed
-from test_gpu_packed import U, check, check_backward, check_forward, draw, f64, pa  # noqa: F401
+from test_gpu_packed import SUB, U, check, check_backward, check_forward, draw, f64, pa  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +130,46 @@ def test_fp16_factors_stay_in_their_sequence(cuda_device, pa, value):  # noqa: F
     z[399] = float("inf")
     late = pa.backward(*x[:3], o, lse, z, lay)
     assert torch.equal(late[0][:399], ref[0][:399])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_peaked_rows_backward(cuda_device, pa, d, dtype):  # noqa: F811
+    # Scores up to about +-100: masked keys far above the row's lse, P of a row on one key.  A score is a float32 sum of d
+    # products, off by at most a step of 2^-23 an addition of the sum of magnitudes, and P by that factor (and 1e-4 for
+    # the exponential); dP - delta as at the head of test_gpu_packed.py, 1e-5 of the largest term.
+    lengths = [300, 77, 500]
+    q, k, v, dO = (t.to(cuda_device) for t in draw(sum(lengths), 4, 2, d, dtype, q_scale=16.0))
+    lay = pa.Layout(lengths)
+    o, lse = pa.forward(q, k, v, lay)
+    grads = pa.backward(q, k, v, o, lse, dO, lay)
+    assert pa.packed_attn_status() == 0
+    x = [f64(t) for t in (q, k, v, o, lse, dO)]
+    *ref, m = packed.backward(*x, lengths)
+    qa, ka = np.abs(x[0]), np.repeat(np.abs(x[1]), 2, axis=1)
+    size = max(float((qa[:, h] @ ka[:, h].T).max()) for h in range(4)) * d ** -0.5
+    p_err = 2.0 ** -23 * d * size + 1e-4
+    vv = np.repeat(x[2], 2, axis=1)
+    term = max(float(np.abs(x[5][:, h] @ vv[:, h].T).max()) for h in range(4))
+    u, s = U[dtype], SUB[dtype]
+    for name, got, r, ds, p, n in (("dq", grads[0], ref[0], "dq_ds", "dq_p", "dq_n"), ("dk", grads[1], ref[1], "dk_ds", "dk_p", "dk_n")):
+        check(name, got, r, u * (m[ds] + np.abs(r)) + p_err * m[ds] + 1e-5 * term * m[p] + s * m[n] + s + 1e-30)
+    check("dv", grads[2], ref[2], u * (m["dv_p"] + np.abs(ref[2])) + p_err * m["dv_p"] + s * m["dv_n"] + s + 1e-30)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_causality_of_the_backward_pass(cuda_device, pa, d):  # noqa: F811
+    # From the same o, lse and dO: keys and values from row 256 on reach no gradient before row 256, and queries and
+    # upstream gradients before row 256 none from there on, whatever they hold.
+    q, k, v, dO = (t.to(cuda_device) for t in draw(400, 4, 2, d, torch.bfloat16))
+    lay = pa.Layout([400])
+    o, lse = pa.forward(q, k, v, lay)
+    want = pa.backward(q, k, v, o, lse, dO, lay)
+    k2, v2, q2, g2 = k.clone(), v.clone(), q.clone(), dO.clone()
+    k2[256:], v2[256:] = float("inf"), float("nan")
+    q2[:256], g2[:256] = float("nan"), float("inf")
+    late = pa.backward(q, k2, v2, o, lse, dO, lay)
+    early = pa.backward(q2, k, v, o, lse, g2, lay)
+    for name, a, b, c in zip(("dq", "dk", "dv"), want, late, early):
+        assert torch.equal(a[:256], b[:256]), name
+        assert torch.equal(a[256:], c[256:]), name
