@@ -215,11 +215,7 @@ def packed_attn_status(stream=None):
 # ------------------------------------------------------------ conveniences
 def _on_stream(stream, device):
     """A context of the stream that a call runs on, for its allocations and its launches."""
-    if isinstance(stream, int):
-        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device))
-    if stream.device != device:
-        raise ValueError(f"the stream is of {stream.device}, the tensors are on {device}")
-    return torch.cuda.stream(stream)
+    return torch.cuda.stream(sa._torch_stream(stream, device))
 
 
 def _new(like, rows):

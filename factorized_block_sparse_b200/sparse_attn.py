@@ -176,15 +176,25 @@ def _stream_ptr(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _torch_stream(stream, device):
+    """torch's object of a stream that is given as one, as a handle, or as an object with a handle."""
+    import torch
+
+    if getattr(stream, "device", device) != device:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on {device}")
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    # 1 is another name of the legacy default stream, whose handle torch knows as 0
+    return torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
+
+
 def _record(stream, device, *tensors):
     """Tells torch's allocator that work on ``stream`` uses the tensors: memory that is dropped behind a call stays
     theirs until the stream has passed it, whichever stream they were allocated on."""
-    import torch
-
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+    stream = _torch_stream(stream, device)
     for t in tensors:
-        if t is not None:
+        if t is not None and t.is_cuda:
             t.record_stream(stream)
 
 

@@ -191,14 +191,13 @@ def _on(device, stream):
     """A context of the device and the stream that a call runs on, for its allocations and its launch."""
     import contextlib
 
-    if stream is not None and not isinstance(stream, int) and stream.device != device:
-        raise ValueError(f"the stream is of {stream.device}, the tensors are on {device}")
+    if stream is not None:
+        stream = sa._torch_stream(stream, device)
     cm = contextlib.ExitStack()
     if device.index != torch.cuda.current_device():
         cm.enter_context(torch.cuda.device(device))
     if stream is not None:
-        cm.enter_context(torch.cuda.stream(
-            torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream))
+        cm.enter_context(torch.cuda.stream(stream))
     return cm
 
 

@@ -137,3 +137,44 @@ def test_a_stream_named_inside_its_capture(cuda_device):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(run(None), got))
+
+
+class _Handle:
+    """A stream of another library: nothing but its handle."""
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.mark.parametrize("of", [lambda s: _Handle(s.cuda_stream), lambda s: 1, lambda s: 2, lambda s: 0])
+def test_streams_that_are_not_torchs(cuda_device, of):
+    # an object with a handle; the legacy default stream by its other name, and the calling thread's default stream
+    from factorized_block_sparse_b200 import packed_attn as pa
+    from factorized_block_sparse_b200 import sparse_attn as sa
+    from factorized_block_sparse_b200 import sparse_block as sb
+
+    side = torch.cuda.Stream(device=cuda_device)
+    s = of(side)
+    lay, strided = pa.Layout([200, 56]), sa.Layout("strided", 256, 16, 0, 16)
+    q, k, v, dO = (torch.randn(256, 2, 64, device=cuda_device).to(torch.bfloat16) for _ in range(4))
+    o, lse = pa.forward(q, k, v, lay)
+    b = [t.transpose(0, 1).contiguous()[None] for t in (q, k, v, dO)]
+    bo, bl = sa.forward(*b[:3], strided)
+    want = sa.backward(*b[:3], bo, bl, b[3], strided)
+    o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+    torch.cuda.synchronize()
+    pa.packed_attn_fwd(q, k, v, o2, lse2, lay, stream=s)
+    bo2, bl2 = sa.forward(*b[:3], strided, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(bo, bo2) and torch.equal(bl, bl2)
+    got = sa.backward(*b[:3], bo, bl, b[3], strided, stream=s)
+    torch.cuda.synchronize()
+    grads = pa.backward(q, k, v, o, lse, dO, lay)
+    x, g = q.reshape(256, 128), torch.ones(128, device=cuda_device)
+    norm, total = sb.layer_norm(x, g), sb.grad_norm(grads)
+    torch.cuda.synchronize()
+    o3, lse3 = pa.forward(q, k, v, lay, stream=s)
+    mine = [o3, lse3, *pa.backward(q, k, v, o, lse, dO, lay, stream=s), *sb.layer_norm(x, g, stream=s), sb.grad_norm(grads, stream=s)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((o, lse, *grads, *norm, total), mine))
+    assert torch.equal(want[1], got[1]) and torch.equal(want[2], got[2])  # (dq adds up in any order)
