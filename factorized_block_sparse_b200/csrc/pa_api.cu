@@ -224,7 +224,9 @@ size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 // the parts' own cost shows), the longest of them is the pass's time.
 // Measured, in one piece and in parts: one sequence of 4096, 4 heads on one
 // K/V head of 64, 141 and 54 us; one of 2048, 8 on 8 of 64 (longest 16 steps, share
-// 7), 29 and (forced) 52 us.
+// 7), 29 and (forced) 52 us.  The parts' sums take the workspace of `parts`
+// float32 copies of dK and dV: more parts go with fewer tiles, at most 0.23 GB
+// at D = 128 (two parts, 850 key tiles on one K/V head, 40 of them one sequence).
 int bwd_split(int Hq, int Hkv, const pa_layout* L) {
   constexpr int kSms = 148;  // (a size rule: the workspace must not depend on the device)
   if (L->bwd.empty()) return 1;

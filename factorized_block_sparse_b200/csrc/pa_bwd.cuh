@@ -39,9 +39,10 @@
 // second issuing warp (no change), 64 columns a compute thread (dK/dV part 597
 // -> 679 us), dQ's steps in turn by two halves of the warps (1.04 -> 1.07 ms),
 // the exponentials of two groups after those of the other two (1.04 -> 1.07
-// ms).  Times: 2 x 12288 rows, 8 heads of 64, 1.02 ms; ten ragged sequences of
-// 16384 rows, 32 / 8 heads of 128, 1.43 ms; one of 32768, 16 / 2 heads of 128,
-// 12.0 ms.
+// ms).  Times of runs of milliseconds: 2 x 12288 rows, 8 heads of 64, 1.02 ms;
+// ten ragged sequences of 16384 rows, 32 / 8 heads of 128, 1.43 ms; one of
+// 32768, 16 / 2 heads of 128, 12.0 ms; 2 x 8192 rows, 8 / 4 heads of 32, 0.44.
+// In runs of seconds, under the power limit: 1.19, 1.66 and 12.7 ms.
 //
 // Roles of both parts: compute groups of four warps (thread = row of the tile,
 // kCols columns of the step each), four warps for the read-out of an item's

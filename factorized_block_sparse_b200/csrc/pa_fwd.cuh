@@ -25,7 +25,10 @@
 // for 2.1k of products with two units in turn; one sequence of 32768, 16 / 2
 // heads, 3.3 to 3.9 ms (1.1 to 1.3 PFLOP/s; the clock falls with the power).
 // D <= 64: the softmax (1024 cycles of exponentials a tile pair of 1430 in
-// all); 2 x 12288 rows, 8 heads, 0.38 ms (820 TFLOP/s).  An eighth or more of
+// all); 2 x 12288 rows, 8 heads of 64, 0.38 ms (820 TFLOP/s); 2 x 8192 rows,
+// 8 / 4 heads of 32, 0.18 ms.  These times and those below are of runs of
+// milliseconds; in runs of seconds, under the power limit, the same calls take
+// 0.41 ms (text), 0.49 (ten ragged sequences) and 3.6 (32768).  An eighth or more of
 // the exponentials on the FMA pipe did not help either and costs the row sums
 // their last bits.
 //

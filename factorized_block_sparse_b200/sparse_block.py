@@ -6,7 +6,9 @@ kernels for the layer norms, GELU and head layout, cuBLAS and cuBLASLt for
 the projections, ``libsparse_attn.so`` for the attention).  Tensors are
 ``torch.Tensor`` objects on a CUDA device: activations bf16 ``[B, N, C]``
 with ``C = H * D``, projection weights bf16 ``[in, out]``, layer-norm
-parameters and parameter gradients float32.  There is no CPU fallback.
+parameters and parameter gradients float32.  With ``stream=`` the caller orders
+the work before and behind a call; tensors may be dropped as soon as it has
+returned.  There is no CPU fallback.
 """
 
 import ctypes

@@ -78,8 +78,10 @@ void packed_attn_layout_free(pa_layout* layout);
 /* Rows of all sequences together (-1 for a null layout). */
 int64_t packed_attn_layout_rows(const pa_layout* layout);
 /* Copies the tables to the current device, which the first call on a device
- * does by itself; a call that is captured into a CUDA graph needs it done
- * before (it refuses with SA_ERR_INVALID_ARG otherwise). */
+ * does by itself: it allocates, and waits for the copy and for what is queued
+ * on the legacy default stream (packed_attn_layout_free waits for the device).
+ * A call that is captured into a CUDA graph needs it done before (it refuses
+ * with SA_ERR_INVALID_ARG otherwise). */
 int packed_attn_layout_upload(const pa_layout* layout, void* stream);
 
 /*
