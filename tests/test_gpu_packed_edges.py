@@ -173,3 +173,57 @@ def test_causality_of_the_backward_pass(cuda_device, pa, d):  # noqa: F811
     for name, a, b, c in zip(("dq", "dk", "dv"), want, late, early):
         assert torch.equal(a[:256], b[:256]), name
         assert torch.equal(a[256:], c[256:]), name
+
+
+@pytest.mark.parametrize("lengths", [[], [0, 0]])
+@pytest.mark.parametrize("T", [0, 5])
+def test_packings_without_rows(cuda_device, pa, lengths, T):  # noqa: F811
+    # nothing to do: rows behind the last sequence are zero, and a workspace is still given
+    lay = pa.Layout(lengths)
+    q, k, dO = (torch.full((T, h, 64), float("nan"), dtype=torch.bfloat16, device=cuda_device) for h in (4, 2, 4))
+    o, lse = pa.forward(q, k, k, lay)
+    assert o.shape == q.shape and lse.shape == (4, T) and not o.any() and not lse.any()
+    grads = pa.backward(q, k, k, o, lse, dO, lay)
+    assert [g.shape for g in grads] == [q.shape, k.shape, k.shape] and not any(g.any() for g in grads)
+    assert pa.workspace(4, 2, 64, lay, cuda_device).numel() > 0 and pa.packed_attn_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_one_row_one_head_and_values_for_keys(cuda_device, pa, d, dtype):  # noqa: F811
+    # strides of extents of 1 are not looked at, and one tensor may be k and v
+    lay = pa.Layout([1])
+    buf = torch.randn(1 + 3 * 1024, device=cuda_device).to(dtype)
+    q = buf[:d].as_strided((1, 1, d), (3, 5, 1))
+    k = buf[1024:1024 + d].as_strided((1, 1, d), (1, 7, 1))
+    dO = torch.randn(1, 1, d, device=cuda_device).to(dtype)
+    o, lse = pa.forward(q, k, k, lay)
+    check_forward(q, k, k, o, lse, [1])
+    check_backward(q, k, k, o, lse, dO, pa.backward(q, k, k, o, lse, dO, lay), [1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_two_graphs_of_one_workspace_in_turn(cuda_device, pa, dtype):  # noqa: F811
+    # replayed one behind the other they may share it; each replay starts from whatever the other left there
+    sets = [([700, 130], 8, 2, 64), ([2100], 2, 1, 64)]
+    lays = [pa.Layout(s[0]) for s in sets]
+    n = max(pa.workspace(*s[1:], lay, cuda_device).numel() for s, lay in zip(sets, lays))
+    ws = torch.full((n,), 255, dtype=torch.uint8, device=cuda_device)
+    x, want, graphs = [], [], []
+    for (lengths, hq, hkv, d), lay in zip(sets, lays):
+        t = [t.to(cuda_device) for t in draw(sum(lengths), hq, hkv, d, dtype)]
+        o, lse = pa.forward(*t[:3], lay)
+        x.append((t, o, lse))
+        want.append(pa.backward(*t[:3], o, lse, t[3], lay))
+    s = torch.cuda.Stream()
+    for (t, o, lse), lay in zip(x, lays):
+        g = torch.cuda.CUDAGraph()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(g, stream=s):
+            out = pa.backward(*t[:3], o, lse, t[3], lay, ws=ws)
+        graphs.append((g, out))
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        graphs[i][0].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want[i], graphs[i][1]))
+    assert pa.packed_attn_status() == 0
