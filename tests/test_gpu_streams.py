@@ -93,7 +93,7 @@ def test_dropped_tensors_keep_their_memory(cuda_device, calls, name, as_handle):
     inputs = make(cuda_device)
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(100_000_000)
+        torch.cuda._sleep(300_000_000)
     out = call(inputs, s)
     gone = {inputs[i].untyped_storage().data_ptr(): inputs[i].untyped_storage().nbytes() for i in which}
     del inputs
